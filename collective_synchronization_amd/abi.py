@@ -37,6 +37,11 @@ COLLECTIVE_IDS = {"allreduce": AR_ALLREDUCE, "allgather": AR_ALLGATHER,
 PROTO_IDS = {"ll": AR_LL, "ll128": AR_LL128, "sentinel": AR_SENTINEL,
              "barrier": AR_BARRIER}
 PROTO_NAMES = {v: k for k, v in PROTO_IDS.items()}
+AR_BF16, AR_F16, AR_F32, AR_E4M3_ROW, AR_E4M3_MX, AR_E2M1_MX = range(6)
+FORMATS = {"bf16": AR_BF16, "f16": AR_F16, "f32": AR_F32, "row8": AR_E4M3_ROW,
+           "mx8": AR_E4M3_MX, "mx4": AR_E2M1_MX}
+AR_NORM_MAX_HIDDEN = 65536
+AR_REDUCE_NORM_MAX_HIDDEN = 16384
 
 
 class ar_desc(ctypes.Structure):
@@ -62,6 +67,31 @@ class ar_sim_params(ctypes.Structure):
                 ("epoch", ar_epoch), ("timeout_ns", ctypes.c_uint64),
                 ("delay_ticks", ctypes.c_void_p), ("tile_order", ctypes.c_void_p),
                 ("trace", ctypes.c_void_p)]
+
+
+class ar_norm_params(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("hidden", ctypes.c_int64),
+                ("eps", ctypes.c_float), ("format", ctypes.c_int32),
+                ("gamma", ctypes.c_void_p), ("res_format", ctypes.c_int32),
+                ("y_format", ctypes.c_int32), ("residual", ctypes.c_void_p),
+                ("residual_stride", ctypes.c_int64), ("residual_out", ctypes.c_void_p),
+                ("residual_out_stride", ctypes.c_int64), ("y", ctypes.c_void_p),
+                ("y_stride", ctypes.c_int64), ("scales", ctypes.c_void_p),
+                ("scale_stride", ctypes.c_int64), ("reserved", ctypes.c_int32)]
+
+
+class ar_linear_params(ctypes.Structure):
+    _fields_ = [("nranks", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("rows", ctypes.c_int64), ("outputs", ctypes.c_int64),
+                ("inputs", ctypes.c_int64), ("x_format", ctypes.c_int32),
+                ("y_format", ctypes.c_int32), ("x", ctypes.c_void_p),
+                ("x_stride", ctypes.c_int64), ("x_rank_stride", ctypes.c_int64),
+                ("x_scales", ctypes.c_void_p), ("x_scale_stride", ctypes.c_int64),
+                ("x_scale_rank_stride", ctypes.c_int64), ("w", ctypes.c_void_p),
+                ("w_stride", ctypes.c_int64), ("w_rank_stride", ctypes.c_int64),
+                ("w_scales", ctypes.c_void_p), ("w_scale_stride", ctypes.c_int64),
+                ("w_scale_rank_stride", ctypes.c_int64), ("y", ctypes.c_void_p),
+                ("y_stride", ctypes.c_int64), ("y_rank_stride", ctypes.c_int64)]
 
 
 class ar_cost_entry(ctypes.Structure):
@@ -122,6 +152,14 @@ _SIGS = {
     "ar_scale_pack": ([ctypes.POINTER(ar_desc), _vp, _i64, _vp, _vp, ar_epoch, _vp],
                       ctypes.c_int),
     "ar_scale_rows": ([_i32, _i64, _vp, _i64, _vp, _vp, _i64, _vp], ctypes.c_int),
+    "ar_residual_norm": ([ctypes.POINTER(ar_norm_params), _vp, _i64, _vp], ctypes.c_int),
+    "ar_reduce_norm": ([ctypes.POINTER(ar_desc), _vp, ctypes.POINTER(ar_norm_params), ar_epoch,
+                        _vp, _u64, _i32, _vp], ctypes.c_int),
+    "ar_quantize_mx": ([_i64, _i64, _i32, _vp, _i64, _i32, _vp, _i64, _vp, _i64, _vp],
+                       ctypes.c_int),
+    "ar_dequantize_mx": ([_i64, _i64, _i32, _vp, _i64, _vp, _i64, _i32, _vp, _i64, _vp],
+                         ctypes.c_int),
+    "ar_mx4_linear": ([ctypes.POINTER(ar_linear_params), _vp], ctypes.c_int),
     "ar_sim_run": ([ctypes.POINTER(ar_sim_params), _vp], ctypes.c_int),
     "ar_sim_run_static": ([ctypes.POINTER(ar_sim_params), _vp, _vp], ctypes.c_int),
     "ar_sim_chain_run": ([ctypes.POINTER(ar_sim_params), _vp, _vp], ctypes.c_int),
@@ -322,6 +360,63 @@ def ar_scale_rows(nranks, count, inp, in_stride, scales, out, out_stride,
                   stream=None) -> None:
     _check(_lib.ar_scale_rows(nranks, count, _ptr(inp), in_stride, _ptr(scales), _ptr(out),
                               out_stride, _stream(stream)), "ar_scale_rows")
+
+
+def format_id(f) -> int:
+    return FORMATS[f] if isinstance(f, str) else int(f)
+
+
+def norm_params(rows, hidden, eps, fmt, gamma, res_fmt, residual, residual_stride,
+                residual_out, residual_out_stride, y_fmt, y, y_stride, scales=None,
+                scale_stride=0) -> ar_norm_params:
+    """The norm of ar_residual_norm and ar_reduce_norm: formats by name or id
+    (FORMATS); gamma, residual and residual_out may be None."""
+    return ar_norm_params(rows, hidden, eps, format_id(fmt), _ptr(gamma), format_id(res_fmt),
+                          format_id(y_fmt), _ptr(residual), residual_stride, _ptr(residual_out),
+                          residual_out_stride, _ptr(y), y_stride, _ptr(scales), scale_stride, 0)
+
+
+def ar_residual_norm(params: ar_norm_params, x, x_stride, stream=None) -> None:
+    _check(_lib.ar_residual_norm(ctypes.byref(params), _ptr(x), x_stride, _stream(stream)),
+           "ar_residual_norm")
+
+
+def ar_reduce_norm(desc, scratch, params: ar_norm_params, epoch, ctrl, timeout_ns: int = 0,
+                   flags: int = 0, stream=None) -> None:
+    _check(_lib.ar_reduce_norm(ctypes.byref(desc), _ptr(scratch), ctypes.byref(params), epoch,
+                               _ptr(ctrl), timeout_ns, flags, _stream(stream)),
+           "ar_reduce_norm")
+
+
+def ar_quantize_mx(rows, cols, in_fmt, inp, in_stride, out_fmt, codes, codes_stride, scales,
+                   scale_stride, stream=None) -> None:
+    _check(_lib.ar_quantize_mx(rows, cols, format_id(in_fmt), _ptr(inp), in_stride,
+                               format_id(out_fmt), _ptr(codes), codes_stride, _ptr(scales),
+                               scale_stride, _stream(stream)), "ar_quantize_mx")
+
+
+def ar_dequantize_mx(rows, cols, in_fmt, codes, codes_stride, scales, scale_stride, out_fmt,
+                     out, out_stride, stream=None) -> None:
+    _check(_lib.ar_dequantize_mx(rows, cols, format_id(in_fmt), _ptr(codes), codes_stride,
+                                 _ptr(scales), scale_stride, format_id(out_fmt), _ptr(out),
+                                 out_stride, _stream(stream)), "ar_dequantize_mx")
+
+
+def linear_params(nranks, rows, outputs, inputs, x_fmt, x, x_stride, x_rank_stride, x_scales,
+                  x_scale_stride, x_scale_rank_stride, w, w_stride, w_rank_stride, w_scales,
+                  w_scale_stride, w_scale_rank_stride, y_fmt, y, y_stride,
+                  y_rank_stride) -> ar_linear_params:
+    """One ar_mx4_linear: y_r [rows, outputs] = x_r [rows, inputs] times the
+    transpose of w_r [outputs, inputs] for every rank."""
+    return ar_linear_params(nranks, 0, rows, outputs, inputs, format_id(x_fmt), format_id(y_fmt),
+                            _ptr(x), x_stride, x_rank_stride, _ptr(x_scales), x_scale_stride,
+                            x_scale_rank_stride, _ptr(w), w_stride, w_rank_stride,
+                            _ptr(w_scales), w_scale_stride, w_scale_rank_stride, _ptr(y),
+                            y_stride, y_rank_stride)
+
+
+def ar_mx4_linear(params: ar_linear_params, stream=None) -> None:
+    _check(_lib.ar_mx4_linear(ctypes.byref(params), _stream(stream)), "ar_mx4_linear")
 
 
 def sim_params(desc, nops, inp, in_stride, out, out_stride, scratch, ctrl, epoch,

@@ -46,6 +46,31 @@ def rows_from_device(t: torch.Tensor, count: int, shape) -> np.ndarray:
     return t.cpu().numpy().view(np.uint16)[:, :count].reshape(tuple(shape) + (count,))
 
 
+class FormatRows:
+    """`rows` rows of `cols` elements in one of the library's row formats
+    (abi.FORMATS) on a device: `data` and, for the 8- and 4-bit formats,
+    `scales`, with the strides the C ABI takes (elements of the float formats,
+    bytes of the others; scale_stride 0 where there is one scale a row)."""
+
+    def __init__(self, rows: int, cols: int, fmt, device="cuda"):
+        self.fmt = abi.format_id(fmt)
+        self.rows, self.cols = rows, cols
+        self.scales, self.scale_stride = None, 0
+        blocks = max(1, round_up(cols, 32) // 32)
+        if self.fmt <= abi.AR_F32:
+            dtype = (torch.bfloat16, torch.float16, torch.float32)[self.fmt]
+            self.stride = row_stride(cols)
+        else:
+            dtype = torch.uint8
+            self.stride = 16 * blocks if self.fmt == abi.AR_E2M1_MX else 32 * blocks
+        self.data = torch.zeros((rows, self.stride), dtype=dtype, device=device)
+        if self.fmt == abi.AR_E4M3_ROW:
+            self.scales = torch.zeros((rows,), dtype=torch.float32, device=device)
+        elif self.fmt > abi.AR_E4M3_ROW:
+            self.scale_stride = round_up(blocks, 4)
+            self.scales = torch.zeros((rows, self.scale_stride), dtype=torch.uint8, device=device)
+
+
 class Workspace:
     """Receive buffers and control block for one descriptor on one device.
 
@@ -112,6 +137,12 @@ class Workspace:
         flags = abi.AR_FLAG_REARM if (rearm and self.desc.proto == abi.AR_SENTINEL) else 0
         abi.ar_reduce_validate(self.desc, self.scratch, out_dev, out_stride, self.epoch,
                                self.ctrl, timeout_ns, flags, stream)
+
+    def reduce_norm(self, params, timeout_ns=0, rearm=True, stream=None) -> None:
+        """reduce with the norm of abi.norm_params in place of its output."""
+        flags = abi.AR_FLAG_REARM if (rearm and self.desc.proto == abi.AR_SENTINEL) else 0
+        abi.ar_reduce_norm(self.desc, self.scratch, params, self.epoch, self.ctrl, timeout_ns,
+                           flags, stream)
 
     def gather(self, out_dev, out_stride, timeout_ns=0, rearm=True, stream=None) -> None:
         flags = abi.AR_FLAG_REARM if (rearm and self.desc.proto == abi.AR_SENTINEL) else 0

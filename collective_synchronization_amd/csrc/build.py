@@ -15,11 +15,13 @@ PKG = os.path.dirname(HERE)
 LIB = os.path.join(PKG, "libcsync_ar.so")
 SOURCES = [os.path.join(HERE, "ar_kernels.hip"), os.path.join(HERE, "ar_collectives.hip"),
            os.path.join(HERE, "ar_static.hip"), os.path.join(HERE, "ar_state.hip"),
-           os.path.join(HERE, "ar_linear.hip"),
+           os.path.join(HERE, "ar_linear.hip"), os.path.join(HERE, "ar_norm.hip"),
+           os.path.join(HERE, "ar_mx.hip"), os.path.join(HERE, "ar_mxlinear.hip"),
            os.path.join(HERE, "ar_select.cpp")]
 INCLUDE = os.path.join(os.path.dirname(PKG), "include")
 HEADERS = [os.path.join(INCLUDE, "ar_device.h"), os.path.join(INCLUDE, "ar_protocols.h"),
-           os.path.join(HERE, "ar_host.h"), os.path.join(INCLUDE, "ar.h"),
+           os.path.join(HERE, "ar_host.h"), os.path.join(HERE, "ar_rows.h"),
+           os.path.join(INCLUDE, "ar.h"),
            os.path.join(INCLUDE, "ar_dev.h")]
 ARCH = os.environ.get("AR_OFFLOAD_ARCH", "gfx950")
 

@@ -339,6 +339,149 @@ int ar_scale_pack(const ar_desc* d, const void* in, int64_t in_stride,
 int ar_scale_rows(int32_t nranks, int64_t count, const void* in, int64_t in_stride,
                   const float* scales, void* out, int64_t out_stride, void* stream);
 
+/* ------------------------------------------------------ layer operators --- */
+/*
+ * What a tensor-parallel layer computes between one all-reduce and the next:
+ * the residual addition and norm of the reduced rows (alone, or in the
+ * receive side of the all-reduce), rows to and from microscaled floats, and
+ * the row-parallel linear layer on 4-bit weights whose output rows are the
+ * next payload.  Forward only: nothing of this library is trained through.
+ *
+ * Row formats.  A row of `cols` elements takes
+ *   AR_BF16, AR_F16, AR_F32: cols values; strides count elements;
+ *   AR_E4M3_ROW: cols bytes of OCP e4m3 codes and one binary32 scale a row
+ *        (scales: float[rows], no stride);
+ *   AR_E4M3_MX: 32*ceil(cols/32) bytes of e4m3 codes and one e8m0 byte (the
+ *        scale 2^(code - 127); 0xFF: NaN) for each 32 elements;
+ *   AR_E2M1_MX: 16*ceil(cols/32) bytes of e2m1 codes, the even element in
+ *        the low half of its byte, and one e8m0 byte for each 32 elements.
+ * Strides of codes and of e8m0 scales count bytes.  Values are codes times
+ * their scale.  Alignment: rows 16 bytes, strides multiples of 8 elements or
+ * of 16 code bytes; scales 4 bytes, strides of e8m0 scales multiples of 4.
+ * Rows that are written: nothing past `cols` but the codes of the last block,
+ * which are zero there.  Rows that are read: up to the 16-byte boundary after
+ * their last byte; what lies past `cols` does not count.
+ *
+ * To 8 and 4 bits, everything rounds once, to nearest even, and saturates at
+ * the format's largest value (448 or 6):
+ *   AR_E4M3_ROW: s = max(max|v| / 448, 2^-126), code = e4m3(v * (1/s)); a row
+ *        with a NaN or an infinity has the scale NaN and codes 0x7F;
+ *   MX: e = floor(log2 max|v|) - 8 (e4m3) or - 2 (e2m1), at least -127, code =
+ *        round(v * 2^-e), scale code e + 127; a block with a NaN or an infinity
+ *        has the scale 0xFF and codes 0x7F (e4m3) or 0 (e2m1).
+ */
+typedef enum {
+    AR_BF16 = 0,
+    AR_F16 = 1,
+    AR_F32 = 2,
+    AR_E4M3_ROW = 3,
+    AR_E4M3_MX = 4,
+    AR_E2M1_MX = 5
+} ar_format;
+
+/* Longest row ar_residual_norm and ar_reduce_norm take. */
+#define AR_NORM_MAX_HIDDEN 65536
+#define AR_REDUCE_NORM_MAX_HIDDEN 16384
+
+typedef struct {
+    int64_t rows;               /* tokens, >= 0 */
+    int64_t hidden;             /* elements of a row, >= 0 */
+    float eps;                  /* >= 0, finite */
+    int32_t format;             /* of x and gamma: AR_BF16, AR_F16 or AR_F32 */
+    const void* gamma;          /* hidden elements; NULL: ones */
+    int32_t res_format;         /* of both residuals: `format` or AR_F32 */
+    int32_t y_format;           /* `format`, or one of the 8- and 4-bit ones */
+    const void* residual;       /* NULL: none is added */
+    int64_t residual_stride;
+    void* residual_out;         /* NULL: not written; may be `residual` */
+    int64_t residual_out_stride;
+    void* y;
+    int64_t y_stride;
+    void* scales;               /* 8- and 4-bit y only */
+    int64_t scale_stride;       /* MX only */
+    int32_t reserved;           /* must be 0 */
+} ar_norm_params;
+
+/*
+ * ar_residual_norm -- for every row
+ *     h = residual + x,  r = 1/sqrt(sum(h^2)/hidden + eps),  v = (h*r)*gamma
+ * in binary32; residual_out = h and y = v, each rounded once to its format.
+ * x: device, rows at x + i*x_stride elements.  y and residual_out may be x
+ * where formats and strides agree; other overlaps are not allowed.  The
+ * order of the sum is fixed by the shape, so equal calls give equal bits.
+ * rows or hidden 0: nothing is written.  AR_ESIZE: hidden above
+ * AR_NORM_MAX_HIDDEN, rows above 2^31 - 1.
+ */
+int ar_residual_norm(const ar_norm_params* p, const void* x, int64_t x_stride, void* stream);
+
+/*
+ * ar_reduce_norm -- ar_reduce_validate with ar_residual_norm in place of its
+ * output: after ar_pack_* of payloads of rows*hidden elements, every consumer
+ * c polls and validates its receive buffer, adds the ranks' rows in rank
+ * order in binary32 and goes on from that sum (which is not rounded) as
+ * ar_residual_norm does from x.  The sum itself is not written anywhere.
+ *   d: AR_ALLREDUCE, any protocol; d->count = rows*hidden.
+ *   p: format AR_BF16; hidden a multiple of 8 (AR_EALIGN) and at most
+ *      AR_REDUCE_NORM_MAX_HIDDEN (AR_ESIZE).  Every row buffer holds
+ *      nconsumers*rows rows, consumer c's from row c*rows on.  residual_out
+ *      may be residual.
+ *   scratch, e, ctrl, timeout_ns, flags and errors as for
+ *   ar_reduce_validate; a row any of whose blocks failed is not written.
+ */
+int ar_reduce_norm(const ar_desc* d, void* scratch, const ar_norm_params* p, ar_epoch e,
+                   void* ctrl, uint64_t timeout_ns, int32_t flags, void* stream);
+
+/*
+ * ar_quantize_mx -- rows of AR_BF16, AR_F16 or AR_F32 to AR_E4M3_MX or
+ * AR_E2M1_MX.  ar_dequantize_mx -- the values of such rows, rounded once to
+ * out_format (exact in AR_F32 and AR_BF16 but for results outside their
+ * range).  rows or cols 0: nothing is written.  AR_ESIZE: rows of more than
+ * 2^31 - 1 8-element chunks in all.
+ */
+int ar_quantize_mx(int64_t rows, int64_t cols, int32_t in_format, const void* in,
+                   int64_t in_stride, int32_t out_format, void* codes, int64_t codes_stride,
+                   void* scales, int64_t scale_stride, void* stream);
+int ar_dequantize_mx(int64_t rows, int64_t cols, int32_t in_format, const void* codes,
+                     int64_t codes_stride, const void* scales, int64_t scale_stride,
+                     int32_t out_format, void* out, int64_t out_stride, void* stream);
+
+typedef struct {
+    int32_t nranks;             /* simulated ranks, 1..AR_MAX_RANKS */
+    int32_t reserved;           /* must be 0 */
+    int64_t rows;               /* M: tokens, >= 0 */
+    int64_t outputs;            /* N, >= 0 */
+    int64_t inputs;             /* K: inputs of one rank's shard, >= 0 */
+    int32_t x_format;           /* AR_BF16, AR_E4M3_ROW, AR_E4M3_MX, AR_E2M1_MX */
+    int32_t y_format;           /* AR_BF16 or AR_F32 */
+    const void* x;              /* rank r's row m: x + r*x_rank_stride + m*x_stride */
+    int64_t x_stride, x_rank_stride;
+    const void* x_scales;       /* not for AR_BF16 */
+    int64_t x_scale_stride;     /* MX only (AR_E4M3_ROW: one float a row) */
+    int64_t x_scale_rank_stride;
+    const void* w;              /* AR_E2M1_MX: row n holds output n's weights */
+    int64_t w_stride, w_rank_stride;
+    const void* w_scales;
+    int64_t w_scale_stride, w_scale_rank_stride;
+    void* y;                    /* elements: y + r*y_rank_stride + m*y_stride + n */
+    int64_t y_stride, y_rank_stride;
+} ar_linear_params;
+
+/*
+ * ar_mx4_linear -- row-parallel linear layer shards on 4-bit weights: for
+ * every rank r, y_r[m][n] = sum over k of x_r[m][k] * w_r[n][k], products
+ * and sums in the matrix cores with binary32 accumulation, rounded once.  It
+ * is the producer of one all-reduce: with y_stride = outputs and
+ * y_rank_stride a row stride of ar_pack_*, rank r's y is its payload.
+ * Strides of x and w as for their formats; rank strides in the same units
+ * and with the same alignment, 0 where the ranks share a tensor.  x of all
+ * ranks may be slices of one row (x_rank_stride = inputs).  y: any stride
+ * that holds a row, aligned to its element; it may not overlap the inputs,
+ * nor the ranks' y each other.  A scale NaN makes its products NaN.  inputs 0:
+ * zeros are written; rows or outputs 0: nothing is.  AR_ESIZE: a size above
+ * 2^30.
+ */
+int ar_mx4_linear(const ar_linear_params* p, void* stream);
+
 /* ------------------------------------------------------------ simulator --- */
 /*
  * ar_sim_run -- `nops` back-to-back one-shot all-reduces in one persistent
