@@ -266,6 +266,280 @@ __global__ __launch_bounds__(kWave * WN * WK) void k_mx_linear_rows(MxLinArgs a)
   }
 }
 
+// ---------------------------------------------------------- many tokens ---
+//
+// Bound by the matrix cores.  A workgroup holds BN outputs by BM tokens; K
+// goes by in steps of 128 elements (64 for bf16 inputs), three steps' codes in
+// shared memory: while one is multiplied the next has arrived and the one
+// after is on its way, loaded straight into shared memory, and one barrier a
+// step is enough.  Rows lie there as they come, 16-byte pieces permuted by the
+// row so that the lanes that read at once meet different banks; the loads
+// apply the permutation to their addresses.  Scales come 512 elements at a
+// time, one row a thread.
+
+// 16 bytes a lane from the buffer straight into shared memory, at `lds` (the
+// wave's own address) + 16 * lane.
+__device__ __forceinline__ void load_to_lds(rsrc_t r, uint8_t* lds, uint32_t lane_off, uint32_t off) {
+  typedef __attribute__((address_space(3))) void lds_void;
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)lds, 16, lane_off, off, 0, 0);
+}
+
+template <int XF>
+struct TileShape {
+  static constexpr int BK = XF == AR_BF16 ? 64 : 128;      // elements of K a step
+  static constexpr int XB = XF == AR_E2M1_MX ? 64 : 128;   // bytes of an x row a step
+  static constexpr int WB = BK / 2;                        // bytes of a weight row
+  static constexpr int XC = XB / 16, WC = WB / 16;         // 16-byte pieces
+  static constexpr int steps_scales = 512 / BK;            // steps that share 16 scales a row
+};
+
+// Where piece `c` of row `r` lies among the row's C pieces: 8 rows that are
+// read together cover every 16-byte column of 128 bytes.
+template <int C>
+__device__ __forceinline__ int place(int r, int c) {
+  if constexpr (C == 8) return c ^ (r & 7);
+  else if constexpr (C == 4) return c ^ ((r >> 1) & 3);
+  else return c ^ ((r >> 2) & 1);
+}
+
+__device__ __forceinline__ void barrier_only() {
+  compiler_barrier();
+  __builtin_amdgcn_s_barrier();
+  compiler_barrier();
+}
+
+template <int XF_, int YF_, int BM_, int BN_, int WM_, int WN_>
+struct Tile {
+  static constexpr int XF = XF_, YF = YF_, BM = BM_, BN = BN_, WM = WM_, WN = WN_;
+  using T = TileShape<XF>;
+  static constexpr int waves = (BM / WM) * (BN / WN);
+  static constexpr int threads = waves * kWave;
+  static constexpr int xbytes = BM * T::XB, wbytes = BN * T::WB;
+  static constexpr int stage = xbytes + wbytes;
+  static constexpr int nx = xbytes / 16 / threads, nw = wbytes / 16 / threads;   // loads a thread
+  static constexpr int scales = (BM + BN) * 16;
+  static constexpr int lds = 3 * stage + 2 * scales;
+  static_assert(nx >= 1 && nw >= 1 && BM + BN == threads, "one row of scales a thread");
+};
+
+template <class G>
+__global__ __launch_bounds__(G::threads) void k_mx_linear_tiles(MxLinArgs a) {
+  using T = typename G::T;
+  constexpr int XF = G::XF, YF = G::YF, BM = G::BM, BN = G::BN, WM = G::WM, WN = G::WN;
+  constexpr int TI = WN / 16, TJ = WM / 16;                // matrix tiles of a wave
+  __shared__ __align__(256) uint8_t smem[G::lds];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int c = lane & 15, g = lane >> 4;
+  const int wi = wave % (BN / WN), wj = wave / (BN / WN);
+
+  // Workgroups go round the 8 XCDs one by one; each XCD takes a run of tiles
+  // that walks down strips of 8 tiles of outputs, so that the 32 tiles it
+  // holds at a time share few rows of either operand in its own L2.
+  const int total = gridDim.x;
+  int b = blockIdx.x;
+  {
+    const int per = total / 8, extra = total % 8, xcd = b % 8, k = b / 8;
+    b = xcd * per + min(xcd, extra) + k;
+  }
+  const int per_rank = a.n_groups * a.m_groups;
+  const int r = b / per_rank;
+  b -= r * per_rank;
+  constexpr int strip = 8;
+  const int s0 = b / (strip * a.m_groups) * strip;         // first output tile of the strip
+  const int width = min(strip, a.n_groups - s0);
+  b -= s0 * a.m_groups;
+  const int n0 = (s0 + b % width) * BN, m0 = b / width * BM;
+
+  const uint8_t* xbase = a.x + r * a.x_rank + m0 * a.x_stride;
+  const uint8_t* wbase = a.w + r * a.w_rank + n0 * a.w_stride;
+  const rsrc_t xr = make_rsrc(xbase, 0x7FFFFFFFu), wr = make_rsrc(wbase, 0x7FFFFFFFu);
+  const int mlast = a.M - 1 - m0, nlast = a.N - 1 - n0;    // rows past the end read the last one
+
+  // this thread's pieces of a step: source offsets at step 0
+  uint32_t xo[G::nx], wo[G::nw];
+#pragma unroll
+  for (int i = 0; i < G::nx; ++i) {
+    const int at = i * G::threads + tid, row = at / T::XC;
+    xo[i] = (uint32_t)min(row, mlast) * (uint32_t)a.x_stride + place<T::XC>(row, at % T::XC) * 16;
+  }
+#pragma unroll
+  for (int i = 0; i < G::nw; ++i) {
+    const int at = i * G::threads + tid, row = at / T::WC;
+    wo[i] = (uint32_t)min(row, nlast) * (uint32_t)a.w_stride + place<T::WC>(row, at % T::WC) * 16;
+  }
+  auto load_step = [&](int k, int buf) {
+    uint8_t* at = smem + buf * G::stage + wave * 1024;
+#pragma unroll
+    for (int i = 0; i < G::nx; ++i)
+      load_to_lds(xr, at + i * G::threads * 16, xo[i], (uint32_t)k * T::XB);
+#pragma unroll
+    for (int i = 0; i < G::nw; ++i)
+      load_to_lds(wr, at + G::xbytes + i * G::threads * 16, wo[i], (uint32_t)k * T::WB);
+  };
+  // a step that K ends in: zeros past it
+  auto load_tail = [&](int k, int buf) {
+    uint8_t* at = smem + buf * G::stage + tid * 16;
+#pragma unroll
+    for (int i = 0; i < G::nx; ++i) {
+      const int slot = i * G::threads + tid, row = slot / T::XC;
+      const int first = k * T::XB + place<T::XC>(row, slot % T::XC) * 16;       // byte of the row
+      const int end = XF == AR_BF16 ? 2 * a.K : (XF == AR_E4M3_ROW ? a.K : a.nb * (XF == AR_E2M1_MX ? 16 : 32));
+      u32x4 v = u32x4{0u, 0u, 0u, 0u};
+      if (first < end) v = keep_bytes(ldg16(xbase + xo[i] + k * T::XB), end - first);
+      *reinterpret_cast<u32x4*>(at + i * G::threads * 16) = v;
+    }
+#pragma unroll
+    for (int i = 0; i < G::nw; ++i) {
+      const int slot = i * G::threads + tid, row = slot / T::WC;
+      const int first = k * T::WB + place<T::WC>(row, slot % T::WC) * 16;
+      u32x4 v = u32x4{0u, 0u, 0u, 0u};
+      if (first < a.nb * 16) v = ldg16(wbase + wo[i] + k * T::WB);
+      *reinterpret_cast<u32x4*>(at + G::xbytes + i * G::threads * 16) = v;
+    }
+  };
+  // scales: thread t holds weight row t, or token t - BN
+  const bool mine_w = tid < BN;
+  const bool no_scale = !mine_w && !is_mx_format(XF);
+  const uint8_t* wsafe = a.ws + r * a.ws_rank + n0 * a.ws_stride;
+  const uint8_t* srow = mine_w ? a.ws + r * a.ws_rank + (n0 + min(tid, nlast)) * a.ws_stride
+                               : a.xs + r * a.xs_rank + (m0 + min(tid - BN, mlast)) * a.xs_stride;
+  // 16 scales from step k on, raw; the last dword again where the row has ended
+  const int slast = (a.nb - 1) & ~3;
+  auto load_scales = [&](int k) -> u32x4 {
+    const int blk = k * (T::BK / 32);
+    u32x4 v;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      v[q] = *reinterpret_cast<const uint32_t*>((no_scale ? wsafe : srow) + min(blk + 4 * q, slast));
+    return v;
+  };
+  // into shared memory, with 1 for every block past the end
+  auto put_scales = [&](int k, u32x4 v) {
+    const int left = a.nb - k * (T::BK / 32);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int n = no_scale ? 0 : left - 4 * q;
+      const uint32_t keep = n >= 4 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << (8 * n)) - 1u);
+      v[q] = (v[q] & keep) | (0x7F7F7F7Fu & ~keep);
+    }
+    *reinterpret_cast<u32x4*>(smem + 3 * G::stage + (k / T::steps_scales & 1) * G::scales + tid * 16) = v;
+  };
+
+  f32x4 acc[TI][TJ];
+#pragma unroll
+  for (int i = 0; i < TI; ++i)
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+  auto compute = [&](int k, int buf) {
+    const uint8_t* xs = smem + buf * G::stage;
+    const uint8_t* ws = xs + G::xbytes;
+    const int ss = k / T::steps_scales;
+    const uint8_t* sc = smem + 3 * G::stage + (ss & 1) * G::scales + (k % T::steps_scales) * (T::BK / 32);
+    if constexpr (XF == AR_BF16) {
+      // group g takes elements 16g .. 16g + 15, 8 in each of two instructions
+      u32x4 x[TJ][2];
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) {
+        const int row = wj * WM + j * 16 + c;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          x[j][h] = *reinterpret_cast<const u32x4*>(xs + row * T::XB + place<T::XC>(row, 2 * g + h) * 16);
+      }
+#pragma unroll
+      for (int i = 0; i < TI; ++i) {
+        const int row = wi * WN + i * 16 + c;
+        const u32x2 w = *reinterpret_cast<const u32x2*>(ws + row * T::WB + place<T::WC>(row, g >> 1) * 16 +
+                                                        (g & 1) * 8);
+        const float scale = __uint_as_float((uint32_t)sc[row * 16 + (g >> 1)] << 23);
+        const bf16x8 w0 = weights_bf16(w.x, scale), w1 = weights_bf16(w.y, scale);
+#pragma unroll
+        for (int j = 0; j < TJ; ++j) {
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w0, __builtin_bit_cast(bf16x8, x[j][0]),
+                                                              acc[i][j], 0, 0, 0);
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w1, __builtin_bit_cast(bf16x8, x[j][1]),
+                                                              acc[i][j], 0, 0, 0);
+        }
+      }
+    } else {
+      constexpr u32x4 none = u32x4{0u, 0u, 0u, 0u};
+      constexpr int xcode = XF == AR_E2M1_MX ? 4 : 0;
+      i32x8 x[TJ];
+      int xsc[TJ];
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) {
+        const int row = wj * WM + j * 16 + c;
+        if constexpr (XF == AR_E2M1_MX) {
+          x[j] = operand(*reinterpret_cast<const u32x4*>(xs + row * T::XB + place<T::XC>(row, g) * 16), none);
+        } else {
+          x[j] = operand(*reinterpret_cast<const u32x4*>(xs + row * T::XB + place<T::XC>(row, g) * 16),
+                         *reinterpret_cast<const u32x4*>(xs + row * T::XB + place<T::XC>(row, 4 + g) * 16));
+        }
+        xsc[j] = XF == AR_E4M3_ROW ? 127 : (int)sc[(BN + row) * 16 + g];
+      }
+#pragma unroll
+      for (int i = 0; i < TI; ++i) {
+        const int row = wi * WN + i * 16 + c;
+        const i32x8 w =
+            operand(*reinterpret_cast<const u32x4*>(ws + row * T::WB + place<T::WC>(row, g) * 16), none);
+        const int wsc = (int)sc[row * 16 + g];
+#pragma unroll
+        for (int j = 0; j < TJ; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x[j], acc[i][j], 4, xcode, 0, wsc,
+                                                                       0, xsc[j]);
+      }
+    }
+  };
+
+  // whole steps, then maybe one that K ends in
+  const int full = (is_mx_format(XF) ? a.nb * 32 : a.K) / T::BK;
+  const int steps = (a.nb * 32 + T::BK - 1) / T::BK;
+  if (full > 0) load_step(0, 0);
+  if (full > 1) load_step(1, 1);
+  if (steps > 0) put_scales(0, load_scales(0));
+  u32x4 next = u32x4{0u, 0u, 0u, 0u};
+  int buf = 0;
+  for (int k = 0; k < full; ++k) {
+    // step k has arrived when at most one step's loads are still on their way
+    // (the scales' loads, where there are some, only make the wait longer), and
+    // this wave's own scales are written
+    if (k + 1 < full) __builtin_amdgcn_s_waitcnt(0x0070 | (G::nx + G::nw));
+    else __builtin_amdgcn_s_waitcnt(0x0070);
+    barrier_only();
+    int into = buf + 2;
+    if (into >= 3) into -= 3;
+    if (k + 2 < full) load_step(k + 2, into);
+    const int ks = k % T::steps_scales;
+    if (ks == 0 && k + T::steps_scales < steps) next = load_scales(k + T::steps_scales);
+    compute(k, buf);
+    if (ks == T::steps_scales - 1 && k + 1 < steps) put_scales(k + 1, next);
+    if (++buf == 3) buf = 0;
+  }
+  if (steps > full) {
+    __syncthreads();
+    load_tail(full, buf);
+    __syncthreads();
+    compute(full, buf);
+  }
+#pragma unroll
+  for (int j = 0; j < TJ; ++j) {
+    const int m = m0 + wj * WM + j * 16 + c;
+    if (m >= a.M) continue;
+    float scale = 1.0f;
+    if constexpr (XF == AR_E4M3_ROW) {
+      if (a.K > 0) scale = *reinterpret_cast<const float*>(a.xs + r * a.xs_rank + m * a.xs_stride);
+    }
+#pragma unroll
+    for (int i = 0; i < TI; ++i) {
+      const int n = n0 + wi * WN + i * 16 + 4 * g;
+      f32x4 v = acc[i][j];
+      if constexpr (XF == AR_E4M3_ROW) v *= scale;
+      if (n < a.N) store_out4<YF>(a.y, r * a.y_rank + m * a.y_stride + n, n, a.N, a.vec != 0, v);
+    }
+  }
+}
+
 // ================================================================ host side
 
 static int check_linear(const ar_linear_params* p) {
@@ -319,8 +593,24 @@ static hipError_t launch_rows(const MxLinArgs& a0, int nranks, int mt_groups, hi
   return go(k_mx_linear_rows<XF, YF, MT, 4, 1>, 4, 4);
 }
 
+template <int XF, int YF, int BM, int BN, int WM, int WN>
+static hipError_t launch_tiles(const MxLinArgs& a0, int nranks, hipStream_t s) {
+  MxLinArgs a = a0;
+  a.n_groups = (a.N + BN - 1) / BN;
+  a.m_groups = (a.M + BM - 1) / BM;
+  using G = Tile<XF, YF, BM, BN, WM, WN>;
+  return launch(k_mx_linear_tiles<G>, dim3((unsigned)((int64_t)nranks * a.n_groups * a.m_groups)),
+                dim3(G::threads), s, a);
+}
+
 template <int XF, int YF>
 static hipError_t launch_linear(const MxLinArgs& a, int nranks, hipStream_t s) {
+  // the tile kernels' offsets inside a tile are 31 bits
+  if (a.M > 64 && a.x_stride < (1 << 23) && a.w_stride < (1 << 23)) {
+    const int64_t big = (int64_t)((a.N + 255) / 256) * ((a.M + 255) / 256) * nranks;
+    if (big >= 256) return launch_tiles<XF, YF, 256, 256, 64, 128>(a, nranks, s);
+    return launch_tiles<XF, YF, 128, 128, 64, 64>(a, nranks, s);
+  }
   if (a.M <= 16) return launch_rows<XF, YF, 1>(a, nranks, 1, s);
   if (a.M <= 32) return launch_rows<XF, YF, 2>(a, nranks, 1, s);
   return launch_rows<XF, YF, 4>(a, nranks, (a.M + 63) / 64, s);
