@@ -40,7 +40,7 @@ PROTO_NAMES = {v: k for k, v in PROTO_IDS.items()}
 AR_BF16, AR_F16, AR_F32, AR_E4M3_ROW, AR_E4M3_MX, AR_E2M1_MX = range(6)
 FORMATS = {"bf16": AR_BF16, "f16": AR_F16, "f32": AR_F32, "row8": AR_E4M3_ROW,
            "mx8": AR_E4M3_MX, "mx4": AR_E2M1_MX}
-AR_NORM_MAX_HIDDEN = 65536
+AR_NORM_MAX_HIDDEN = 32768
 AR_REDUCE_NORM_MAX_HIDDEN = 16384
 
 
@@ -216,8 +216,9 @@ def _ptr(x) -> Optional[int]:
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        # what torch.cuda.current_stream().cuda_stream gives, without the
+        # Stream object: 0.3 against 2.8 us of a call of 4 to 7 us
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

@@ -36,8 +36,9 @@ __global__ __launch_bounds__(kBlock) void k_quantize_mx(MxArgs a) {
   const uint32_t row = div_by(n, a.per_row);
   const int c = (int)(n - row * a.per_row.d);
   float v[8];
-  load8<F>(static_cast<const typename Elem<F>::type*>(a.in) + (int64_t)row * a.in_stride, a.cols,
-           (int64_t)c * 8, v);
+  values<F>(load_raw<F>(static_cast<const typename Elem<F>::type*>(a.in) + (int64_t)row * a.in_stride,
+                        a.cols, (int64_t)c * 8),
+            a.cols, (int64_t)c * 8, v);
   store8_mx<Q>(static_cast<uint8_t*>(a.codes) + (int64_t)row * a.codes_stride,
                a.scales + (int64_t)row * a.scale_stride, c, (int)a.per_row.d, v);
 }

@@ -24,7 +24,12 @@
 
 namespace ar {
 
-constexpr int kNormMaxThreads = 1024;
+// Threads a row at most: 16384 rows of 8192, bf16 to 8-bit blocks, take 164 us
+// (5.74 TB/s) with 512 threads and 2 chunks each, 179 with 1024 and 1, 173
+// with 256 and 4.
+constexpr int kNormThreads = 512;
+constexpr int kNormChunks = 8;       // chunks a thread at most
+static_assert(kNormThreads * kNormChunks * 8 == AR_NORM_MAX_HIDDEN, "the longest row");
 
 struct NormArgs {
   const void* x;
@@ -46,8 +51,36 @@ struct NormArgs {
 // The waves' partial sums or maxima; a second array so that the maximum's
 // writes need not wait for the sum's readers.
 struct NormShared {
-  float sum[kNormMaxThreads / kWave];
-  uint32_t max[kNormMaxThreads / kWave];
+  float sum[kNormThreads / kWave];
+  uint32_t max[kNormThreads / kWave];
+};
+
+__device__ __forceinline__ int64_t chunk_first(int i) {
+  return ((int64_t)i * blockDim.x + threadIdx.x) * 8;
+}
+
+// Gamma is loaded beside the rows, before the sum: one trip to memory for all
+// inputs, which is what bounds a single row.  Beyond two chunks a thread the
+// registers are better spent on more rows in flight; gamma then comes, from
+// the L2, when it is used.
+constexpr bool gamma_first(int ni) { return ni <= 2; }
+
+template <int FX, int NI>
+struct Gamma {
+  Raw<FX> raw[gamma_first(NI) ? NI : 1];
+  rsrc_t row;
+  __device__ __forceinline__ Gamma(const NormArgs& a) : row(raw_row(a.gamma, a.hidden, sizeof(typename Elem<FX>::type))) {
+    if constexpr (gamma_first(NI)) {
+#pragma unroll
+      for (int i = 0; i < NI; ++i) raw[i] = load_raw<FX>(row, chunk_first(i));
+    }
+  }
+  __device__ __forceinline__ void get(const NormArgs& a, int i, float (&g)[8]) const {
+    if constexpr (gamma_first(NI)) values<FX>(raw[i], a.hidden, chunk_first(i), g);
+    else values<FX>(load_raw<FX>(row, chunk_first(i)), a.hidden, chunk_first(i), g);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) g[k] = a.gamma ? g[k] : 1.0f;
+  }
 };
 
 // From the row's h in registers (chunk i of thread t: elements
@@ -56,7 +89,7 @@ struct NormShared {
 // elements in order, lanes by a butterfly, waves in order.
 template <int FX, int FR, int FY, int NI>
 __device__ __forceinline__ void norm_finish(const NormArgs& a, int64_t row, float (&h)[NI][8],
-                                            NormShared& sm) {
+                                            const Gamma<FX, NI>& gamma, NormShared& sm) {
   const int t = threadIdx.x, threads = blockDim.x;
   const int waves = threads >> 6, wave = t >> 6;
   const int chunks = (int)((a.hidden + 7) >> 3);
@@ -85,17 +118,11 @@ __device__ __forceinline__ void norm_finish(const NormArgs& a, int64_t row, floa
   }
   const float r = 1.0f / __builtin_sqrtf(s * a.inv_hidden + a.eps);
 
-  const typename Elem<FX>::type* gm = static_cast<const typename Elem<FX>::type*>(a.gamma);
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
     const int c = i * threads + t;
     float g[8];
-    if (gm && c < chunks) {
-      load8<FX>(gm, H, (int64_t)c * 8, g);
-    } else {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) g[k] = 1.0f;
-    }
+    gamma.get(a, i, g);
 #pragma unroll
     for (int k = 0; k < 8; ++k) h[i][k] = (h[i][k] * r) * g[k];
     // a row whose r is not finite makes NaN of the zeros past its end
@@ -152,27 +179,33 @@ __device__ __forceinline__ void norm_finish(const NormArgs& a, int64_t row, floa
 }
 
 template <int FX, int FR, int FY, int NI>
-__global__ __launch_bounds__(kNormMaxThreads) void k_residual_norm(NormArgs a) {
+__global__ __launch_bounds__(kNormThreads) void k_residual_norm(NormArgs a) {
   __shared__ NormShared sm;
   const int64_t row = blockIdx.x;
-  const int t = threadIdx.x, threads = blockDim.x;
   const int64_t H = a.hidden;
-  const auto* xr = static_cast<const typename Elem<FX>::type*>(a.x) + row * a.x_stride;
-  const auto* rr = a.res ? static_cast<const typename Elem<FR>::type*>(a.res) + row * a.res_stride
-                         : nullptr;
+  constexpr int sx = sizeof(typename Elem<FX>::type), sr = sizeof(typename Elem<FR>::type);
+  const rsrc_t xr = raw_row(static_cast<const uint8_t*>(a.x) + row * a.x_stride * sx, H, sx);
+  const rsrc_t rr =
+      raw_row(a.res ? static_cast<const uint8_t*>(a.res) + row * a.res_stride * sr : nullptr, H, sr);
+  const Gamma<FX, NI> gamma(a);
   float h[NI][8];
+  Raw<FX> xw[NI];
+  Raw<FR> rw[NI];
 #pragma unroll
-  for (int i = 0; i < NI; ++i) load8<FX>(xr, H, ((int64_t)i * threads + t) * 8, h[i]);
-  if (rr) {
-    float q[NI][8];
+  for (int i = 0; i < NI; ++i) xw[i] = load_raw<FX>(xr, chunk_first(i));
 #pragma unroll
-    for (int i = 0; i < NI; ++i) load8<FR>(rr, H, ((int64_t)i * threads + t) * 8, q[i]);
+  for (int i = 0; i < NI; ++i) rw[i] = load_raw<FR>(rr, chunk_first(i));
 #pragma unroll
-    for (int i = 0; i < NI; ++i)
+  for (int i = 0; i < NI; ++i) {
+    values<FX>(xw[i], H, chunk_first(i), h[i]);
+    if (a.res) {
+      float q[8];
+      values<FR>(rw[i], H, chunk_first(i), q);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) h[i][k] = q[i][k] + h[i][k];
+      for (int k = 0; k < 8; ++k) h[i][k] = q[k] + h[i][k];
+    }
   }
-  norm_finish<FX, FR, FY, NI>(a, row, h, sm);
+  norm_finish<FX, FR, FY, NI>(a, row, h, gamma, sm);
 }
 
 // ------------------------------------------------- in the receive side ---
@@ -189,57 +222,65 @@ struct ReduceNormArgs {
   int32_t res_format, y_format;
 };
 
-// 8 elements [e, e + 8) (e a multiple of 8) of one rank's payload, as packed
-// bf16 pairs, with the evidence that they have arrived.
+// 8 elements [e, e + 8) (e a multiple of 8) of one rank's payload as they lie
+// in its slot: 32 bytes of LL words, 16 of the others.
+template <int P> struct Raw8 { u32x4 a; };
+template <> struct Raw8<kLL> { u32x4 a, b; };
+
 template <int P>
-__device__ __forceinline__ void recv8(rsrc_t rs, uint32_t slot, uint32_t e, uint32_t seq,
-                                      uint32_t stale, uint32_t (&w)[4], bool& ok, bool& bad) {
+__device__ __forceinline__ Raw8<P> recv8(rsrc_t rs, uint32_t slot, uint32_t e) {
   if constexpr (P == kLL) {
-    const u32x4 a = ld16(rs, slot + e * 4u);
-    const u32x4 b = ld16(rs, slot + e * 4u + 16u);
-    bool o1, b1, o2, b2;
-    classify<P>(a, seq, stale, o1, b1);
-    classify<P>(b, seq, stale, o2, b2);
-    ok = o1 && o2;
-    bad = b1 || b2;
-    w[0] = a.x; w[1] = a.z; w[2] = b.x; w[3] = b.z;
+    return {ld16(rs, slot + e * 4u), ld16(rs, slot + e * 4u + 16u)};
   } else if constexpr (P == kLL128) {
     // the two halves of the chunk lie in one line each (60 = 15 * 4), maybe
     // in different ones; their flags have been seen before this load
     const uint32_t l0 = e / 60u, l1 = (e + 4u) / 60u;
     const u32x2 a = ld8(rs, slot + l0 * 128u + (e - 60u * l0) * 2u);
     const u32x2 b = ld8(rs, slot + l1 * 128u + (e + 4u - 60u * l1) * 2u);
-    ok = true;
-    bad = false;
-    w[0] = a.x; w[1] = a.y; w[2] = b.x; w[3] = b.y;
+    return {u32x4{a.x, a.y, b.x, b.y}};
   } else {
-    const u32x4 a = ld16(rs, slot + e * 2u);
-    classify<P>(a, seq, stale, ok, bad);
-    w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+    return {ld16(rs, slot + e * 2u)};
   }
 }
 
-// The residual and the norm of a reduced row.  The formats are chosen at run
-// time here: one kernel for each protocol and shape instead of eight.
+// Evidence that the chunk has arrived (LL128: the flags', elsewhere).
+template <int P>
+__device__ __forceinline__ void check8(const Raw8<P>& v, uint32_t seq, uint32_t stale, bool& ok, bool& bad) {
+  if constexpr (P == kLL) {
+    bool o, b;
+    classify<P>(v.a, seq, stale, o, b);
+    ok = ok && o;
+    bad = bad || b;
+    classify<P>(v.b, seq, stale, o, b);
+    ok = ok && o;
+    bad = bad || b;
+  } else if constexpr (P != kLL128) {
+    bool o, b;
+    classify<P>(v.a, seq, stale, o, b);
+    ok = ok && o;
+    bad = bad || b;
+  }
+}
+
+template <int P>
+__device__ __forceinline__ void words8(const Raw8<P>& v, uint32_t (&w)[4]) {
+  if constexpr (P == kLL) {
+    w[0] = v.a.x; w[1] = v.a.z; w[2] = v.b.x; w[3] = v.b.z;
+  } else {
+    w[0] = v.a.x; w[1] = v.a.y; w[2] = v.a.z; w[3] = v.a.w;
+  }
+}
+
+// The norm of a reduced row.  The formats are chosen at run time here: one
+// kernel for each protocol and shape instead of eight.
 template <int FR, int NI>
 __device__ __forceinline__ void reduce_finish(const ReduceNormArgs& a, int64_t row, float (&h)[NI][8],
-                                              NormShared& sm) {
-  const int t = threadIdx.x, threads = blockDim.x;
-  if (a.n.res) {
-    const auto* rr = static_cast<const typename Elem<FR>::type*>(a.n.res) + row * a.n.res_stride;
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      float q[8];
-      load8<FR>(rr, a.n.hidden, ((int64_t)i * threads + t) * 8, q);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) h[i][k] = q[k] + h[i][k];
-    }
-  }
+                                              const Gamma<AR_BF16, NI>& gamma, NormShared& sm) {
   switch (a.y_format) {
-    case AR_E4M3_ROW: norm_finish<AR_BF16, FR, AR_E4M3_ROW, NI>(a.n, row, h, sm); break;
-    case AR_E4M3_MX: norm_finish<AR_BF16, FR, AR_E4M3_MX, NI>(a.n, row, h, sm); break;
-    case AR_E2M1_MX: norm_finish<AR_BF16, FR, AR_E2M1_MX, NI>(a.n, row, h, sm); break;
-    default: norm_finish<AR_BF16, FR, AR_BF16, NI>(a.n, row, h, sm); break;
+    case AR_E4M3_ROW: norm_finish<AR_BF16, FR, AR_E4M3_ROW, NI>(a.n, row, h, gamma, sm); break;
+    case AR_E4M3_MX: norm_finish<AR_BF16, FR, AR_E4M3_MX, NI>(a.n, row, h, gamma, sm); break;
+    case AR_E2M1_MX: norm_finish<AR_BF16, FR, AR_E2M1_MX, NI>(a.n, row, h, gamma, sm); break;
+    default: norm_finish<AR_BF16, FR, AR_BF16, NI>(a.n, row, h, gamma, sm); break;
   }
 }
 
@@ -248,9 +289,9 @@ __device__ __forceinline__ void reduce_finish(const ReduceNormArgs& a, int64_t r
 // blocks arrive), adds them in rank order in binary32 and goes on with the
 // norm; the sum is never rounded or written.
 template <int P, int NMAX, int NI>
-__global__ __launch_bounds__(NMAX == 16 ? 512 : kNormMaxThreads) void k_reduce_norm(ReduceNormArgs a) {
+__global__ __launch_bounds__(kNormThreads) void k_reduce_norm(ReduceNormArgs a) {
   __shared__ NormShared sm;
-  __shared__ int err;
+  __shared__ int status[kNormThreads / kWave];
   const int t = threadIdx.x, threads = blockDim.x, lane = t & 63;
   const int c = blockIdx.x / a.rows;                       // consumer
   const int row = blockIdx.x - c * a.rows;
@@ -258,8 +299,20 @@ __global__ __launch_bounds__(NMAX == 16 ? 512 : kNormMaxThreads) void k_reduce_n
   const rsrc_t rs = make_rsrc(a.scratch, a.scratch_bytes);
   const uint32_t src0 = ((uint32_t)c * 2u + a.parity) * (uint32_t)a.nranks * a.slot_bytes;
   const uint32_t stale = seq_prev(seq_prev(a.seq));
-  if (t == 0) err = 0;
-  __syncthreads();
+  // gamma and the residual need no waiting: on their way before the polls
+  const int64_t orow = (int64_t)c * a.rows + row;
+  const Gamma<AR_BF16, NI> gamma(a.n);
+  const bool res32 = a.res_format == AR_F32;
+  const int sr = res32 ? 4 : 2;
+  const rsrc_t rr = raw_row(
+      a.n.res ? static_cast<const uint8_t*>(a.n.res) + orow * a.n.res_stride * sr : nullptr, H, sr);
+  Raw<AR_F32> rw[NI];                                      // a bf16 residual takes the first half
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    const uint32_t off = (uint32_t)chunk_first(i) * (uint32_t)sr;
+    rw[i].a = __builtin_amdgcn_raw_buffer_load_b128(rr, off, 0, 0);
+    rw[i].b = __builtin_amdgcn_raw_buffer_load_b128(rr, res32 ? off + 16u : 0xFFFFFFF0u, 0, 0);
+  }
   float h[NI][8];
   int st = 0;
 #pragma unroll
@@ -267,7 +320,7 @@ __global__ __launch_bounds__(NMAX == 16 ? 512 : kNormMaxThreads) void k_reduce_n
     const int64_t first = ((int64_t)i * threads + t) * 8;
     const bool active = first < H;
     const uint32_t e = (uint32_t)row * (uint32_t)H + (uint32_t)first;
-    uint32_t w[NMAX][4];
+    Raw8<P> raw[NMAX];
     Waiter wt(a.timeout_ticks, a.ctrl);
     if (P == kLL128 && st == 0) {
       // the line flags first, the data only after they have been seen
@@ -275,17 +328,24 @@ __global__ __launch_bounds__(NMAX == 16 ? 512 : kNormMaxThreads) void k_reduce_n
         bool ok = true, bad = false;
         if (active) {
           const uint32_t l0 = e / 60u, l1 = (e + 4u) / 60u;
+          u32x2 f[NMAX][2];
 #pragma unroll
-          for (int r = 0; r < NMAX; ++r) {
-            if (r >= a.nranks) continue;
-            const uint32_t slot = src0 + (uint32_t)r * a.slot_bytes;
-            const u32x2 f = ld8(rs, slot + l0 * 128u + 120u);
-            const u32x2 g = ld8(rs, slot + l1 * 128u + 120u);
-            const bool o1 = f.x == a.seq && f.y == 0u, o2 = g.x == a.seq && g.y == 0u;
-            ok = ok && o1 && o2;
-            bad = bad || (!o1 && !(f.y == 0u && (f.x == 0u || f.x == stale))) ||
-                  (!o2 && !(g.y == 0u && (g.x == 0u || g.x == stale)));
-          }
+          for (int r = 0; r < NMAX; ++r)
+            if (r < a.nranks) {
+              const uint32_t slot = src0 + (uint32_t)r * a.slot_bytes;
+              f[r][0] = ld8(rs, slot + l0 * 128u + 120u);
+              f[r][1] = ld8(rs, slot + l1 * 128u + 120u);
+            }
+#pragma unroll
+          for (int r = 0; r < NMAX; ++r)
+            if (r < a.nranks)
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const u32x2 v = f[r][k];
+                const bool o = v.x == a.seq && v.y == 0u;
+                ok = ok && o;
+                bad = bad || (!o && !(v.y == 0u && (v.x == 0u || v.x == stale)));
+              }
         }
         if (__ballot(bad) != 0ull) {
           if (lane == 0) report_error(a.ctrl, kEcorrupt);
@@ -303,14 +363,13 @@ __global__ __launch_bounds__(NMAX == 16 ? 512 : kNormMaxThreads) void k_reduce_n
     while (st == 0) {
       bool ok = true, bad = false;
       if (active) {
+        // every rank's loads first, then the checks: one trip for all
 #pragma unroll
-        for (int r = 0; r < NMAX; ++r) {
-          if (r >= a.nranks) continue;
-          bool o, b;
-          recv8<P>(rs, src0 + (uint32_t)r * a.slot_bytes, e, a.seq, stale, w[r], o, b);
-          ok = ok && o;
-          bad = bad || b;
-        }
+        for (int r = 0; r < NMAX; ++r)
+          if (r < a.nranks) raw[r] = recv8<P>(rs, src0 + (uint32_t)r * a.slot_bytes, e);
+#pragma unroll
+        for (int r = 0; r < NMAX; ++r)
+          if (r < a.nranks) check8<P>(raw[r], a.seq, stale, ok, bad);
       }
       if (__ballot(bad) != 0ull) {
         if (lane == 0) report_error(a.ctrl, kEcorrupt);
@@ -336,21 +395,33 @@ __global__ __launch_bounds__(NMAX == 16 ? 512 : kNormMaxThreads) void k_reduce_n
 #pragma unroll
       for (int r = 0; r < NMAX; ++r) {
         if (r >= a.nranks) continue;
+        uint32_t w[4];
+        words8<P>(raw[r], w);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           // rank 0 starts the sum: an addition to zero would lose a -0
-          h[i][2 * k] = r == 0 ? bf_lo(w[r][k]) : h[i][2 * k] + bf_lo(w[r][k]);
-          h[i][2 * k + 1] = r == 0 ? bf_hi(w[r][k]) : h[i][2 * k + 1] + bf_hi(w[r][k]);
+          h[i][2 * k] = r == 0 ? bf_lo(w[k]) : h[i][2 * k] + bf_lo(w[k]);
+          h[i][2 * k + 1] = r == 0 ? bf_hi(w[k]) : h[i][2 * k + 1] + bf_hi(w[k]);
         }
       }
     }
   }
-  if (st != 0 && lane == 0) err = 1;
+  if (lane == 0) status[t >> 6] = st;
   __syncthreads();
-  if (err) return;                                         // whole workgroup
-  const int64_t orow = (int64_t)c * a.rows + row;
-  if (a.res_format == AR_F32) reduce_finish<AR_F32, NI>(a, orow, h, sm);
-  else reduce_finish<AR_BF16, NI>(a, orow, h, sm);
+  for (int w = 0; w < threads >> 6; ++w) st |= status[w];
+  if (st != 0) return;                                     // whole workgroup
+  if (a.n.res) {
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      float q[8];
+      if (res32) values<AR_F32>(rw[i], H, chunk_first(i), q);
+      else values<AR_BF16>(Raw<AR_BF16>{rw[i].a}, H, chunk_first(i), q);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) h[i][k] = q[k] + h[i][k];
+    }
+  }
+  if (res32) reduce_finish<AR_F32, NI>(a, orow, h, gamma, sm);
+  else reduce_finish<AR_BF16, NI>(a, orow, h, gamma, sm);
 }
 
 // ================================================================ host side
@@ -360,10 +431,10 @@ struct NormShape {
   int threads, ni;
 };
 
-static NormShape norm_shape(int64_t hidden, int max_threads) {
+static NormShape norm_shape(int64_t hidden) {
   const int64_t chunks = (hidden + 31) / 32 * 4;
   int ni = 1;
-  while (ni < 8 && chunks > (int64_t)ni * max_threads) ni <<= 1;
+  while (chunks > (int64_t)ni * kNormThreads) ni <<= 1;
   int64_t threads = (ceil_div64(chunks, ni) + 63) / 64 * 64;
   return {(int)threads, ni};
 }
@@ -461,7 +532,7 @@ int ar_residual_norm(const ar_norm_params* p, const void* x, int64_t x_stride, v
   NormArgs a = norm_args(p);
   a.x = x;
   a.x_stride = x_stride;
-  const NormShape g = norm_shape(p->hidden, kNormMaxThreads);
+  const NormShape g = norm_shape(p->hidden);
   hipStream_t s = static_cast<hipStream_t>(stream);
   hipError_t e;
   if (p->format == AR_F32) {
@@ -512,7 +583,7 @@ int ar_reduce_norm(const ar_desc* d, void* scratch, const ar_norm_params* p, ar_
   a.rearm = (flags & AR_FLAG_REARM) && d->proto == kSentinel;
   a.res_format = p->res_format;
   a.y_format = p->y_format;
-  const NormShape g = norm_shape(p->hidden, d->nranks > 8 ? 512 : kNormMaxThreads);
+  const NormShape g = norm_shape(p->hidden);
   const unsigned blocks = (unsigned)(p->rows * d->nconsumers);
   hipStream_t s = static_cast<hipStream_t>(stream);
   hipError_t err;

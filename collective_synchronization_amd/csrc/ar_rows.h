@@ -21,19 +21,13 @@ __host__ __device__ constexpr bool is_mx_format(int f) { return f == AR_E4M3_MX 
 
 // ------------------------------------------------------------- chunks ---
 // A chunk is 8 elements of one row, 16-byte aligned in a 16-bit row.  Rows
-// are read and written below `count` only; a chunk that ends past it goes
-// element by element.
+// are written below `count` only; a chunk that ends past it goes element by
+// element.
 
 template <int F> struct Elem;
 template <> struct Elem<AR_BF16> { typedef uint16_t type; };
 template <> struct Elem<AR_F16> { typedef _Float16 type; };
 template <> struct Elem<AR_F32> { typedef float type; };
-
-template <int F>
-__device__ __forceinline__ float elem_to_f32(typename Elem<F>::type v) {
-  if constexpr (F == AR_BF16) return __uint_as_float((uint32_t)v << 16);
-  else return (float)v;
-}
 
 template <int F>
 __device__ __forceinline__ typename Elem<F>::type elem_from_f32(float v) {
@@ -45,29 +39,61 @@ __device__ __forceinline__ typename Elem<F>::type elem_from_f32(float v) {
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
-// Elements [first, first + 8) of a row; zeros at and past count.
+// A chunk as it lies in memory.  Loading and converting are apart so that a
+// thread can have all its loads under way before it waits for the first.
+template <int F> struct Raw { u32x4 a; };
+template <> struct Raw<AR_F32> { u32x4 a, b; };
+
+// Elements [first, first + 8) of a row, up to the 16-byte boundary after
+// element count - 1; zeros past that.
 template <int F>
-__device__ __forceinline__ void load8(const typename Elem<F>::type* __restrict__ row,
-                                      int64_t count, int64_t first, float (&v)[8]) {
-  if (first + 8 <= count) {
+__device__ __forceinline__ Raw<F> load_raw(const void* row, int64_t count, int64_t first) {
+  Raw<F> r{};
+  const auto* p = static_cast<const typename Elem<F>::type*>(row) + first;
+  if (first < count) r.a = *reinterpret_cast<const u32x4*>(p);
+  if constexpr (F == AR_F32) {
+    if (first + 4 < count) r.b = *reinterpret_cast<const u32x4*>(p + 4);
+  }
+  return r;
+}
+
+// The same through a buffer resource whose range is the row up to that
+// boundary (raw_row below): no branch, so nothing waits on its way.
+template <int F>
+__device__ __forceinline__ Raw<F> load_raw(rsrc_t row, int64_t first) {
+  Raw<F> r;
+  const uint32_t off = (uint32_t)first * (F == AR_F32 ? 4u : 2u);
+  r.a = __builtin_amdgcn_raw_buffer_load_b128(row, off, 0, 0);
+  if constexpr (F == AR_F32) r.b = __builtin_amdgcn_raw_buffer_load_b128(row, off + 16u, 0, 0);
+  return r;
+}
+// `row` the same for all lanes; null: an empty range, which reads as zeros.
+__device__ __forceinline__ rsrc_t raw_row(const void* row, int64_t count, int size) {
+  return make_rsrc(row, row ? (uint32_t)((count * size + 15) & ~int64_t(15)) : 0u);
+}
+
+// The chunk's values; zeros at and past count.
+template <int F>
+__device__ __forceinline__ void values(const Raw<F>& r, int64_t count, int64_t first, float (&v)[8]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
     if constexpr (F == AR_BF16) {
-      const u32x4 d = *reinterpret_cast<const u32x4*>(row + first);
-      v[0] = bf_lo(d.x); v[1] = bf_hi(d.x); v[2] = bf_lo(d.y); v[3] = bf_hi(d.y);
-      v[4] = bf_lo(d.z); v[5] = bf_hi(d.z); v[6] = bf_lo(d.w); v[7] = bf_hi(d.w);
+      v[2 * k] = bf_lo(r.a[k]);
+      v[2 * k + 1] = bf_hi(r.a[k]);
     } else if constexpr (F == AR_F16) {
-      const f16x8 d = *reinterpret_cast<const f16x8*>(row + first);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = (float)d[k];
+      typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+      const uint32_t d = r.a[k];
+      const f16x2 h = __builtin_bit_cast(f16x2, d);
+      v[2 * k] = (float)h.x;
+      v[2 * k + 1] = (float)h.y;
     } else {
-      const f32x4 a = *reinterpret_cast<const f32x4*>(row + first);
-      const f32x4 b = *reinterpret_cast<const f32x4*>(row + first + 4);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) { v[k] = a[k]; v[4 + k] = b[k]; }
+      v[k] = __uint_as_float(r.a[k]);
+      v[4 + k] = __uint_as_float(r.b[k]);
     }
-  } else {
+  }
+  if (first + 8 > count) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      v[k] = first + k < count ? elem_to_f32<F>(row[first + k]) : 0.0f;
+    for (int k = 0; k < 8; ++k) v[k] = first + k < count ? v[k] : 0.0f;
   }
 }
 

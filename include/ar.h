@@ -380,7 +380,7 @@ typedef enum {
 } ar_format;
 
 /* Longest row ar_residual_norm and ar_reduce_norm take. */
-#define AR_NORM_MAX_HIDDEN 65536
+#define AR_NORM_MAX_HIDDEN 32768
 #define AR_REDUCE_NORM_MAX_HIDDEN 16384
 
 typedef struct {

@@ -41,7 +41,7 @@ BAD_NORM = [
     (dict(y_stride=68), -2), (dict(residual_stride=65), -2),
     (dict(y_fmt="mx8", scales=A, scale_stride=6), -2), (dict(y_fmt="mx8", scales=A + 2, scale_stride=4), -2),
     (dict(y_fmt="row8", scales=A + 2), -2), (dict(y_fmt="row8", scales=A, y_stride=72), -2),
-    (dict(hidden=65537, y_stride=1 << 17, residual_stride=1 << 17, residual_out_stride=1 << 17), -3),
+    (dict(hidden=32769, y_stride=1 << 17, residual_stride=1 << 17, residual_out_stride=1 << 17), -3),
     (dict(rows=1 << 31), -3), (dict(y_stride=1 << 41), -3),
 ]
 
