@@ -42,13 +42,23 @@ struct MxLinArgs {
 
 __device__ __forceinline__ u32x4 ldg16(const uint8_t* p) { return *reinterpret_cast<const u32x4*>(p); }
 
-// Scale dword of blocks b..b+3 with every block at or past `nb` set to 1
-// (its codes are zeros; what lies past a row's scales may be anything).
-__device__ __forceinline__ uint32_t scale_dword(const uint8_t* row, int b, int nb) {
-  if (b + 4 <= nb) return *reinterpret_cast<const uint32_t*>(row + b);
-  if (b >= nb) return 0x7F7F7F7Fu;
-  const uint32_t keep = (1u << (8 * (nb - b))) - 1u;
-  return (*reinterpret_cast<const uint32_t*>(row + b) & keep) | (0x7F7F7F7Fu & ~keep);
+// Scales of blocks b .. b+15 of a row, with every block at or past `nb` set to
+// 1 (its codes are zeros; what lies past a row's scales may be anything).
+template <bool TAIL>
+__device__ __forceinline__ u32x4 load_scales16(const uint8_t* row, int b, int nb) {
+  const uint32_t* p = reinterpret_cast<const uint32_t*>(row + b);
+  u32x4 v;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    if (!TAIL) {
+      v[q] = p[q];
+      continue;
+    }
+    const int n = nb - b - 4 * q;
+    const uint32_t keep = n >= 4 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << (8 * n)) - 1u);
+    v[q] = ((n > 0 ? p[q] : 0u) & keep) | (0x7F7F7F7Fu & ~keep);
+  }
+  return v;
 }
 
 // The first `keep` bytes of 16, zeros after them.
@@ -61,79 +71,65 @@ __device__ __forceinline__ u32x4 keep_bytes(u32x4 v, int keep) {
   return v;
 }
 
+// One lane's operands of a 512-element step: 4 blocks of K, one in each of 4
+// matrix instructions, and the row's 16 scales.
 template <int XF>
-struct XFrag;                        // one lane's inputs of a 512-element step
-template <> struct XFrag<AR_E4M3_MX> { u32x4 d[4][2]; uint32_t s; };
+struct XFrag;
+template <> struct XFrag<AR_E4M3_MX> { u32x4 d[4][2]; u32x4 s; };
 template <> struct XFrag<AR_E4M3_ROW> { u32x4 d[4][2]; };
-template <> struct XFrag<AR_E2M1_MX> { u32x4 d[4]; uint32_t s; };
+template <> struct XFrag<AR_E2M1_MX> { u32x4 d[4]; u32x4 s; };
 template <> struct XFrag<AR_BF16> { u32x4 d[4][4]; };
 
 struct WFrag {
   u32x4 d[4];
-  uint32_t s;
+  u32x4 s;
 };
 
-// A step is 16 blocks of K.  Sums over k may go in any order that both
-// operands share, so the four lane groups g = lane / 16 of a wave take blocks
-// 4g .. 4g+3 of it, one in each of 4 matrix instructions: a lane's 64 bytes of
-// weights lie together, and its four scales in one dword.
+// Group g = lane / 16 of a wave holds block 4s + g of the step in instruction
+// s, so that the four groups read 64 bytes of a row together.  (With blocks
+// 4g .. 4g + 3 to group g the four scales of a lane share a dword, but each
+// load then touches all the step's lines and they do not stay in the L1: 4
+// ranks of 16 x 8192 x 2048 took 15.2 us.)
 // The instruction wants 4-bit operands as block g's 32 values in group g, but
-// 8-bit ones as values [16g', 16g' + 16) of the 128, for g' = g and g + 4: half
-// (g & 1) of blocks g/2 and g/2 + 2 -- while group g still gives the scale of
-// block g.
+// 8-bit ones as values [16g', 16g' + 16) of the 128, for g' = g and g + 4 --
+// while group g gives the scale of block g in either case.
 template <bool TAIL>
 __device__ __forceinline__ void load_w(const uint8_t* row, const uint8_t* srow, int step, int g, int nb,
                                        WFrag& f) {
-  const int b = 16 * step + 4 * g;
 #pragma unroll
-  for (int s = 0; s < 4; ++s)
-    f.d[s] = !TAIL || b + s < nb ? ldg16(row + (int64_t)(b + s) * 16) : u32x4{0u, 0u, 0u, 0u};
-  f.s = TAIL ? scale_dword(srow, b, nb) : *reinterpret_cast<const uint32_t*>(srow + b);
+  for (int s = 0; s < 4; ++s) {
+    const int b = 16 * step + 4 * s + g;
+    f.d[s] = !TAIL || b < nb ? ldg16(row + (int64_t)b * 16) : u32x4{0u, 0u, 0u, 0u};
+  }
+  f.s = load_scales16<TAIL>(srow, 16 * step, nb);
 }
 
 template <int XF, bool TAIL>
 __device__ __forceinline__ void load_x(const uint8_t* row, const uint8_t* srow, int step, int g, int nb,
                                        int K, XFrag<XF>& f) {
-  if constexpr (XF == AR_E2M1_MX) {
-    const int b = 16 * step + 4 * g;
 #pragma unroll
-    for (int s = 0; s < 4; ++s)
-      f.d[s] = !TAIL || b + s < nb ? ldg16(row + (int64_t)(b + s) * 16) : u32x4{0u, 0u, 0u, 0u};
-    f.s = TAIL ? scale_dword(srow, b, nb) : *reinterpret_cast<const uint32_t*>(srow + b);
-  } else if constexpr (XF == AR_BF16) {
-    const int b = 16 * step + 4 * g;
-#pragma unroll
-    for (int s = 0; s < 4; ++s)
+  for (int s = 0; s < 4; ++s) {
+    const int b = 16 * step + 4 * s + g;
+    if constexpr (XF == AR_E2M1_MX) {
+      f.d[s] = !TAIL || b < nb ? ldg16(row + (int64_t)b * 16) : u32x4{0u, 0u, 0u, 0u};
+    } else if constexpr (XF == AR_BF16) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int at = (b + s) * 32 + 8 * j;               // element
-        if (!TAIL) {
-          f.d[s][j] = ldg16(row + (int64_t)at * 2);
-        } else {
-          f.d[s][j] = at < K ? keep_bytes(ldg16(row + (int64_t)at * 2), 2 * (K - at))
-                             : u32x4{0u, 0u, 0u, 0u};
-        }
+        const int at = b * 32 + 8 * j;                     // element
+        if (!TAIL) f.d[s][j] = ldg16(row + (int64_t)at * 2);
+        else f.d[s][j] = at < K ? keep_bytes(ldg16(row + (int64_t)at * 2), 2 * (K - at)) : u32x4{0u, 0u, 0u, 0u};
       }
-  } else {
-#pragma unroll
-    for (int s = 0; s < 4; ++s)
+    } else {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int b = 16 * step + 4 * ((g >> 1) + 2 * h) + s;
-        const int at = b * 32 + 16 * (g & 1);
-        if (!TAIL) {
-          f.d[s][h] = ldg16(row + at);
-        } else if (XF == AR_E4M3_MX) {
-          f.d[s][h] = b < nb ? ldg16(row + at) : u32x4{0u, 0u, 0u, 0u};
-        } else {
-          f.d[s][h] = at < K ? keep_bytes(ldg16(row + at), K - at) : u32x4{0u, 0u, 0u, 0u};
-        }
+        const int at = (16 * step + 4 * s) * 32 + 64 * h + 16 * g;
+        const int end = XF == AR_E4M3_MX ? nb * 32 : K;
+        if (!TAIL) f.d[s][h] = ldg16(row + at);
+        else f.d[s][h] = at < end ? keep_bytes(ldg16(row + at), end - at) : u32x4{0u, 0u, 0u, 0u};
       }
-    if constexpr (XF == AR_E4M3_MX) {
-      const int b = 16 * step + 4 * g;
-      f.s = TAIL ? scale_dword(srow, b, nb) : *reinterpret_cast<const uint32_t*>(srow + b);
     }
   }
+  if constexpr (is_mx_format(XF)) f.s = load_scales16<TAIL>(srow, 16 * step, nb);
 }
 
 __device__ __forceinline__ i32x8 operand(u32x4 lo, u32x4 hi) {
@@ -150,13 +146,14 @@ __device__ __forceinline__ bf16x8 weights_bf16(uint32_t codes, float scale) {
   return bf16x8{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
 }
 
-// One block of each lane group: S is the scales' byte and the block's place.
+// Instruction S of a step; `shift` brings block 4S + g's scale to the lowest
+// byte, the one the instruction reads.
 template <int XF, int S>
-__device__ __forceinline__ f32x4 multiply(const WFrag& w, const XFrag<XF>& x, f32x4 acc) {
+__device__ __forceinline__ f32x4 multiply(const WFrag& w, const XFrag<XF>& x, int shift, f32x4 acc) {
   constexpr u32x4 none = u32x4{0u, 0u, 0u, 0u};
+  const uint32_t ws = w.s[S] >> shift;
   if constexpr (XF == AR_BF16) {
-    const uint32_t code = (w.s >> (8 * S)) & 0xFFu;
-    const float scale = __uint_as_float(code << 23);
+    const float scale = __uint_as_float((ws & 0xFFu) << 23);
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
@@ -164,13 +161,14 @@ __device__ __forceinline__ f32x4 multiply(const WFrag& w, const XFrag<XF>& x, f3
     return acc;
   } else if constexpr (XF == AR_E2M1_MX) {
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-        operand(w.d[S], none), operand(x.d[S], none), acc, 4, 4, S, (int)w.s, S, (int)x.s);
+        operand(w.d[S], none), operand(x.d[S], none), acc, 4, 4, 0, (int)ws, 0, (int)(x.s[S] >> shift));
   } else if constexpr (XF == AR_E4M3_MX) {
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-        operand(w.d[S], none), operand(x.d[S][0], x.d[S][1]), acc, 4, 0, S, (int)w.s, S, (int)x.s);
+        operand(w.d[S], none), operand(x.d[S][0], x.d[S][1]), acc, 4, 0, 0, (int)ws, 0,
+        (int)(x.s[S] >> shift));
   } else {
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-        operand(w.d[S], none), operand(x.d[S][0], x.d[S][1]), acc, 4, 0, S, (int)w.s, 0, 127);
+        operand(w.d[S], none), operand(x.d[S][0], x.d[S][1]), acc, 4, 0, 0, (int)ws, 0, 127);
   }
 }
 
@@ -191,88 +189,129 @@ __device__ __forceinline__ void store_out4(void* y, int64_t at, int n, int N, bo
   }
 }
 
-// Few tokens: bound by the stream of weights.  A wave holds 16 outputs and
-// 16 * MT tokens; WK waves split K step by step and join their sums, in
-// order, in shared memory.
-template <int XF, int YF, int MT, int WN, int WK>
+// Few tokens: bound by the stream of weights.  A wave holds 16 * NT outputs
+// and 16 * MT tokens; WK waves split K step by step and join their sums, in
+// order, in shared memory.  The next step's operands are on their way while
+// one is multiplied.
+template <int XF, int YF, int NT, int MT, int WN, int WK>
 __global__ __launch_bounds__(kWave * WN * WK) void k_mx_linear_rows(MxLinArgs a) {
-  __shared__ f32x4 part[WK > 1 ? WK * WN * MT * kWave : 1];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  constexpr int tiles = NT * MT;
+  __shared__ f32x4 part[WK > 1 ? WK * WN * tiles * kWave : 1];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wk = wave % WK, wn = wave / WK;
-  const int c = lane & 15, g = lane >> 4;
+  const int c = lane & 15, g = lane >> 4, shift = 8 * g;
   int b = blockIdx.x;
   const int mg = b % a.m_groups;
   b /= a.m_groups;
   const int ng = b % a.n_groups;
   const int r = b / a.n_groups;
-  const int n0 = (ng * WN + wn) * 16, m0 = mg * MT * 16;
-  const int n = min(n0 + c, a.N - 1);
-  const uint8_t* wrow = a.w + r * a.w_rank + n * a.w_stride;
-  const uint8_t* wsrow = a.ws + r * a.ws_rank + n * a.ws_stride;
-  const uint8_t* xrow[MT];
-  const uint8_t* xsrow[MT];
+  const int n0 = (ng * WN + wn) * 16 * NT, m0 = mg * MT * 16;
+  const uint8_t *wrow[NT], *wsrow[NT], *xrow[MT], *xsrow[MT];
 #pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    const int m = min(m0 + i * 16 + c, a.M - 1);
-    xrow[i] = a.x + r * a.x_rank + m * a.x_stride;
-    xsrow[i] = a.xs + r * a.xs_rank + m * a.xs_stride;
+  for (int i = 0; i < NT; ++i) {                           // rows past the end read the last one
+    const int n = min(n0 + i * 16 + c, a.N - 1);
+    wrow[i] = a.w + r * a.w_rank + n * a.w_stride;
+    wsrow[i] = a.ws + r * a.ws_rank + n * a.ws_stride;
   }
-  f32x4 acc[MT];
 #pragma unroll
-  for (int i = 0; i < MT; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  // steps that hold whole blocks only
+  for (int j = 0; j < MT; ++j) {
+    const int m = min(m0 + j * 16 + c, a.M - 1);
+    xrow[j] = a.x + r * a.x_rank + m * a.x_stride;
+    xsrow[j] = a.xs + r * a.xs_rank + m * a.xs_stride;
+  }
+  f32x4 acc[NT][MT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int j = 0; j < MT; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  struct Step {
+    WFrag w[NT];
+    XFrag<XF> x[MT];
+  };
+  auto load = [&](int st, Step& f) {
+#pragma unroll
+    for (int i = 0; i < NT; ++i) load_w<false>(wrow[i], wsrow[i], st, g, a.nb, f.w[i]);
+#pragma unroll
+    for (int j = 0; j < MT; ++j) load_x<XF, false>(xrow[j], xsrow[j], st, g, a.nb, a.K, f.x[j]);
+  };
+  auto compute = [&](const Step& f) {
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int j = 0; j < MT; ++j) acc[i][j] = multiply<XF, 0>(f.w[i], f.x[j], shift, acc[i][j]);
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int j = 0; j < MT; ++j) acc[i][j] = multiply<XF, 1>(f.w[i], f.x[j], shift, acc[i][j]);
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int j = 0; j < MT; ++j) acc[i][j] = multiply<XF, 2>(f.w[i], f.x[j], shift, acc[i][j]);
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int j = 0; j < MT; ++j) acc[i][j] = multiply<XF, 3>(f.w[i], f.x[j], shift, acc[i][j]);
+  };
+  // steps that hold whole blocks only, then maybe one that K ends in
   const int full = (is_mx_format(XF) ? a.nb : a.K / 32) / 16;
   const int steps = (a.nb + 15) / 16;
-  for (int st = wk; st < steps; st += WK) {
-    WFrag w;
-    XFrag<XF> x[MT];
-    if (st < full) {
-      load_w<false>(wrow, wsrow, st, g, a.nb, w);
-#pragma unroll
-      for (int i = 0; i < MT; ++i) load_x<XF, false>(xrow[i], xsrow[i], st, g, a.nb, a.K, x[i]);
-    } else {
-      load_w<true>(wrow, wsrow, st, g, a.nb, w);
-#pragma unroll
-      for (int i = 0; i < MT; ++i) load_x<XF, true>(xrow[i], xsrow[i], st, g, a.nb, a.K, x[i]);
+  int st = wk;
+  if (st < full) {
+    Step cur;
+    load(st, cur);
+    for (; st + WK < full; st += WK) {
+      Step next;
+      load(st + WK, next);
+      compute(cur);
+      cur = next;
     }
+    compute(cur);
+    st += WK;
+  }
+  if (st < steps) {
+    Step f;
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      acc[i] = multiply<XF, 0>(w, x[i], acc[i]);
-      acc[i] = multiply<XF, 1>(w, x[i], acc[i]);
-      acc[i] = multiply<XF, 2>(w, x[i], acc[i]);
-      acc[i] = multiply<XF, 3>(w, x[i], acc[i]);
-    }
+    for (int i = 0; i < NT; ++i) load_w<true>(wrow[i], wsrow[i], st, g, a.nb, f.w[i]);
+#pragma unroll
+    for (int j = 0; j < MT; ++j) load_x<XF, true>(xrow[j], xsrow[j], st, g, a.nb, a.K, f.x[j]);
+    compute(f);
   }
   if constexpr (WK > 1) {
 #pragma unroll
-    for (int i = 0; i < MT; ++i) part[((wk * WN + wn) * MT + i) * kWave + lane] = acc[i];
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int j = 0; j < MT; ++j)
+        part[((wk * WN + wn) * tiles + i * MT + j) * kWave + lane] = acc[i][j];
     __syncthreads();
   }
 #pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    if (i % WK != wk) continue;                            // the waves of a group share the tiles
-    f32x4 v = acc[i];
-    if constexpr (WK > 1) {
-      v = part[(wn * MT + i) * kWave + lane];
+  for (int i = 0; i < NT; ++i)
 #pragma unroll
-      for (int k = 1; k < WK; ++k) v += part[((k * WN + wn) * MT + i) * kWave + lane];
+    for (int j = 0; j < MT; ++j) {
+      const int t = i * MT + j;
+      if (t % WK != wk) continue;                          // the waves of a group share the tiles
+      f32x4 v = acc[i][j];
+      if constexpr (WK > 1) {
+        v = part[(wn * tiles + t) * kWave + lane];
+#pragma unroll
+        for (int k = 1; k < WK; ++k) v += part[((k * WN + wn) * tiles + t) * kWave + lane];
+      }
+      const int m = m0 + j * 16 + c, n = n0 + i * 16 + 4 * g;
+      if (m >= a.M || n >= a.N) continue;
+      if constexpr (XF == AR_E4M3_ROW) {
+        if (a.K > 0) v *= *reinterpret_cast<const float*>(xsrow[j]);
+      }
+      store_out4<YF>(a.y, r * a.y_rank + m * a.y_stride + n, n, a.N, a.vec != 0, v);
     }
-    const int m = m0 + i * 16 + c;
-    if (m >= a.M || n0 + 4 * g >= a.N) continue;
-    if constexpr (XF == AR_E4M3_ROW) {
-      if (a.K > 0) v *= *reinterpret_cast<const float*>(xsrow[i]);
-    }
-    store_out4<YF>(a.y, r * a.y_rank + m * a.y_stride + n0 + 4 * g, n0 + 4 * g, a.N, a.vec != 0, v);
-  }
 }
 
 // ---------------------------------------------------------- many tokens ---
 //
 // Bound by the matrix cores.  A workgroup holds BN outputs by BM tokens; K
-// goes by in steps of 128 elements (64 for bf16 inputs), three steps' codes in
-// shared memory: while one is multiplied the next has arrived and the one
-// after is on its way, loaded straight into shared memory, and one barrier a
-// step is enough.  Rows lie there as they come, 16-byte pieces permuted by the
+// goes by in steps of 128 elements (64 for bf16 inputs), NS steps' codes in shared
+// memory: while one is multiplied the ones after it are on their way, loaded
+// straight into shared memory, and one barrier a step is enough.  Rows lie there as they come, 16-byte pieces permuted by the
 // row so that the lanes that read at once meet different banks; the loads
 // apply the permutation to their addresses.  Scales come 512 elements at a
 // time, one row a thread.
@@ -284,10 +323,18 @@ __device__ __forceinline__ void load_to_lds(rsrc_t r, uint8_t* lds, uint32_t lan
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)lds, 16, lane_off, off, 0, 0);
 }
 
-template <int XF>
+__device__ __forceinline__ void load_to_lds(const uint8_t* p, uint8_t* lds) {
+  typedef __attribute__((address_space(3))) void lds_void;
+  typedef const __attribute__((address_space(1))) void global_void;
+  __builtin_amdgcn_global_load_lds((global_void*)p, (lds_void*)lds, 16, 0, 0);
+}
+
+template <int XF, int BK_>
 struct TileShape {
-  static constexpr int BK = XF == AR_BF16 ? 64 : 128;      // elements of K a step
-  static constexpr int XB = XF == AR_E2M1_MX ? 64 : 128;   // bytes of an x row a step
+  static constexpr int BK = BK_;                           // elements of K a step
+  static constexpr int BI = XF == AR_BF16 ? 64 : 128;      // and of one round of instructions
+  static constexpr int rounds = BK / BI;
+  static constexpr int XB = XF == AR_BF16 ? 2 * BK : (XF == AR_E2M1_MX ? BK / 2 : BK);  // bytes of an x row
   static constexpr int WB = BK / 2;                        // bytes of a weight row
   static constexpr int XC = XB / 16, WC = WB / 16;         // 16-byte pieces
   static constexpr int steps_scales = 512 / BK;            // steps that share 16 scales a row
@@ -297,7 +344,7 @@ struct TileShape {
 // read together cover every 16-byte column of 128 bytes.
 template <int C>
 __device__ __forceinline__ int place(int r, int c) {
-  if constexpr (C == 8) return c ^ (r & 7);
+  if constexpr (C >= 8) return c ^ (r & 7);
   else if constexpr (C == 4) return c ^ ((r >> 1) & 3);
   else return c ^ ((r >> 2) & 1);
 }
@@ -308,24 +355,36 @@ __device__ __forceinline__ void barrier_only() {
   compiler_barrier();
 }
 
-template <int XF_, int YF_, int BM_, int BN_, int WM_, int WN_>
+template <int XF_, int YF_, int BK_, int BM_, int BN_, int WM_, int WN_, int NS_>
 struct Tile {
-  static constexpr int XF = XF_, YF = YF_, BM = BM_, BN = BN_, WM = WM_, WN = WN_;
-  using T = TileShape<XF>;
+  static constexpr int XF = XF_, YF = YF_, BM = BM_, BN = BN_, WM = WM_, WN = WN_, NS = NS_;
+  using T = TileShape<XF, BK_>;
   static constexpr int waves = (BM / WM) * (BN / WN);
   static constexpr int threads = waves * kWave;
   static constexpr int xbytes = BM * T::XB, wbytes = BN * T::WB;
   static constexpr int stage = xbytes + wbytes;
-  static constexpr int nx = xbytes / 16 / threads, nw = wbytes / 16 / threads;   // loads a thread
-  static constexpr int scales = (BM + BN) * 16;
-  static constexpr int lds = 3 * stage + 2 * scales;
-  static_assert(nx >= 1 && nw >= 1 && BM + BN == threads, "one row of scales a thread");
+  // 16-byte pieces of a step, and loads of a thread (where there are fewer
+  // pieces than threads, some load a piece that another one loads too)
+  static constexpr int px = xbytes / 16, pw = wbytes / 16;
+  static constexpr int nx = (px + threads - 1) / threads, nw = (pw + threads - 1) / threads;
+  // rows of scales: the weights', then the tokens' where they have some
+  static constexpr int srows = is_mx_format(XF) ? BM + BN : BN;
+  static constexpr int swaves = (srows + kWave - 1) / kWave;
+  static constexpr int ns = (swaves + waves - 1) / waves;
+  static constexpr int scales = swaves * kWave * 16;
+  static constexpr int lds = NS * stage + 2 * scales;
+  static_assert(px % kWave == 0 && pw % kWave == 0, "whole waves load");
+  static_assert(threads % px == 0 || px % threads == 0, "");
+  static_assert(threads % pw == 0 || pw % threads == 0, "");
+  static_assert(waves % swaves == 0 || swaves % waves == 0, "");
+  static_assert(NS - 1 <= T::steps_scales, "scales of two runs of steps at a time");
+  static_assert((NS - 2) * (nx + nw) < 64, "loads on their way that a wait can name");
 };
 
 template <class G>
 __global__ __launch_bounds__(G::threads) void k_mx_linear_tiles(MxLinArgs a) {
   using T = typename G::T;
-  constexpr int XF = G::XF, YF = G::YF, BM = G::BM, BN = G::BN, WM = G::WM, WN = G::WN;
+  constexpr int XF = G::XF, YF = G::YF, BM = G::BM, BN = G::BN, WM = G::WM, WN = G::WN, NS = G::NS;
   constexpr int TI = WN / 16, TJ = WM / 16;                // matrix tiles of a wave
   __shared__ __align__(256) uint8_t smem[G::lds];
   const int tid = threadIdx.x, lane = tid & 63;
@@ -360,70 +419,66 @@ __global__ __launch_bounds__(G::threads) void k_mx_linear_tiles(MxLinArgs a) {
   uint32_t xo[G::nx], wo[G::nw];
 #pragma unroll
   for (int i = 0; i < G::nx; ++i) {
-    const int at = i * G::threads + tid, row = at / T::XC;
+    const int at = (i * G::threads + tid) % G::px, row = at / T::XC;
     xo[i] = (uint32_t)min(row, mlast) * (uint32_t)a.x_stride + place<T::XC>(row, at % T::XC) * 16;
   }
 #pragma unroll
   for (int i = 0; i < G::nw; ++i) {
-    const int at = i * G::threads + tid, row = at / T::WC;
+    const int at = (i * G::threads + tid) % G::pw, row = at / T::WC;
     wo[i] = (uint32_t)min(row, nlast) * (uint32_t)a.w_stride + place<T::WC>(row, at % T::WC) * 16;
   }
   auto load_step = [&](int k, int buf) {
-    uint8_t* at = smem + buf * G::stage + wave * 1024;
+    uint8_t* at = smem + buf * G::stage;
 #pragma unroll
     for (int i = 0; i < G::nx; ++i)
-      load_to_lds(xr, at + i * G::threads * 16, xo[i], (uint32_t)k * T::XB);
+      load_to_lds(xr, at + (i * G::threads + wave * kWave) % G::px * 16, xo[i], (uint32_t)k * T::XB);
 #pragma unroll
     for (int i = 0; i < G::nw; ++i)
-      load_to_lds(wr, at + G::xbytes + i * G::threads * 16, wo[i], (uint32_t)k * T::WB);
+      load_to_lds(wr, at + G::xbytes + (i * G::threads + wave * kWave) % G::pw * 16, wo[i],
+                  (uint32_t)k * T::WB);
   };
   // a step that K ends in: zeros past it
   auto load_tail = [&](int k, int buf) {
-    uint8_t* at = smem + buf * G::stage + tid * 16;
+    uint8_t* at = smem + buf * G::stage;
 #pragma unroll
     for (int i = 0; i < G::nx; ++i) {
-      const int slot = i * G::threads + tid, row = slot / T::XC;
+      const int slot = (i * G::threads + tid) % G::px, row = slot / T::XC;
       const int first = k * T::XB + place<T::XC>(row, slot % T::XC) * 16;       // byte of the row
       const int end = XF == AR_BF16 ? 2 * a.K : (XF == AR_E4M3_ROW ? a.K : a.nb * (XF == AR_E2M1_MX ? 16 : 32));
       u32x4 v = u32x4{0u, 0u, 0u, 0u};
       if (first < end) v = keep_bytes(ldg16(xbase + xo[i] + k * T::XB), end - first);
-      *reinterpret_cast<u32x4*>(at + i * G::threads * 16) = v;
+      *reinterpret_cast<u32x4*>(at + slot * 16) = v;
     }
 #pragma unroll
     for (int i = 0; i < G::nw; ++i) {
-      const int slot = i * G::threads + tid, row = slot / T::WC;
+      const int slot = (i * G::threads + tid) % G::pw, row = slot / T::WC;
       const int first = k * T::WB + place<T::WC>(row, slot % T::WC) * 16;
       u32x4 v = u32x4{0u, 0u, 0u, 0u};
       if (first < a.nb * 16) v = ldg16(wbase + wo[i] + k * T::WB);
-      *reinterpret_cast<u32x4*>(at + G::xbytes + i * G::threads * 16) = v;
+      *reinterpret_cast<u32x4*>(at + G::xbytes + slot * 16) = v;
     }
   };
-  // scales: thread t holds weight row t, or token t - BN
-  const bool mine_w = tid < BN;
-  const bool no_scale = !mine_w && !is_mx_format(XF);
-  const uint8_t* wsafe = a.ws + r * a.ws_rank + n0 * a.ws_stride;
-  const uint8_t* srow = mine_w ? a.ws + r * a.ws_rank + (n0 + min(tid, nlast)) * a.ws_stride
-                               : a.xs + r * a.xs_rank + (m0 + min(tid - BN, mlast)) * a.xs_stride;
-  // 16 scales from step k on, raw; the last dword again where the row has ended
-  const int slast = (a.nb - 1) & ~3;
-  auto load_scales = [&](int k) -> u32x4 {
+  // Scales of the run of steps that begins with step k: 16 of each row, those
+  // of the tokens after those of the weights.
+  const uint8_t* srow[G::ns];
+#pragma unroll
+  for (int i = 0; i < G::ns; ++i) {
+    const int row = (i * G::threads + tid) % (G::swaves * kWave);
+    srow[i] = !is_mx_format(XF) || row < BN
+                  ? a.ws + r * a.ws_rank + (n0 + min(row, nlast)) * a.ws_stride
+                  : a.xs + r * a.xs_rank + (m0 + min(row - BN, mlast)) * a.xs_stride;
+  }
+  auto load_scales = [&](int k) {
+    uint8_t* at = smem + NS * G::stage + (k / T::steps_scales & 1) * G::scales;
     const int blk = k * (T::BK / 32);
-    u32x4 v;
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-      v[q] = *reinterpret_cast<const uint32_t*>((no_scale ? wsafe : srow) + min(blk + 4 * q, slast));
-    return v;
-  };
-  // into shared memory, with 1 for every block past the end
-  auto put_scales = [&](int k, u32x4 v) {
-    const int left = a.nb - k * (T::BK / 32);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int n = no_scale ? 0 : left - 4 * q;
-      const uint32_t keep = n >= 4 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << (8 * n)) - 1u);
-      v[q] = (v[q] & keep) | (0x7F7F7F7Fu & ~keep);
+    for (int i = 0; i < G::ns; ++i) {
+      if (blk + 16 <= a.nb)
+        load_to_lds(srow[i] + blk, at + (i * G::threads + wave * kWave) % (G::swaves * kWave) * 16);
+      else                                                 // K ends in these
+        *reinterpret_cast<u32x4*>(at + (i * G::threads + tid) % (G::swaves * kWave) * 16) =
+            load_scales16<true>(srow[i], blk, a.nb);
     }
-    *reinterpret_cast<u32x4*>(smem + 3 * G::stage + (k / T::steps_scales & 1) * G::scales + tid * 16) = v;
   };
 
   f32x4 acc[TI][TJ];
@@ -432,62 +487,88 @@ __global__ __launch_bounds__(G::threads) void k_mx_linear_tiles(MxLinArgs a) {
 #pragma unroll
     for (int j = 0; j < TJ; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-  auto compute = [&](int k, int buf) {
+  // Operands of one round (round h of a step) in registers.  8- and 4-bit
+  // tokens: one matrix instruction a tile; bf16: two, group g with elements
+  // 16g .. 16g + 15 of the 64.
+  struct Tokens {
+    u32x4 d[TJ][2];
+    int s[TJ];
+  };
+  struct Weights {
+    u32x4 d;
+    int s;
+  };
+  auto scales_at = [&](int k, int h) {
+    return smem + NS * G::stage + (k / T::steps_scales & 1) * G::scales + (k % T::steps_scales) * (T::BK / 32) +
+           h * (T::BI / 32);
+  };
+  auto read_tokens = [&](int k, int h, int buf, Tokens& f) {
     const uint8_t* xs = smem + buf * G::stage;
-    const uint8_t* ws = xs + G::xbytes;
-    const int ss = k / T::steps_scales;
-    const uint8_t* sc = smem + 3 * G::stage + (ss & 1) * G::scales + (k % T::steps_scales) * (T::BK / 32);
+    const uint8_t* sc = scales_at(k, h);
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) {
+      const int row = wj * WM + j * 16 + c;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        if (XF == AR_E2M1_MX && q == 1) continue;
+        const int piece = h * (T::XC / T::rounds) + (XF == AR_BF16 ? 2 * g + q : 4 * q + g);
+        f.d[j][q] = *reinterpret_cast<const u32x4*>(xs + row * T::XB + place<T::XC>(row, piece) * 16);
+      }
+      if constexpr (is_mx_format(XF)) f.s[j] = (int)sc[(BN + row) * 16 + g];
+    }
+  };
+  auto read_weights = [&](int k, int h, int buf, int i, Weights& f) {
+    const uint8_t* ws = smem + buf * G::stage + G::xbytes;
+    const uint8_t* sc = scales_at(k, h);
+    const int first = h * (T::WC / T::rounds);
+    const int row = wi * WN + i * 16 + c;
     if constexpr (XF == AR_BF16) {
-      // group g takes elements 16g .. 16g + 15, 8 in each of two instructions
-      u32x4 x[TJ][2];
+      const u32x2 d = *reinterpret_cast<const u32x2*>(ws + row * T::WB +
+                                                      place<T::WC>(row, first + (g >> 1)) * 16 + (g & 1) * 8);
+      f.d.x = d.x;
+      f.d.y = d.y;
+      f.s = (int)sc[row * 16 + (g >> 1)];
+    } else {
+      f.d = *reinterpret_cast<const u32x4*>(ws + row * T::WB + place<T::WC>(row, first + g) * 16);
+      f.s = (int)sc[row * 16 + g];
+    }
+  };
+  auto multiply_row = [&](int i, const Weights& w, const Tokens& x) {
+    if constexpr (XF == AR_BF16) {
+      const float scale = __uint_as_float((uint32_t)w.s << 23);
+      const bf16x8 w0 = weights_bf16(w.d.x, scale), w1 = weights_bf16(w.d.y, scale);
 #pragma unroll
       for (int j = 0; j < TJ; ++j) {
-        const int row = wj * WM + j * 16 + c;
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          x[j][h] = *reinterpret_cast<const u32x4*>(xs + row * T::XB + place<T::XC>(row, 2 * g + h) * 16);
-      }
-#pragma unroll
-      for (int i = 0; i < TI; ++i) {
-        const int row = wi * WN + i * 16 + c;
-        const u32x2 w = *reinterpret_cast<const u32x2*>(ws + row * T::WB + place<T::WC>(row, g >> 1) * 16 +
-                                                        (g & 1) * 8);
-        const float scale = __uint_as_float((uint32_t)sc[row * 16 + (g >> 1)] << 23);
-        const bf16x8 w0 = weights_bf16(w.x, scale), w1 = weights_bf16(w.y, scale);
-#pragma unroll
-        for (int j = 0; j < TJ; ++j) {
-          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w0, __builtin_bit_cast(bf16x8, x[j][0]),
-                                                              acc[i][j], 0, 0, 0);
-          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w1, __builtin_bit_cast(bf16x8, x[j][1]),
-                                                              acc[i][j], 0, 0, 0);
-        }
+        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w0, __builtin_bit_cast(bf16x8, x.d[j][0]),
+                                                            acc[i][j], 0, 0, 0);
+        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w1, __builtin_bit_cast(bf16x8, x.d[j][1]),
+                                                            acc[i][j], 0, 0, 0);
       }
     } else {
       constexpr u32x4 none = u32x4{0u, 0u, 0u, 0u};
-      constexpr int xcode = XF == AR_E2M1_MX ? 4 : 0;
-      i32x8 x[TJ];
-      int xsc[TJ];
 #pragma unroll
       for (int j = 0; j < TJ; ++j) {
-        const int row = wj * WM + j * 16 + c;
-        if constexpr (XF == AR_E2M1_MX) {
-          x[j] = operand(*reinterpret_cast<const u32x4*>(xs + row * T::XB + place<T::XC>(row, g) * 16), none);
-        } else {
-          x[j] = operand(*reinterpret_cast<const u32x4*>(xs + row * T::XB + place<T::XC>(row, g) * 16),
-                         *reinterpret_cast<const u32x4*>(xs + row * T::XB + place<T::XC>(row, 4 + g) * 16));
-        }
-        xsc[j] = XF == AR_E4M3_ROW ? 127 : (int)sc[(BN + row) * 16 + g];
+        const i32x8 b = operand(x.d[j][0], XF == AR_E2M1_MX ? none : x.d[j][1]);
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+            operand(w.d, none), b, acc[i][j], 4, XF == AR_E2M1_MX ? 4 : 0, 0, w.s, 0,
+            is_mx_format(XF) ? x.s[j] : 127);
       }
+    }
+  };
+  // one weight tile's operands ahead of the products, so that reads of shared
+  // memory and matrix instructions of one wave overlap
+  auto compute = [&](int k, int buf) {
+#pragma unroll
+    for (int h = 0; h < T::rounds; ++h) {
+      Tokens x;
+      Weights w[2];
+      read_tokens(k, h, buf, x);
+      read_weights(k, h, buf, 0, w[0]);
 #pragma unroll
       for (int i = 0; i < TI; ++i) {
-        const int row = wi * WN + i * 16 + c;
-        const i32x8 w =
-            operand(*reinterpret_cast<const u32x4*>(ws + row * T::WB + place<T::WC>(row, g) * 16), none);
-        const int wsc = (int)sc[row * 16 + g];
-#pragma unroll
-        for (int j = 0; j < TJ; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x[j], acc[i][j], 4, xcode, 0, wsc,
-                                                                       0, xsc[j]);
+        if (i + 1 < TI) read_weights(k, h, buf, i + 1, w[(i + 1) & 1]);
+        multiply_row(i, w[i & 1], x);
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
   };
@@ -495,26 +576,72 @@ __global__ __launch_bounds__(G::threads) void k_mx_linear_tiles(MxLinArgs a) {
   // whole steps, then maybe one that K ends in
   const int full = (is_mx_format(XF) ? a.nb * 32 : a.K) / T::BK;
   const int steps = (a.nb * 32 + T::BK - 1) / T::BK;
-  if (full > 0) load_step(0, 0);
-  if (full > 1) load_step(1, 1);
-  if (steps > 0) put_scales(0, load_scales(0));
-  u32x4 next = u32x4{0u, 0u, 0u, 0u};
+  if (steps > 0) load_scales(0);
+#pragma unroll
+  for (int k = 0; k < NS - 1; ++k)
+    if (k < full) load_step(k, k);
+  constexpr int behind = (NS - 2) * (G::nx + G::nw);
+  constexpr int wait_behind = 0x0F70 | (behind & 15) | (behind >> 4) << 14;      // vmcnt alone
   int buf = 0;
-  for (int k = 0; k < full; ++k) {
-    // step k has arrived when at most one step's loads are still on their way
-    // (the scales' loads, where there are some, only make the wait longer), and
-    // this wave's own scales are written
-    if (k + 1 < full) __builtin_amdgcn_s_waitcnt(0x0070 | (G::nx + G::nw));
-    else __builtin_amdgcn_s_waitcnt(0x0070);
-    barrier_only();
-    int into = buf + 2;
-    if (into >= 3) into -= 3;
-    if (k + 2 < full) load_step(k + 2, into);
-    const int ks = k % T::steps_scales;
-    if (ks == 0 && k + T::steps_scales < steps) next = load_scales(k + T::steps_scales);
-    compute(k, buf);
-    if (ks == T::steps_scales - 1 && k + 1 < steps) put_scales(k + 1, next);
-    if (++buf == 3) buf = 0;
+  if constexpr (G::waves == 8) {
+    // Two waves to a SIMD, half a step apart: while one reads its operands of
+    // a step from shared memory, the other one multiplies, and they change
+    // places at a barrier.  Waves 0..3 read step k in phase 2k and multiply in
+    // 2k + 1, waves 4..7 one phase later.  Step k + NS - 1 goes into the buffer
+    // of step k - 1, which was last read in phase 2k - 1.  4096 x 8192 x 8192,
+    // 8-bit tokens: 211 us against 220 with all waves in step, bf16 382 against
+    // 430.  (A wave's tile as 32 x 32 x 64 instructions: 233.)
+    static_assert(T::rounds == 1, "a phase is a step");
+    const bool late = wave >= 4;
+    auto arrived = [&](int k) {                            // this wave's loads of step k + 1
+      if (NS > 2 && k + NS - 1 < full) __builtin_amdgcn_s_waitcnt(wait_behind);
+      else __builtin_amdgcn_s_waitcnt(0x0F70);
+    };
+    auto change = [&]() {
+      __builtin_amdgcn_sched_barrier(0);
+      barrier_only();
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    if (full > 0) {
+      if (NS > 2 && full > NS - 2) __builtin_amdgcn_s_waitcnt(wait_behind & ~0x0F00);
+      else __builtin_amdgcn_s_waitcnt(0x0070);
+      change();
+      if (late) change();
+    }
+    for (int k = 0; k < full; ++k) {
+      const int ahead = k + NS - 1;
+      if (ahead < steps && ahead % T::steps_scales == 0) load_scales(ahead);
+      if (ahead < full) load_step(ahead, buf == 0 ? NS - 1 : buf - 1);
+      Tokens x;
+      Weights w[TI];
+      read_tokens(k, 0, buf, x);
+#pragma unroll
+      for (int i = 0; i < TI; ++i) read_weights(k, 0, buf, i, w[i]);
+      __builtin_amdgcn_s_waitcnt(0xC07F);                  // operands here, own scales written
+      if (late) arrived(k);
+      change();
+#pragma unroll
+      for (int i = 0; i < TI; ++i) multiply_row(i, w[i], x);
+      if (!late) arrived(k);
+      change();
+      if (++buf == NS) buf = 0;
+    }
+    if (full > 0 && !late) change();
+  } else {
+    for (int k = 0; k < full; ++k) {
+      // Step k has arrived when at most the NS - 2 steps after it are still on
+      // their way (scales among them only make the wait longer), and this
+      // wave's own scales are written.
+      if (k + NS - 2 < full) __builtin_amdgcn_s_waitcnt(wait_behind & ~0x0F00);
+      else __builtin_amdgcn_s_waitcnt(0x0070);
+      barrier_only();
+      // into the buffer of step k - 1, which every wave has left
+      const int ahead = k + NS - 1;
+      if (ahead < steps && ahead % T::steps_scales == 0) load_scales(ahead);
+      if (ahead < full) load_step(ahead, buf == 0 ? NS - 1 : buf - 1);
+      compute(k, buf);
+      if (++buf == NS) buf = 0;
+    }
   }
   if (steps > full) {
     __syncthreads();
@@ -577,28 +704,40 @@ static int check_linear(const ar_linear_params* p) {
   return AR_OK;
 }
 
-template <int XF, int YF, int MT>
-static hipError_t launch_rows(const MxLinArgs& a0, int nranks, int mt_groups, hipStream_t s) {
+// Up to 16 tokens.  Waves of 32 outputs read x half as often as waves of 16,
+// and K is split until 2048 waves (two for each SIMD) share the stream of
+// weights; where even 8 parts do not give that many, waves take 16 outputs.
+// 16 tokens, 8-bit, 4 x 8192 x 2048: 11.1 us with 32 outputs, 14.3 with 16; one
+// token, 4096 x 4096: 3.9 us with 16 outputs and 4 parts, 5.4 with 32 and 8; 16
+// tokens, 8192 x 8192: 11.3 us with 8 parts, 11.9 with 4, 19 with 2.
+constexpr int64_t kRowsWaves = 2048;
+
+template <int XF, int YF, int NT>
+static hipError_t launch_rows(const MxLinArgs& a0, int nranks, hipStream_t s) {
   MxLinArgs a = a0;
-  a.m_groups = mt_groups;
   const int steps = (a.nb + 15) / 16;
-  const int tiles = (a.N + 15) / 16;
-  auto go = [&](auto kernel, int wn, int waves) {
-    a.n_groups = (tiles + wn - 1) / wn;
+  const int64_t tiles = (a.N + 16 * NT - 1) / (16 * NT);
+  a.m_groups = (a.M + 15) / 16;
+  auto go = [&](auto kernel, int wn, int wk) {
+    a.n_groups = (int)((tiles + wn - 1) / wn);
     return launch(kernel, dim3((unsigned)((int64_t)nranks * a.n_groups * a.m_groups)),
-                  dim3(kWave * waves), s, a);
+                  dim3(kWave * wn * wk), s, a);
   };
-  if (steps >= 4) return go(k_mx_linear_rows<XF, YF, MT, 1, 4>, 1, 4);
-  if (steps >= 2) return go(k_mx_linear_rows<XF, YF, MT, 2, 2>, 2, 4);
-  return go(k_mx_linear_rows<XF, YF, MT, 4, 1>, 4, 4);
+  int wk = 1;
+  while (wk < 8 && 2 * wk <= steps && tiles * nranks * wk < kRowsWaves) wk *= 2;
+  switch (wk) {
+    case 1: return go(k_mx_linear_rows<XF, YF, NT, 1, 4, 1>, 4, 1);
+    case 2: return go(k_mx_linear_rows<XF, YF, NT, 1, 2, 2>, 2, 2);
+    case 4: return go(k_mx_linear_rows<XF, YF, NT, 1, 1, 4>, 1, 4);
+    default: return go(k_mx_linear_rows<XF, YF, NT, 1, 1, 8>, 1, 8);
+  }
 }
 
-template <int XF, int YF, int BM, int BN, int WM, int WN>
+template <class G>
 static hipError_t launch_tiles(const MxLinArgs& a0, int nranks, hipStream_t s) {
   MxLinArgs a = a0;
-  a.n_groups = (a.N + BN - 1) / BN;
-  a.m_groups = (a.M + BM - 1) / BM;
-  using G = Tile<XF, YF, BM, BN, WM, WN>;
+  a.n_groups = (a.N + G::BN - 1) / G::BN;
+  a.m_groups = (a.M + G::BM - 1) / G::BM;
   return launch(k_mx_linear_tiles<G>, dim3((unsigned)((int64_t)nranks * a.n_groups * a.m_groups)),
                 dim3(G::threads), s, a);
 }
@@ -606,14 +745,18 @@ static hipError_t launch_tiles(const MxLinArgs& a0, int nranks, hipStream_t s) {
 template <int XF, int YF>
 static hipError_t launch_linear(const MxLinArgs& a, int nranks, hipStream_t s) {
   // the tile kernels' offsets inside a tile are 31 bits
-  if (a.M > 64 && a.x_stride < (1 << 23) && a.w_stride < (1 << 23)) {
+  if (a.M > 16 && a.x_stride < (1 << 23) && a.w_stride < (1 << 23)) {
+    constexpr int K1 = XF == AR_BF16 ? 64 : 128;
+    constexpr bool x4 = XF == AR_E2M1_MX;
     const int64_t big = (int64_t)((a.N + 255) / 256) * ((a.M + 255) / 256) * nranks;
-    if (big >= 256) return launch_tiles<XF, YF, 256, 256, 64, 128>(a, nranks, s);
-    return launch_tiles<XF, YF, 128, 128, 64, 64>(a, nranks, s);
+    if (a.M <= 32) return launch_tiles<Tile<XF, YF, K1, 32, 64, 32, 16, 5>>(a, nranks, s);
+    if (a.M <= 64) return launch_tiles<Tile<XF, YF, K1, 64, 64, 32, 32, 4>>(a, nranks, s);
+    if (big >= 256) return launch_tiles<Tile<XF, YF, K1, 256, 256, 64, 128, 3>>(a, nranks, s);
+    return launch_tiles<Tile<XF, YF, x4 ? 256 : K1, 128, 128, 64, 64, x4 ? 2 : 3>>(a, nranks, s);
   }
-  if (a.M <= 16) return launch_rows<XF, YF, 1>(a, nranks, 1, s);
-  if (a.M <= 32) return launch_rows<XF, YF, 2>(a, nranks, 1, s);
-  return launch_rows<XF, YF, 4>(a, nranks, (a.M + 63) / 64, s);
+  const int64_t steps = (a.nb + 15) / 16, wide = (int64_t)((a.N + 31) / 32) * nranks;
+  if (wide * (steps < 8 ? steps : 8) >= kRowsWaves) return launch_rows<XF, YF, 2>(a, nranks, s);
+  return launch_rows<XF, YF, 1>(a, nranks, s);
 }
 
 template <int XF>
