@@ -355,11 +355,15 @@ __device__ __forceinline__ void barrier_only() {
   compiler_barrier();
 }
 
-template <int XF_, int YF_, int BK_, int BM_, int BN_, int WM_, int WN_, int NS_>
+// KG groups of waves share a step's rounds among them and join their sums at
+// the end: more waves, and fewer steps one after the other, where there are few
+// tiles.
+template <int XF_, int YF_, int BK_, int BM_, int BN_, int WM_, int WN_, int NS_, int KG_ = 1>
 struct Tile {
-  static constexpr int XF = XF_, YF = YF_, BM = BM_, BN = BN_, WM = WM_, WN = WN_, NS = NS_;
+  static constexpr int XF = XF_, YF = YF_, BM = BM_, BN = BN_, WM = WM_, WN = WN_, NS = NS_,
+                       KG = KG_;
   using T = TileShape<XF, BK_>;
-  static constexpr int waves = (BM / WM) * (BN / WN);
+  static constexpr int tile_waves = (BM / WM) * (BN / WN), waves = tile_waves * KG;
   static constexpr int threads = waves * kWave;
   static constexpr int xbytes = BM * T::XB, wbytes = BN * T::WB;
   static constexpr int stage = xbytes + wbytes;
@@ -372,12 +376,16 @@ struct Tile {
   static constexpr int swaves = (srows + kWave - 1) / kWave;
   static constexpr int ns = (swaves + waves - 1) / waves;
   static constexpr int scales = swaves * kWave * 16;
-  static constexpr int lds = NS * stage + 2 * scales;
+  // runs of scales held: the one in use and the next, or one a step
+  static constexpr int runs = T::steps_scales > 1 ? 2 : NS;
+  static constexpr int lds = NS * stage + runs * scales;
   static_assert(px % kWave == 0 && pw % kWave == 0, "whole waves load");
   static_assert(threads % px == 0 || px % threads == 0, "");
   static_assert(threads % pw == 0 || pw % threads == 0, "");
   static_assert(waves % swaves == 0 || swaves % waves == 0, "");
-  static_assert(NS - 1 <= T::steps_scales, "scales of two runs of steps at a time");
+  static_assert(NS - 1 <= T::steps_scales || T::steps_scales == 1, "scales of two runs of steps at a time");
+  static_assert(KG == 1 || KG == T::rounds, "a round for each group");
+  static_assert(KG == 1 || tile_waves * WM * WN * 4 * KG <= lds, "room to join the sums");
   static_assert((NS - 2) * (nx + nw) < 64, "loads on their way that a wait can name");
 };
 
@@ -390,7 +398,8 @@ __global__ __launch_bounds__(G::threads) void k_mx_linear_tiles(MxLinArgs a) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c = lane & 15, g = lane >> 4;
-  const int wi = wave % (BN / WN), wj = wave / (BN / WN);
+  const int kg = wave / G::tile_waves, tw = wave % G::tile_waves;
+  const int wi = tw % (BN / WN), wj = tw / (BN / WN);
 
   // Workgroups go round the 8 XCDs one by one; each XCD takes a run of tiles
   // that walks down strips of 8 tiles of outputs, so that the 32 tiles it
@@ -469,7 +478,7 @@ __global__ __launch_bounds__(G::threads) void k_mx_linear_tiles(MxLinArgs a) {
                   : a.xs + r * a.xs_rank + (m0 + min(row - BN, mlast)) * a.xs_stride;
   }
   auto load_scales = [&](int k) {
-    uint8_t* at = smem + NS * G::stage + (k / T::steps_scales & 1) * G::scales;
+    uint8_t* at = smem + NS * G::stage + k / T::steps_scales % G::runs * G::scales;
     const int blk = k * (T::BK / 32);
 #pragma unroll
     for (int i = 0; i < G::ns; ++i) {
@@ -499,7 +508,7 @@ __global__ __launch_bounds__(G::threads) void k_mx_linear_tiles(MxLinArgs a) {
     int s;
   };
   auto scales_at = [&](int k, int h) {
-    return smem + NS * G::stage + (k / T::steps_scales & 1) * G::scales + (k % T::steps_scales) * (T::BK / 32) +
+    return smem + NS * G::stage + k / T::steps_scales % G::runs * G::scales + (k % T::steps_scales) * (T::BK / 32) +
            h * (T::BI / 32);
   };
   auto read_tokens = [&](int k, int h, int buf, Tokens& f) {
@@ -559,7 +568,8 @@ __global__ __launch_bounds__(G::threads) void k_mx_linear_tiles(MxLinArgs a) {
   // memory and matrix instructions of one wave overlap
   auto compute = [&](int k, int buf) {
 #pragma unroll
-    for (int h = 0; h < T::rounds; ++h) {
+    for (int q = 0; q < T::rounds / G::KG; ++q) {
+      const int h = G::KG > 1 ? kg : q;
       Tokens x;
       Weights w[2];
       read_tokens(k, h, buf, x);
@@ -576,14 +586,15 @@ __global__ __launch_bounds__(G::threads) void k_mx_linear_tiles(MxLinArgs a) {
   // whole steps, then maybe one that K ends in
   const int full = (is_mx_format(XF) ? a.nb * 32 : a.K) / T::BK;
   const int steps = (a.nb * 32 + T::BK - 1) / T::BK;
-  if (steps > 0) load_scales(0);
 #pragma unroll
-  for (int k = 0; k < NS - 1; ++k)
+  for (int k = 0; k < NS - 1; ++k) {
+    if (k < steps && k % T::steps_scales == 0) load_scales(k);
     if (k < full) load_step(k, k);
+  }
   constexpr int behind = (NS - 2) * (G::nx + G::nw);
   constexpr int wait_behind = 0x0F70 | (behind & 15) | (behind >> 4) << 14;      // vmcnt alone
   int buf = 0;
-  if constexpr (G::waves == 8) {
+  if constexpr (G::tile_waves == 8) {
     // Two waves to a SIMD, half a step apart: while one reads its operands of
     // a step from shared memory, the other one multiplies, and they change
     // places at a barrier.  Waves 0..3 read step k in phase 2k and multiply in
@@ -648,6 +659,26 @@ __global__ __launch_bounds__(G::threads) void k_mx_linear_tiles(MxLinArgs a) {
     load_tail(full, buf);
     __syncthreads();
     compute(full, buf);
+  }
+  if constexpr (G::KG > 1) {
+    // the groups' sums, joined in order through shared memory by group 0
+    __syncthreads();
+    f32x4* part = reinterpret_cast<f32x4*>(smem) + (tw * TI * TJ) * kWave + lane;
+    constexpr int group = G::tile_waves * TI * TJ * kWave;
+    if (kg > 0) {
+#pragma unroll
+      for (int i = 0; i < TI; ++i)
+#pragma unroll
+        for (int j = 0; j < TJ; ++j) part[(kg - 1) * group + (i * TJ + j) * kWave] = acc[i][j];
+    }
+    __syncthreads();
+    if (kg > 0) return;
+#pragma unroll
+    for (int q = 1; q < G::KG; ++q)
+#pragma unroll
+      for (int i = 0; i < TI; ++i)
+#pragma unroll
+        for (int j = 0; j < TJ; ++j) acc[i][j] += part[(q - 1) * group + (i * TJ + j) * kWave];
   }
 #pragma unroll
   for (int j = 0; j < TJ; ++j) {
@@ -742,17 +773,33 @@ static hipError_t launch_tiles(const MxLinArgs& a0, int nranks, hipStream_t s) {
                 dim3(G::threads), s, a);
 }
 
+// Which kernel.  The largest tile that gives every CU (256) one; tiles of 32
+// tokens with K shared by 4 groups of waves where even those are not more than
+// the CUs.  Measured both ways, 8-bit tokens, in us:
+//   256 x 256 against 128 x 128 tiles: 2048 x 8192 x 8192 101 and 130, 1024 x
+//   8192 x 8192 102 (128 tiles) and 66;
+//   128 x 128 against 64 x 64: 4 x 128 x 8192 x 2048 17.5 and 19.4, 256 x 4096 x
+//   4096 24.3 (64 tiles) and 11.7;
+//   64 x 64 against 32 x 64 with 4 groups: 256 x 4096 x 4096 11.7 and 19.9, 64 x
+//   4096 x 4096 11.0 (64 tiles) and 10.0;
+//   32 x 64, one group against 4: 4 x 32 x 8192 x 2048 9.4 and 14, 32 x 8192 x
+//   8192 21.0 (128 tiles) and 16.3.
+// The tile kernels' offsets inside a tile are 31 bits: rows further apart take
+// the other kernel at any number of tokens.
 template <int XF, int YF>
 static hipError_t launch_linear(const MxLinArgs& a, int nranks, hipStream_t s) {
-  // the tile kernels' offsets inside a tile are 31 bits
   if (a.M > 16 && a.x_stride < (1 << 23) && a.w_stride < (1 << 23)) {
     constexpr int K1 = XF == AR_BF16 ? 64 : 128;
-    constexpr bool x4 = XF == AR_E2M1_MX;
-    const int64_t big = (int64_t)((a.N + 255) / 256) * ((a.M + 255) / 256) * nranks;
+    constexpr bool x4 = XF == AR_E2M1_MX;                  // small enough for steps of 256
+    auto tiles = [&](int bm, int bn) -> int64_t {
+      return (int64_t)((a.N + bn - 1) / bn) * ((a.M + bm - 1) / bm) * nranks;
+    };
+    if (tiles(256, 256) >= 256) return launch_tiles<Tile<XF, YF, K1, 256, 256, 64, 128, 3>>(a, nranks, s);
+    if (a.M > 64 && tiles(128, 128) >= 256)
+      return launch_tiles<Tile<XF, YF, x4 ? 256 : K1, 128, 128, 64, 64, x4 ? 2 : 3>>(a, nranks, s);
+    if (tiles(32, 64) <= 256) return launch_tiles<Tile<XF, YF, 4 * K1, 32, 64, 32, 16, 3, 4>>(a, nranks, s);
     if (a.M <= 32) return launch_tiles<Tile<XF, YF, K1, 32, 64, 32, 16, 5>>(a, nranks, s);
-    if (a.M <= 64) return launch_tiles<Tile<XF, YF, K1, 64, 64, 32, 32, 4>>(a, nranks, s);
-    if (big >= 256) return launch_tiles<Tile<XF, YF, K1, 256, 256, 64, 128, 3>>(a, nranks, s);
-    return launch_tiles<Tile<XF, YF, x4 ? 256 : K1, 128, 128, 64, 64, x4 ? 2 : 3>>(a, nranks, s);
+    return launch_tiles<Tile<XF, YF, 2 * K1, 64, 64, 32, 32, 3, 2>>(a, nranks, s);
   }
   const int64_t steps = (a.nb + 15) / 16, wide = (int64_t)((a.N + 31) / 32) * nranks;
   if (wide * (steps < 8 ? steps : 8) >= kRowsWaves) return launch_rows<XF, YF, 2>(a, nranks, s);

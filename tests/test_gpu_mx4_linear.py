@@ -74,8 +74,9 @@ def _run(ranks, m, n, k, xf, xd, wd, yf, y_stride=None, y_rank=None):
 SIZES = [(1, 1, 16, 32), (1, 1, 1, 1), (2, 3, 17, 33), (8, 1, 4096, 512), (1, 16, 64, 512), (1, 17, 100, 1000),
          (4, 5, 33, 544), (1, 33, 48, 2080), (2, 64, 80, 1536), (1, 65, 130, 640), (1, 200, 300, 1056),
          (2, 130, 520, 288), (1, 257, 260, 2048), (1, 300, 1030, 160),
-         # enough tokens and outputs for the largest tiles
-         (16, 300, 2000, 544), (16, 257, 2050, 96), (8, 700, 2500, 1100)]
+         # each of the tile kernels, by its number of tiles; K in whole steps and not
+         (16, 300, 2000, 544), (16, 257, 2050, 96), (8, 700, 2500, 1100), (16, 100, 2000, 1100),
+         (16, 20, 2000, 1100), (16, 32, 1100, 64), (16, 60, 2000, 300), (1, 40, 100, 3500), (3, 100, 200, 2560)]
 
 
 @pytest.mark.parametrize("yf", ("bf16", "f32"))
