@@ -776,14 +776,15 @@ static hipError_t launch_tiles(const MxLinArgs& a0, int nranks, hipStream_t s) {
 // Which kernel.  The largest tile that gives every CU (256) one; tiles of 32
 // tokens with K shared by 4 groups of waves where even those are not more than
 // the CUs.  Measured both ways, 8-bit tokens, in us:
-//   256 x 256 against 128 x 128 tiles: 2048 x 8192 x 8192 101 and 130, 1024 x
+//   256 x 256 against 128 x 128 tiles: 2048 x 8192 x 8192 108 and 131, 1024 x
 //   8192 x 8192 102 (128 tiles) and 66;
 //   128 x 128 against 64 x 64: 4 x 128 x 8192 x 2048 17.5 and 19.4, 256 x 4096 x
 //   4096 24.3 (64 tiles) and 11.7;
-//   64 x 64 against 32 x 64 with 4 groups: 256 x 4096 x 4096 11.7 and 19.9, 64 x
-//   4096 x 4096 11.0 (64 tiles) and 10.0;
-//   32 x 64, one group against 4: 4 x 32 x 8192 x 2048 9.4 and 14, 32 x 8192 x
-//   8192 21.0 (128 tiles) and 16.3.
+//   64 x 64 (2 groups) against 32 x 64 (4): 256 x 4096 x 4096 11.7 and 19.9, 64 x
+//   4096 x 4096 11.0 (64 tiles) and 10.0, 32 x 8192 x 8192 18.5 (128 tiles) and
+//   16.3;
+//   32 x 64 (1 group) against 64 x 64 (2): 8 x 32 x 4096 x 512 (bf16) 6.0 and
+//   7.9, 4 x 32 x 8192 x 2048 9.9 and 10.5.
 // The tile kernels' offsets inside a tile are 31 bits: rows further apart take
 // the other kernel at any number of tokens.
 template <int XF, int YF>
