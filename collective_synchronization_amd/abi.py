@@ -214,6 +214,17 @@ def _ptr(x) -> Optional[int]:
     return x.data_ptr()
 
 
+def _gpu_ptr(x, where: str) -> Optional[int]:
+    """_ptr for the layer operators: a tensor that is not on the current
+    device is refused, since its address would fault the GPU."""
+    if x is None or x.__class__ is int:
+        return x
+    d = x.get_device()
+    if d < 0 or d != torch._C._cuda_getDevice():
+        raise ArError(AR_EINVAL, f"{where}: a tensor on {x.device}, not on the current device")
+    return x.data_ptr()
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
         # what torch.cuda.current_stream().cuda_stream gives, without the
@@ -372,35 +383,39 @@ def norm_params(rows, hidden, eps, fmt, gamma, res_fmt, residual, residual_strid
                 scale_stride=0) -> ar_norm_params:
     """The norm of ar_residual_norm and ar_reduce_norm: formats by name or id
     (FORMATS); gamma, residual and residual_out may be None."""
-    return ar_norm_params(rows, hidden, eps, format_id(fmt), _ptr(gamma), format_id(res_fmt),
-                          format_id(y_fmt), _ptr(residual), residual_stride, _ptr(residual_out),
-                          residual_out_stride, _ptr(y), y_stride, _ptr(scales), scale_stride, 0)
+    w = "norm_params"
+    return ar_norm_params(rows, hidden, eps, format_id(fmt), _gpu_ptr(gamma, w),
+                          format_id(res_fmt), format_id(y_fmt), _gpu_ptr(residual, w),
+                          residual_stride, _gpu_ptr(residual_out, w), residual_out_stride,
+                          _gpu_ptr(y, w), y_stride, _gpu_ptr(scales, w), scale_stride, 0)
 
 
 def ar_residual_norm(params: ar_norm_params, x, x_stride, stream=None) -> None:
-    _check(_lib.ar_residual_norm(ctypes.byref(params), _ptr(x), x_stride, _stream(stream)),
-           "ar_residual_norm")
+    _check(_lib.ar_residual_norm(ctypes.byref(params), _gpu_ptr(x, "ar_residual_norm"), x_stride,
+                                 _stream(stream)), "ar_residual_norm")
 
 
 def ar_reduce_norm(desc, scratch, params: ar_norm_params, epoch, ctrl, timeout_ns: int = 0,
                    flags: int = 0, stream=None) -> None:
-    _check(_lib.ar_reduce_norm(ctypes.byref(desc), _ptr(scratch), ctypes.byref(params), epoch,
-                               _ptr(ctrl), timeout_ns, flags, _stream(stream)),
-           "ar_reduce_norm")
+    w = "ar_reduce_norm"
+    _check(_lib.ar_reduce_norm(ctypes.byref(desc), _gpu_ptr(scratch, w), ctypes.byref(params),
+                               epoch, _gpu_ptr(ctrl, w), timeout_ns, flags, _stream(stream)), w)
 
 
 def ar_quantize_mx(rows, cols, in_fmt, inp, in_stride, out_fmt, codes, codes_stride, scales,
                    scale_stride, stream=None) -> None:
-    _check(_lib.ar_quantize_mx(rows, cols, format_id(in_fmt), _ptr(inp), in_stride,
-                               format_id(out_fmt), _ptr(codes), codes_stride, _ptr(scales),
-                               scale_stride, _stream(stream)), "ar_quantize_mx")
+    w = "ar_quantize_mx"
+    _check(_lib.ar_quantize_mx(rows, cols, format_id(in_fmt), _gpu_ptr(inp, w), in_stride,
+                               format_id(out_fmt), _gpu_ptr(codes, w), codes_stride,
+                               _gpu_ptr(scales, w), scale_stride, _stream(stream)), w)
 
 
 def ar_dequantize_mx(rows, cols, in_fmt, codes, codes_stride, scales, scale_stride, out_fmt,
                      out, out_stride, stream=None) -> None:
-    _check(_lib.ar_dequantize_mx(rows, cols, format_id(in_fmt), _ptr(codes), codes_stride,
-                                 _ptr(scales), scale_stride, format_id(out_fmt), _ptr(out),
-                                 out_stride, _stream(stream)), "ar_dequantize_mx")
+    w = "ar_dequantize_mx"
+    _check(_lib.ar_dequantize_mx(rows, cols, format_id(in_fmt), _gpu_ptr(codes, w), codes_stride,
+                                 _gpu_ptr(scales, w), scale_stride, format_id(out_fmt),
+                                 _gpu_ptr(out, w), out_stride, _stream(stream)), w)
 
 
 def linear_params(nranks, rows, outputs, inputs, x_fmt, x, x_stride, x_rank_stride, x_scales,
@@ -409,11 +424,12 @@ def linear_params(nranks, rows, outputs, inputs, x_fmt, x, x_stride, x_rank_stri
                   y_rank_stride) -> ar_linear_params:
     """One ar_mx4_linear: y_r [rows, outputs] = x_r [rows, inputs] times the
     transpose of w_r [outputs, inputs] for every rank."""
+    f = "linear_params"
     return ar_linear_params(nranks, 0, rows, outputs, inputs, format_id(x_fmt), format_id(y_fmt),
-                            _ptr(x), x_stride, x_rank_stride, _ptr(x_scales), x_scale_stride,
-                            x_scale_rank_stride, _ptr(w), w_stride, w_rank_stride,
-                            _ptr(w_scales), w_scale_stride, w_scale_rank_stride, _ptr(y),
-                            y_stride, y_rank_stride)
+                            _gpu_ptr(x, f), x_stride, x_rank_stride, _gpu_ptr(x_scales, f),
+                            x_scale_stride, x_scale_rank_stride, _gpu_ptr(w, f), w_stride,
+                            w_rank_stride, _gpu_ptr(w_scales, f), w_scale_stride,
+                            w_scale_rank_stride, _gpu_ptr(y, f), y_stride, y_rank_stride)
 
 
 def ar_mx4_linear(params: ar_linear_params, stream=None) -> None:

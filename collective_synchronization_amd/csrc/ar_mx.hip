@@ -89,8 +89,8 @@ __global__ __launch_bounds__(kBlock) void k_dequantize_mx(MxArgs a) {
   float v[8];
   values8<Q>(static_cast<const uint8_t*>(a.codes) + (int64_t)row * a.codes_stride,
              a.scales + (int64_t)row * a.scale_stride, c, v);
-  store8<F, true>(static_cast<typename Elem<F>::type*>(a.out) + (int64_t)row * a.out_stride, a.cols,
-                  (int64_t)c * 8, v);
+  store8<F>(static_cast<typename Elem<F>::type*>(a.out) + (int64_t)row * a.out_stride, a.cols,
+            (int64_t)c * 8, v);
 }
 
 static int mx_check(int64_t rows, int64_t cols, int32_t f, const void* p, int64_t stride, int32_t q,

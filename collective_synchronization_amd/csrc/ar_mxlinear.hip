@@ -61,14 +61,26 @@ __device__ __forceinline__ u32x4 load_scales16(const uint8_t* row, int b, int nb
   return v;
 }
 
-// The first `keep` bytes of 16, zeros after them.
-__device__ __forceinline__ u32x4 keep_bytes(u32x4 v, int keep) {
+// The first `keep` bits of 128, zeros after them.
+__device__ __forceinline__ u32x4 keep_bits(u32x4 v, int64_t keep) {
 #pragma unroll
   for (int d = 0; d < 4; ++d) {
-    const int k = keep - 4 * d;
-    v[d] &= k >= 4 ? 0xFFFFFFFFu : (k <= 0 ? 0u : (1u << (8 * k)) - 1u);
+    const int64_t k = keep - 32 * d;
+    v[d] &= k >= 32 ? 0xFFFFFFFFu : (k <= 0 ? 0u : (1u << k) - 1u);
   }
   return v;
+}
+
+// Bits of one element of an input row.
+template <int XF>
+constexpr int elem_bits() { return XF == AR_BF16 ? 16 : (XF == AR_E2M1_MX ? 4 : 8); }
+
+// 16 bytes of an input row from element `at` on, zeros at and past element K:
+// what lies there in x does not count, and then neither does what lies there in
+// w, whose values are finite.
+template <int XF>
+__device__ __forceinline__ u32x4 load_x_tail(const uint8_t* p, int64_t at, int64_t K) {
+  return at < K ? keep_bits(ldg16(p), (K - at) * elem_bits<XF>()) : u32x4{0u, 0u, 0u, 0u};
 }
 
 // One lane's operands of a 512-element step: 4 blocks of K, one in each of 4
@@ -111,21 +123,19 @@ __device__ __forceinline__ void load_x(const uint8_t* row, const uint8_t* srow, 
   for (int s = 0; s < 4; ++s) {
     const int b = 16 * step + 4 * s + g;
     if constexpr (XF == AR_E2M1_MX) {
-      f.d[s] = !TAIL || b < nb ? ldg16(row + (int64_t)b * 16) : u32x4{0u, 0u, 0u, 0u};
+      const uint8_t* p = row + (int64_t)b * 16;
+      f.d[s] = TAIL ? load_x_tail<XF>(p, (int64_t)b * 32, K) : ldg16(p);
     } else if constexpr (XF == AR_BF16) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int at = b * 32 + 8 * j;                     // element
-        if (!TAIL) f.d[s][j] = ldg16(row + (int64_t)at * 2);
-        else f.d[s][j] = at < K ? keep_bytes(ldg16(row + (int64_t)at * 2), 2 * (K - at)) : u32x4{0u, 0u, 0u, 0u};
+        const int64_t at = (int64_t)b * 32 + 8 * j;
+        f.d[s][j] = TAIL ? load_x_tail<XF>(row + at * 2, at, K) : ldg16(row + at * 2);
       }
     } else {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int at = (16 * step + 4 * s) * 32 + 64 * h + 16 * g;
-        const int end = XF == AR_E4M3_MX ? nb * 32 : K;
-        if (!TAIL) f.d[s][h] = ldg16(row + at);
-        else f.d[s][h] = at < end ? keep_bytes(ldg16(row + at), end - at) : u32x4{0u, 0u, 0u, 0u};
+        const int64_t at = (int64_t)(16 * step + 4 * s) * 32 + 64 * h + 16 * g;
+        f.d[s][h] = TAIL ? load_x_tail<XF>(row + at, at, K) : ldg16(row + at);
       }
     }
   }
@@ -253,8 +263,8 @@ __global__ __launch_bounds__(kWave * WN * WK) void k_mx_linear_rows(MxLinArgs a)
 #pragma unroll
       for (int j = 0; j < MT; ++j) acc[i][j] = multiply<XF, 3>(f.w[i], f.x[j], shift, acc[i][j]);
   };
-  // steps that hold whole blocks only, then maybe one that K ends in
-  const int full = (is_mx_format(XF) ? a.nb : a.K / 32) / 16;
+  // whole steps, then maybe one that K ends in
+  const int full = a.K / 512;
   const int steps = (a.nb + 15) / 16;
   int st = wk;
   if (st < full) {
@@ -452,11 +462,9 @@ __global__ __launch_bounds__(G::threads) void k_mx_linear_tiles(MxLinArgs a) {
 #pragma unroll
     for (int i = 0; i < G::nx; ++i) {
       const int slot = (i * G::threads + tid) % G::px, row = slot / T::XC;
-      const int first = k * T::XB + place<T::XC>(row, slot % T::XC) * 16;       // byte of the row
-      const int end = XF == AR_BF16 ? 2 * a.K : (XF == AR_E4M3_ROW ? a.K : a.nb * (XF == AR_E2M1_MX ? 16 : 32));
-      u32x4 v = u32x4{0u, 0u, 0u, 0u};
-      if (first < end) v = keep_bytes(ldg16(xbase + xo[i] + k * T::XB), end - first);
-      *reinterpret_cast<u32x4*>(at + slot * 16) = v;
+      const int64_t first = (int64_t)k * T::XB + place<T::XC>(row, slot % T::XC) * 16;  // byte of the row
+      *reinterpret_cast<u32x4*>(at + slot * 16) =
+          load_x_tail<XF>(xbase + xo[i] + k * T::XB, first * 8 / elem_bits<XF>(), a.K);
     }
 #pragma unroll
     for (int i = 0; i < G::nw; ++i) {
@@ -584,7 +592,7 @@ __global__ __launch_bounds__(G::threads) void k_mx_linear_tiles(MxLinArgs a) {
   };
 
   // whole steps, then maybe one that K ends in
-  const int full = (is_mx_format(XF) ? a.nb * 32 : a.K) / T::BK;
+  const int full = a.K / T::BK;
   const int steps = (a.nb * 32 + T::BK - 1) / T::BK;
 #pragma unroll
   for (int k = 0; k < NS - 1; ++k) {
@@ -823,8 +831,8 @@ int ar_mx4_linear(const ar_linear_params* p, void* stream) {
   const int rc = check_linear(p);
   if (rc) return rc;
   if (p->rows == 0 || p->outputs == 0) return AR_OK;
-  // workgroups of the kernel with the smallest tiles (64 outputs or 16, 64 tokens or all)
-  const int64_t tiles = ceil_div64(p->outputs, 16) * ceil_div64(p->rows, 64) * p->nranks;
+  // workgroups of the kernel with the smallest tiles
+  const int64_t tiles = ceil_div64(p->outputs, 16) * ceil_div64(p->rows, 16) * p->nranks;
   if (tiles > INT32_MAX) return AR_ESIZE;
   MxLinArgs a{};
   const int64_t xe = p->x_format == AR_BF16 ? 2 : 1;

@@ -97,17 +97,17 @@ __device__ __forceinline__ void values(const Raw<F>& r, int64_t count, int64_t f
   }
 }
 
-// NT: past the caches, for a kernel that only writes what it reads many times
-// over.  8192 x 8192 from 4 bits to bf16: 27.8 us against 39.1 with ordinary
-// stores; the norm's rows gain nothing (1000 x 4100: 7.8 us against 7.0).
-template <bool NT, typename V>
-__device__ __forceinline__ void store_vec(void* p, V v) {
-  if constexpr (NT) __builtin_nontemporal_store(v, reinterpret_cast<V*>(p));
-  else *reinterpret_cast<V*>(p) = v;
+// Float rows go past the caches: the next kernel reads them on any XCD, and the
+// lines that they would displace are inputs still to be read.  8192 x 8192 from
+// 4 bits to bf16: 27.8 us against 39.1 with ordinary stores; the norm of 16384 x
+// 8192 to bf16 180 against 185, of 1000 x 4100 fp16 7.8 against 8.4.
+template <typename V>
+__device__ __forceinline__ void store_nt(void* p, V v) {
+  __builtin_nontemporal_store(v, reinterpret_cast<V*>(p));
 }
 
 // One rounding to the row's type, nearest even.
-template <int F, bool NT = false>
+template <int F>
 __device__ __forceinline__ void store8(typename Elem<F>::type* __restrict__ row, int64_t count,
                                        int64_t first, const float (&v)[8]) {
   if (first + 8 <= count) {
@@ -115,15 +115,15 @@ __device__ __forceinline__ void store8(typename Elem<F>::type* __restrict__ row,
       u32x4 d;
       d.x = pack2(to_bf16(v[0]), to_bf16(v[1])); d.y = pack2(to_bf16(v[2]), to_bf16(v[3]));
       d.z = pack2(to_bf16(v[4]), to_bf16(v[5])); d.w = pack2(to_bf16(v[6]), to_bf16(v[7]));
-      store_vec<NT>(row + first, d);
+      store_nt(row + first, d);
     } else if constexpr (F == AR_F16) {
       f16x8 d;
 #pragma unroll
       for (int k = 0; k < 8; ++k) d[k] = (_Float16)v[k];
-      store_vec<NT>(row + first, d);
+      store_nt(row + first, d);
     } else {
-      store_vec<NT>(row + first, f32x4{v[0], v[1], v[2], v[3]});
-      store_vec<NT>(row + first + 4, f32x4{v[4], v[5], v[6], v[7]});
+      store_nt(row + first, f32x4{v[0], v[1], v[2], v[3]});
+      store_nt(row + first + 4, f32x4{v[4], v[5], v[6], v[7]});
     }
   } else {
 #pragma unroll

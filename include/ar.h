@@ -435,8 +435,8 @@ int ar_reduce_norm(const ar_desc* d, void* scratch, const ar_norm_params* p, ar_
  * ar_quantize_mx -- rows of AR_BF16, AR_F16 or AR_F32 to AR_E4M3_MX or
  * AR_E2M1_MX.  ar_dequantize_mx -- the values of such rows, rounded once to
  * out_format (exact in AR_F32 and AR_BF16 but for results outside their
- * range).  rows or cols 0: nothing is written.  AR_ESIZE: rows of more than
- * 2^31 - 1 8-element chunks in all.
+ * range).  Outputs may not overlap inputs.  rows or cols 0: nothing is
+ * written.  AR_ESIZE: more than 2^31 - 1 8-element chunks in all.
  */
 int ar_quantize_mx(int64_t rows, int64_t cols, int32_t in_format, const void* in,
                    int64_t in_stride, int32_t out_format, void* codes, int64_t codes_stride,
@@ -476,7 +476,9 @@ typedef struct {
  * and with the same alignment, 0 where the ranks share a tensor.  x of all
  * ranks may be slices of one row (x_rank_stride = inputs).  y: any stride
  * that holds a row, aligned to its element; it may not overlap the inputs,
- * nor the ranks' y each other.  A scale NaN makes its products NaN.  inputs 0:
+ * nor the ranks' y each other.  A scale NaN makes its products NaN; what lies
+ * past `inputs` in rows of x and w does not count.  The order of every sum is
+ * fixed by the sizes, so equal calls give equal bits.  inputs 0:
  * zeros are written; rows or outputs 0: nothing is.  AR_ESIZE: a size above
  * 2^30.
  */

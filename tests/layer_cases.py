@@ -30,11 +30,14 @@ def float_rows(v, fmt, extra=0, device="cuda"):
 
 def code_rows(codes, scales, fmt, cols, extra=0, device="cuda"):
     """8- or 4-bit rows on the device from element codes (one a byte, whole
-    blocks for the MX formats); what lies past codes and scales is 0xFF."""
+    blocks for the MX formats); what lies past the row's last element, in its
+    last block and after it, and past the scales is the worst there is."""
     rows = codes.shape[0]
     r = buffers.FormatRows(rows, cols, fmt, device)
     r.stride += 16 * extra
     host = np.full((rows, r.stride), 0xFF, dtype=np.uint8)
+    codes = codes.copy()
+    codes[:, cols:] = 15 if fmt == "mx4" else 0x7F     # -6, or NaN: nobody may use them
     packed = layer.pack4(codes) if fmt == "mx4" else codes
     host[:, :packed.shape[1]] = packed
     r.data = torch.from_numpy(host).to(device)

@@ -118,6 +118,20 @@ def test_norm_of_zeros_and_extremes(y_fmt):
         assert np.isnan(sc).all() if y_fmt == "row8" else (sc == 255).all()
 
 
+def test_norm_in_place_and_many_rows():
+    """y over x, residual_out over the residual; more rows than 2^16."""
+    rng = np.random.default_rng(6)
+    rows, cols = 70001, 40
+    x, res = _rows(rng, rows, cols, "bf16"), _rows(rng, rows, cols, "bf16")
+    xd, rd = float_rows(x, "bf16"), float_rows(res, "bf16")
+    p = abi.norm_params(rows, cols, 1e-5, "bf16", None, "bf16", rd.data, rd.stride, rd.data, rd.stride,
+                        "bf16", xd.data, xd.stride)
+    abi.ar_residual_norm(p, xd.data, xd.stride)
+    torch.cuda.synchronize()
+    check_float(rd.data[:, :cols].double().cpu().numpy(), x + res, "bf16", 2.0 ** -24)
+    check_float(xd.data[:, :cols].double().cpu().numpy(), layer.norm(x + res, None, 1e-5), "bf16", REL)
+
+
 def test_norm_rows_past_32_bits():
     """Rows whose offsets pass 2^32 bytes."""
     cols, stride, rows = 64, 1 << 20, 2100

@@ -179,6 +179,42 @@ def test_ranks_take_slices_of_one_row():
     assert np.array_equal(y.double().cpu().numpy(), want)
 
 
+def test_rows_far_apart():
+    """Row strides of 8 MiB, at any number of tokens."""
+    m, n, k, far = 40, 70, 600, 1 << 23
+    rng = np.random.default_rng(11)
+    wv, wd = _dyadic(rng, n, k, "mx4")
+    xv, xn = _dyadic(rng, m, k, "row8")
+    x = torch.zeros((m, far), dtype=torch.uint8, device="cuda")
+    x[:, :k] = xn.data[:, :k]
+    y = torch.zeros((m, n), device="cuda")
+    p = abi.linear_params(1, m, n, k, "row8", x, far, 0, xn.scales, 0, 0, wd.data, wd.stride, 0, wd.scales,
+                          wd.scale_stride, 0, "f32", y, n, 0)
+    abi.ar_mx4_linear(p)
+    torch.cuda.synchronize()
+    assert np.array_equal(y.double().cpu().numpy(), xv @ wv.T)
+
+
+def test_two_streams_at_once():
+    """Calls on two streams, tiles of different kernels, beside each other."""
+    rng = np.random.default_rng(12)
+    cases = []
+    for m, n, k in ((1, 4096, 1024), (200, 2000, 1100)):
+        xv, xd = _dyadic(rng, m, k, "mx8")
+        wv, wd = _dyadic(rng, n, k, "mx4")
+        y = torch.zeros((m, n), device="cuda")
+        p = abi.linear_params(1, m, n, k, "mx8", xd.data, xd.stride, 0, xd.scales, xd.scale_stride, 0,
+                              wd.data, wd.stride, 0, wd.scales, wd.scale_stride, 0, "f32", y, n, 0)
+        cases.append((p, y, xv @ wv.T, (xd, wd), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for p, _, _, _, s in cases:
+            abi.ar_mx4_linear(p, stream=s)
+    torch.cuda.synchronize()
+    for _, y, want, _, _ in cases:
+        assert np.array_equal(y.double().cpu().numpy(), want)
+
+
 @pytest.mark.parametrize("m", (1, 90))
 def test_same_bits_every_time_and_in_a_graph(m):
     rng = np.random.default_rng(4)

@@ -161,6 +161,22 @@ def test_linear_refuses_null_and_reserved():
     assert _code(abi.ar_mx4_linear, _linear(outputs=0, w=None, y=None)) == 0
 
 
+def test_tensors_not_on_the_gpu_are_refused():
+    """Their addresses would fault it."""
+    t = torch.zeros((2, 64), dtype=torch.bfloat16)
+    for make in (lambda: _norm(y=t), lambda: _norm(gamma=t), lambda: _norm(residual=t),
+                 lambda: _norm(residual_out=t), lambda: _norm(scales=t), lambda: _linear(x=t),
+                 lambda: _linear(w_scales=t), lambda: _linear(y=t),
+                 lambda: abi.ar_residual_norm(_norm(), t, 64, stream=0),
+                 lambda: abi.ar_quantize_mx(2, 64, "bf16", t, 64, "mx8", A, 64, A, 4, stream=0),
+                 lambda: abi.ar_dequantize_mx(2, 64, "mx8", A, 64, A, 4, "bf16", t, 64, stream=0),
+                 lambda: abi.ar_reduce_norm(abi.make_desc(4, 128, "ll"), t, _norm(), abi.ar_epoch_init(), A,
+                                            stream=0)):
+        with pytest.raises(abi.ArError) as e:
+            make()
+        assert e.value.code == abi.AR_EINVAL
+
+
 # ------------------------------------------------ the 64-bit forms' tables --
 
 def test_e4m3_table_is_torch_s():
