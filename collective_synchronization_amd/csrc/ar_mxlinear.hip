@@ -187,8 +187,7 @@ __device__ __forceinline__ void store_out4(void* y, int64_t at, int n, int N, bo
   typename Elem<YF>::type* p = static_cast<typename Elem<YF>::type*>(y) + at;
   if (vec && n + 4 <= N) {
     if constexpr (YF == AR_BF16) {
-      *reinterpret_cast<u32x2*>(p) =
-          u32x2{pack2(to_bf16(v[0]), to_bf16(v[1])), pack2(to_bf16(v[2]), to_bf16(v[3]))};
+      *reinterpret_cast<u32x2*>(p) = u32x2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
     } else {
       *reinterpret_cast<f32x4*>(p) = v;
     }

@@ -4,12 +4,14 @@
 //     h = residual + x,  r = 1 / sqrt(sum(h^2) / hidden + eps),
 //     v = (h * r) * gamma;  residual_out = round(h);  y = v in y's format.
 //
-// Everything between the inputs and the two outputs is binary32: h is not
-// rounded before the norm, and each output is rounded once.
+// h is binary32 and not rounded before the norm, the sum is binary64, and each
+// output is rounded once.
 //
 // What bounds it: for many rows the memory system (x and the residual read
 // once, both outputs written once; a row stays in registers between the sum
-// and the scaling), for few rows the launch and one trip to memory.  One
+// and the scaling): 16384 x 8192, bf16, to 8-bit blocks 162 us, 5.8 TB/s, to
+// bf16 180 us, 6.0 TB/s, where a plain copy reaches 5.1.  For few rows the launch
+// and one trip to memory: one row of 4096 3.0 us.  One
 // workgroup a row: 8 consecutive elements a thread and step, so a wave reads
 // 1 KiB of a 16-bit row in one instruction, and the 4 lanes of an aligned
 // group hold one 32-element block of the MX formats.
@@ -24,9 +26,8 @@
 
 namespace ar {
 
-// Threads a row at most: 16384 rows of 8192, bf16 to 8-bit blocks, take 164 us
-// (5.74 TB/s) with 512 threads and 2 chunks each, 179 with 1024 and 1, 173
-// with 256 and 4.
+// Threads a row at most: 16384 rows of 8192, bf16 to 8-bit blocks, took 164 us
+// with 512 threads and 2 chunks each, 179 with 1024 and 1, 173 with 256 and 4.
 constexpr int kNormThreads = 512;
 constexpr int kNormChunks = 8;       // chunks a thread at most
 static_assert(kNormThreads * kNormChunks * 8 == AR_NORM_MAX_HIDDEN, "the longest row");
@@ -45,13 +46,13 @@ struct NormArgs {
   int64_t scale_stride;
   int64_t hidden;
   float eps;
-  float inv_hidden;
+  double inv_hidden;
 };
 
 // The waves' partial sums or maxima; a second array so that the maximum's
 // writes need not wait for the sum's readers.
 struct NormShared {
-  float sum[kNormThreads / kWave];
+  double sum[kNormThreads / kWave];
   uint32_t max[kNormThreads / kWave];
 };
 
@@ -76,12 +77,63 @@ struct Gamma {
     }
   }
   __device__ __forceinline__ void get(const NormArgs& a, int i, float (&g)[8]) const {
-    if constexpr (gamma_first(NI)) values<FX>(raw[i], a.hidden, chunk_first(i), g);
-    else values<FX>(load_raw<FX>(row, chunk_first(i)), a.hidden, chunk_first(i), g);
+    if (!a.gamma) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) g[k] = a.gamma ? g[k] : 1.0f;
+      for (int k = 0; k < 8; ++k) g[k] = 1.0f;
+    } else if constexpr (gamma_first(NI)) {
+      values<FX>(raw[i], a.hidden, chunk_first(i), g);
+    } else {
+      values<FX>(load_raw<FX>(row, chunk_first(i)), a.hidden, chunk_first(i), g);
+    }
   }
 };
+
+// 1 / sqrt(x): the binary32 result and one Newton step in binary64.  Infinite
+// and NaN results of the first, and x beyond binary32's range, pass through.
+__device__ __forceinline__ double reciprocal_root(double x) {
+  const double r = (double)(1.0f / __builtin_sqrtf((float)x));
+  const double t = __builtin_fma(-x * r, r, 1.0);
+  return (float)x < 3.0e38f && (float)x > 1.2e-38f ? __builtin_fma(0.5 * r, t, r) : r;
+}
+
+// a * (r_hi + r_lo) * b with the products' rounding errors carried along and
+// added at the end: one rounding in effect.  ODD: towards zero with the last
+// bit set where that is not exact.  Infinite and NaN products end as NaN.
+template <bool ODD>
+__device__ __forceinline__ float product3(float a, float r_hi, float r_lo, float b) {
+  const float p = a * r_hi;
+  const float e = __builtin_fmaf(a, r_lo, __builtin_fmaf(a, r_hi, -p));
+  const float q = p * b;
+  const float c = __builtin_fmaf(e, b, __builtin_fmaf(p, b, -q));
+  const float t = q + c;
+  if constexpr (!ODD) return t;
+  const float d = c - (t - q);                             // what t lacks
+  uint32_t u = __float_as_uint(t);
+  if (d * t < 0.0f) --u;
+  if (d != 0.0f) u |= 1u;
+  return __uint_as_float(u);
+}
+
+// Values for an 8- or 4-bit format.  One that lies just beside a border between
+// two codes and rounds to the border itself would then round the wrong way:
+// borders have at least 19 trailing zeros, and a chunk with such a value is
+// taken again with ODD.
+template <int FY>
+__device__ __forceinline__ void products8(float (&h)[8], float r_hi, float r_lo, const float (&g)[8]) {
+  float v[8];
+  uint32_t least = 0xFFFFFFFFu;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    v[k] = product3<false>(h[k], r_hi, r_lo, g[k]);
+    least = min(least, __float_as_uint(v[k]) & 0x7FFFFu);
+  }
+  if (is_mx_format(FY) && least == 0u) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = product3<true>(h[k], r_hi, r_lo, g[k]);
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k) h[k] = v[k];
+}
 
 // From the row's h in registers (chunk i of thread t: elements
 // [8 * (i * threads + t), ...)) to both outputs.
@@ -103,11 +155,16 @@ __device__ __forceinline__ void norm_finish(const NormArgs& a, int64_t row, floa
       if (c < chunks) store8<FR>(hr, H, (int64_t)c * 8, h[i]);
     }
   }
-  float s = 0.0f;
+  // The sum and r are binary64, and 8- and 4-bit outputs round products that are
+  // right to the last bit of binary32: with binary32 steps throughout, a few of
+  // 4 million codes came out a step off.  (Products in binary64 give the same
+  // codes but take 188 us for 16384 x 8192 instead of 162: about 45
+  // instructions an element are what the vector units do in the memory's time.)
+  double s = 0.0;
 #pragma unroll
   for (int i = 0; i < NI; ++i)
 #pragma unroll
-    for (int k = 0; k < 8; ++k) s = __builtin_fmaf(h[i][k], h[i][k], s);
+    for (int k = 0; k < 8; ++k) s = __builtin_fma((double)h[i][k], (double)h[i][k], s);
 #pragma unroll
   for (int m = 1; m < kWave; m <<= 1) s += __shfl_xor(s, m, kWave);
   if (waves > 1) {
@@ -116,15 +173,20 @@ __device__ __forceinline__ void norm_finish(const NormArgs& a, int64_t row, floa
     s = sm.sum[0];
     for (int w = 1; w < waves; ++w) s += sm.sum[w];
   }
-  const float r = 1.0f / __builtin_sqrtf(s * a.inv_hidden + a.eps);
+  const double r = reciprocal_root(s * a.inv_hidden + (double)a.eps);
+  const float r_hi = (float)r, r_lo = (float)(r - (double)r_hi);
 
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
     const int c = i * threads + t;
     float g[8];
     gamma.get(a, i, g);
+    if constexpr (is_float_format(FY)) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) h[i][k] = (h[i][k] * r) * g[k];
+      for (int k = 0; k < 8; ++k) h[i][k] = (h[i][k] * r_hi) * g[k];
+    } else {
+      products8<FY>(h[i], r_hi, r_lo, g);
+    }
     // a row whose r is not finite makes NaN of the zeros past its end
     if ((int64_t)c * 8 + 8 > H) {
 #pragma unroll
@@ -475,7 +537,7 @@ static NormArgs norm_args(const ar_norm_params* p) {
   a.scale_stride = p->scale_stride;
   a.hidden = p->hidden;
   a.eps = p->eps;
-  a.inv_hidden = 1.0f / (float)p->hidden;
+  a.inv_hidden = 1.0 / (double)p->hidden;
   return a;
 }
 

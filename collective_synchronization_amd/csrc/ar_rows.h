@@ -29,9 +29,16 @@ template <> struct Elem<AR_BF16> { typedef uint16_t type; };
 template <> struct Elem<AR_F16> { typedef _Float16 type; };
 template <> struct Elem<AR_F32> { typedef float type; };
 
+// Two bf16, nearest even, by the conversion instruction (NaNs stay quiet NaNs).
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
+}
+
 template <int F>
 __device__ __forceinline__ typename Elem<F>::type elem_from_f32(float v) {
-  if constexpr (F == AR_BF16) return (uint16_t)to_bf16(v);
+  if constexpr (F == AR_BF16) return (uint16_t)bf16_pair(v, 0.0f);
   else if constexpr (F == AR_F16) return (_Float16)v;
   else return v;
 }
@@ -112,10 +119,8 @@ __device__ __forceinline__ void store8(typename Elem<F>::type* __restrict__ row,
                                        int64_t first, const float (&v)[8]) {
   if (first + 8 <= count) {
     if constexpr (F == AR_BF16) {
-      u32x4 d;
-      d.x = pack2(to_bf16(v[0]), to_bf16(v[1])); d.y = pack2(to_bf16(v[2]), to_bf16(v[3]));
-      d.z = pack2(to_bf16(v[4]), to_bf16(v[5])); d.w = pack2(to_bf16(v[6]), to_bf16(v[7]));
-      store_nt(row + first, d);
+      store_nt(row + first, u32x4{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]),
+                                  bf16_pair(v[6], v[7])});
     } else if constexpr (F == AR_F16) {
       f16x8 d;
 #pragma unroll

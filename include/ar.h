@@ -405,7 +405,8 @@ typedef struct {
 /*
  * ar_residual_norm -- for every row
  *     h = residual + x,  r = 1/sqrt(sum(h^2)/hidden + eps),  v = (h*r)*gamma
- * in binary32; residual_out = h and y = v, each rounded once to its format.
+ * with h in binary32 and the sum in binary64; residual_out = h and y = v, each
+ * rounded once to its format.
  * x: device, rows at x + i*x_stride elements.  y and residual_out may be x
  * where formats and strides agree; other overlaps are not allowed.  The
  * order of the sum is fixed by the shape, so equal calls give equal bits.

@@ -3,12 +3,13 @@
 
 Tolerances, derived from the arithmetic:
 * quantisation and its inverse round once from exact inputs: equal bits;
-* the norm: h is one binary32 addition (2^-24 of h); the sum of squares has
-  only positive terms, so its relative error is at most the longest chain of
-  additions (64 in a thread, 6 levels of lanes, 16 waves) plus the squares'
-  own, 90 steps of 2^-24, halved by the square root; the division by hidden,
-  eps, root, reciprocal and the two products add 6 more: at most
-  51 + 2 <= 64 steps of 2^-24 in all, then the output's own rounding.
+* the norm: h is one binary32 addition (2^-24 of h).  The sum of squares has
+  only positive terms and its relative error is at most the longest chain of
+  additions (64 in a thread, 6 levels of lanes, 16 waves) plus the squares' own,
+  90 steps, halved by the square root; the division by hidden, eps, root,
+  reciprocal and the two products add 6 more.  With every one of them a
+  binary32 step, the worst that is allowed, that is at most 51 + 2 <= 64 steps of
+  2^-24; then the output's own rounding.
 """
 import numpy as np
 import pytest
