@@ -42,21 +42,25 @@ struct MxLinArgs {
 
 __device__ __forceinline__ u32x4 ldg16(const uint8_t* p) { return *reinterpret_cast<const u32x4*>(p); }
 
-// Scales of blocks b .. b+15 of a row, with every block at or past `nb` set to
-// 1 (its codes are zeros; what lies past a row's scales may be anything).
+// Scales of blocks b .. b+15 of a row of `nb`; TAIL: the row's last dword in the
+// place of those past its end.
 template <bool TAIL>
 __device__ __forceinline__ u32x4 load_scales16(const uint8_t* row, int b, int nb) {
-  const uint32_t* p = reinterpret_cast<const uint32_t*>(row + b);
+  const uint32_t* p = reinterpret_cast<const uint32_t*>(row);
   u32x4 v;
 #pragma unroll
+  for (int q = 0; q < 4; ++q) v[q] = p[TAIL ? min(b / 4 + q, (nb - 1) / 4) : b / 4 + q];
+  return v;
+}
+
+// ... with the scale 1 for every block past the end: what lies there may be
+// anything, a NaN too.
+__device__ __forceinline__ u32x4 keep_scales(u32x4 v, int b, int nb) {
+#pragma unroll
   for (int q = 0; q < 4; ++q) {
-    if (!TAIL) {
-      v[q] = p[q];
-      continue;
-    }
     const int n = nb - b - 4 * q;
     const uint32_t keep = n >= 4 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << (8 * n)) - 1u);
-    v[q] = ((n > 0 ? p[q] : 0u) & keep) | (0x7F7F7F7Fu & ~keep);
+    v[q] = (v[q] & keep) | (0x7F7F7F7Fu & ~keep);
   }
   return v;
 }
@@ -75,12 +79,12 @@ __device__ __forceinline__ u32x4 keep_bits(u32x4 v, int64_t keep) {
 template <int XF>
 constexpr int elem_bits() { return XF == AR_BF16 ? 16 : (XF == AR_E2M1_MX ? 4 : 8); }
 
-// 16 bytes of an input row from element `at` on, zeros at and past element K:
-// what lies there in x does not count, and then neither does what lies there in
-// w, whose values are finite.
+// 16 bytes of an input row from element `at` on, with zeros at and past element
+// K: what lies there in x does not count, and then neither does what lies there
+// in w, whose values are finite.
 template <int XF>
-__device__ __forceinline__ u32x4 load_x_tail(const uint8_t* p, int64_t at, int64_t K) {
-  return at < K ? keep_bits(ldg16(p), (K - at) * elem_bits<XF>()) : u32x4{0u, 0u, 0u, 0u};
+__device__ __forceinline__ u32x4 keep_inputs(u32x4 v, int64_t at, int64_t K) {
+  return keep_bits(v, (K - at) * elem_bits<XF>());
 }
 
 // One lane's operands of a 512-element step: 4 blocks of K, one in each of 4
@@ -105,41 +109,57 @@ struct WFrag {
 // The instruction wants 4-bit operands as block g's 32 values in group g, but
 // 8-bit ones as values [16g', 16g' + 16) of the 128, for g' = g and g + 4 --
 // while group g gives the scale of block g in either case.
+// TAIL: a step that K ends in, which reads the row's last piece again in the
+// place of those past its end; keep_step then takes out what does not count.
 template <bool TAIL>
 __device__ __forceinline__ void load_w(const uint8_t* row, const uint8_t* srow, int step, int g, int nb,
                                        WFrag& f) {
 #pragma unroll
   for (int s = 0; s < 4; ++s) {
     const int b = 16 * step + 4 * s + g;
-    f.d[s] = !TAIL || b < nb ? ldg16(row + (int64_t)b * 16) : u32x4{0u, 0u, 0u, 0u};
+    f.d[s] = ldg16(row + (int64_t)(TAIL ? min(b, nb - 1) : b) * 16);
   }
   f.s = load_scales16<TAIL>(srow, 16 * step, nb);
+}
+
+// First element of piece q of instruction s in group g's operand of a step.
+template <int XF>
+__device__ __forceinline__ int64_t input_at(int step, int s, int g, int q) {
+  if constexpr (XF == AR_E2M1_MX) return (int64_t)(16 * step + 4 * s + g) * 32;
+  else if constexpr (XF == AR_BF16) return (int64_t)(16 * step + 4 * s + g) * 32 + 8 * q;
+  else return (int64_t)(16 * step + 4 * s) * 32 + 64 * q + 16 * g;
+}
+template <int XF> constexpr int input_pieces() { return XF == AR_E2M1_MX ? 1 : (XF == AR_BF16 ? 4 : 2); }
+
+template <int XF>
+__device__ __forceinline__ u32x4& input_piece(XFrag<XF>& f, int s, int q) {
+  if constexpr (XF == AR_E2M1_MX) return f.d[s];
+  else return f.d[s][q];
 }
 
 template <int XF, bool TAIL>
 __device__ __forceinline__ void load_x(const uint8_t* row, const uint8_t* srow, int step, int g, int nb,
                                        int K, XFrag<XF>& f) {
+  constexpr int per = 128 / elem_bits<XF>();               // elements of 16 bytes
 #pragma unroll
-  for (int s = 0; s < 4; ++s) {
-    const int b = 16 * step + 4 * s + g;
-    if constexpr (XF == AR_E2M1_MX) {
-      const uint8_t* p = row + (int64_t)b * 16;
-      f.d[s] = TAIL ? load_x_tail<XF>(p, (int64_t)b * 32, K) : ldg16(p);
-    } else if constexpr (XF == AR_BF16) {
+  for (int s = 0; s < 4; ++s)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int64_t at = (int64_t)b * 32 + 8 * j;
-        f.d[s][j] = TAIL ? load_x_tail<XF>(row + at * 2, at, K) : ldg16(row + at * 2);
-      }
-    } else {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int64_t at = (int64_t)(16 * step + 4 * s) * 32 + 64 * h + 16 * g;
-        f.d[s][h] = TAIL ? load_x_tail<XF>(row + at, at, K) : ldg16(row + at);
-      }
+    for (int q = 0; q < input_pieces<XF>(); ++q) {
+      int64_t at = input_at<XF>(step, s, g, q);
+      if (TAIL) at = min(at, (int64_t)((K - 1) / per) * per);
+      input_piece<XF>(f, s, q) = ldg16(row + at * elem_bits<XF>() / 8);
     }
-  }
   if constexpr (is_mx_format(XF)) f.s = load_scales16<TAIL>(srow, 16 * step, nb);
+}
+
+template <int XF>
+__device__ __forceinline__ void keep_step(int step, int g, int nb, int K, XFrag<XF>& f) {
+#pragma unroll
+  for (int s = 0; s < 4; ++s)
+#pragma unroll
+    for (int q = 0; q < input_pieces<XF>(); ++q)
+      input_piece<XF>(f, s, q) = keep_inputs<XF>(input_piece<XF>(f, s, q), input_at<XF>(step, s, g, q), K);
+  if constexpr (is_mx_format(XF)) f.s = keep_scales(f.s, 16 * step, nb);
 }
 
 __device__ __forceinline__ i32x8 operand(u32x4 lo, u32x4 hi) {
@@ -238,11 +258,26 @@ __global__ __launch_bounds__(kWave * WN * WK) void k_mx_linear_rows(MxLinArgs a)
     WFrag w[NT];
     XFrag<XF> x[MT];
   };
+  const int full = a.K / 512, steps = (a.nb + 15) / 16;    // the last step may be one that K ends in
   auto load = [&](int st, Step& f) {
+    if (st < full) {
 #pragma unroll
-    for (int i = 0; i < NT; ++i) load_w<false>(wrow[i], wsrow[i], st, g, a.nb, f.w[i]);
+      for (int i = 0; i < NT; ++i) load_w<false>(wrow[i], wsrow[i], st, g, a.nb, f.w[i]);
 #pragma unroll
-    for (int j = 0; j < MT; ++j) load_x<XF, false>(xrow[j], xsrow[j], st, g, a.nb, a.K, f.x[j]);
+      for (int j = 0; j < MT; ++j) load_x<XF, false>(xrow[j], xsrow[j], st, g, a.nb, a.K, f.x[j]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < NT; ++i) load_w<true>(wrow[i], wsrow[i], st, g, a.nb, f.w[i]);
+#pragma unroll
+      for (int j = 0; j < MT; ++j) load_x<XF, true>(xrow[j], xsrow[j], st, g, a.nb, a.K, f.x[j]);
+    }
+  };
+  auto keep = [&](int st, Step& f) {
+    if (st < full) return;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) f.w[i].s = keep_scales(f.w[i].s, 16 * st, a.nb);
+#pragma unroll
+    for (int j = 0; j < MT; ++j) keep_step<XF>(st, g, a.nb, a.K, f.x[j]);
   };
   auto compute = [&](const Step& f) {
 #pragma unroll
@@ -262,29 +297,18 @@ __global__ __launch_bounds__(kWave * WN * WK) void k_mx_linear_rows(MxLinArgs a)
 #pragma unroll
       for (int j = 0; j < MT; ++j) acc[i][j] = multiply<XF, 3>(f.w[i], f.x[j], shift, acc[i][j]);
   };
-  // whole steps, then maybe one that K ends in
-  const int full = a.K / 512;
-  const int steps = (a.nb + 15) / 16;
-  int st = wk;
-  if (st < full) {
+  if (wk < steps) {
     Step cur;
+    int st = wk;
     load(st, cur);
-    for (; st + WK < full; st += WK) {
+    for (; st + WK < steps; st += WK) {
       Step next;
       load(st + WK, next);
-      compute(cur);
+      compute(cur);                                        // never the last step
       cur = next;
     }
+    keep(st, cur);
     compute(cur);
-    st += WK;
-  }
-  if (st < steps) {
-    Step f;
-#pragma unroll
-    for (int i = 0; i < NT; ++i) load_w<true>(wrow[i], wsrow[i], st, g, a.nb, f.w[i]);
-#pragma unroll
-    for (int j = 0; j < MT; ++j) load_x<XF, true>(xrow[j], xsrow[j], st, g, a.nb, a.K, f.x[j]);
-    compute(f);
   }
   if constexpr (WK > 1) {
 #pragma unroll
@@ -430,8 +454,11 @@ __global__ __launch_bounds__(G::threads) void k_mx_linear_tiles(MxLinArgs a) {
 
   const uint8_t* xbase = a.x + r * a.x_rank + m0 * a.x_stride;
   const uint8_t* wbase = a.w + r * a.w_rank + n0 * a.w_stride;
-  const rsrc_t xr = make_rsrc(xbase, 0x7FFFFFFFu), wr = make_rsrc(wbase, 0x7FFFFFFFu);
   const int mlast = a.M - 1 - m0, nlast = a.N - 1 - n0;    // rows past the end read the last one
+  // ranges to the 16-byte boundary after the tile's last row
+  const int64_t xrange = min(mlast, BM - 1) * a.x_stride + ((int64_t)a.K * elem_bits<XF>() + 127) / 128 * 16;
+  const int64_t wrange = min(nlast, BN - 1) * a.w_stride + (int64_t)a.nb * 16;
+  const rsrc_t xr = make_rsrc(xbase, (uint32_t)xrange), wr = make_rsrc(wbase, (uint32_t)wrange);
 
   // this thread's pieces of a step: source offsets at step 0
   uint32_t xo[G::nx], wo[G::nw];
@@ -455,23 +482,19 @@ __global__ __launch_bounds__(G::threads) void k_mx_linear_tiles(MxLinArgs a) {
       load_to_lds(wr, at + G::xbytes + (i * G::threads + wave * kWave) % G::pw * 16, wo[i],
                   (uint32_t)k * T::WB);
   };
-  // a step that K ends in: zeros past it
-  auto load_tail = [&](int k, int buf) {
+  // In a step that K ends in, once it has arrived: zeros for x past K.  (What
+  // was read there lies in the row, or in the next one, or is the zeros that a
+  // read past the buffer's range gives.)
+  auto keep_step = [&](int k, int buf) {
     uint8_t* at = smem + buf * G::stage;
 #pragma unroll
-    for (int i = 0; i < G::nx; ++i) {
-      const int slot = (i * G::threads + tid) % G::px, row = slot / T::XC;
+    for (int i = 0; i < (G::px + G::threads - 1) / G::threads; ++i) {
+      const int slot = i * G::threads + tid;
+      if (slot >= G::px) break;
+      const int row = slot / T::XC;
       const int64_t first = (int64_t)k * T::XB + place<T::XC>(row, slot % T::XC) * 16;  // byte of the row
-      *reinterpret_cast<u32x4*>(at + slot * 16) =
-          load_x_tail<XF>(xbase + xo[i] + k * T::XB, first * 8 / elem_bits<XF>(), a.K);
-    }
-#pragma unroll
-    for (int i = 0; i < G::nw; ++i) {
-      const int slot = (i * G::threads + tid) % G::pw, row = slot / T::WC;
-      const int first = k * T::WB + place<T::WC>(row, slot % T::WC) * 16;
-      u32x4 v = u32x4{0u, 0u, 0u, 0u};
-      if (first < a.nb * 16) v = ldg16(wbase + wo[i] + k * T::WB);
-      *reinterpret_cast<u32x4*>(at + G::xbytes + slot * 16) = v;
+      u32x4* p = reinterpret_cast<u32x4*>(at + slot * 16);
+      *p = keep_inputs<XF>(*p, first * 8 / elem_bits<XF>(), a.K);
     }
   };
   // Scales of the run of steps that begins with step k: 16 of each row, those
@@ -493,7 +516,7 @@ __global__ __launch_bounds__(G::threads) void k_mx_linear_tiles(MxLinArgs a) {
         load_to_lds(srow[i] + blk, at + (i * G::threads + wave * kWave) % (G::swaves * kWave) * 16);
       else                                                 // K ends in these
         *reinterpret_cast<u32x4*>(at + (i * G::threads + tid) % (G::swaves * kWave) * 16) =
-            load_scales16<true>(srow[i], blk, a.nb);
+            keep_scales(load_scales16<true>(srow[i], blk, a.nb), blk, a.nb);
     }
   };
 
@@ -590,13 +613,13 @@ __global__ __launch_bounds__(G::threads) void k_mx_linear_tiles(MxLinArgs a) {
     }
   };
 
-  // whole steps, then maybe one that K ends in
+  // whole steps, then maybe one that K ends in, loaded as the others are
   const int full = a.K / T::BK;
   const int steps = (a.nb * 32 + T::BK - 1) / T::BK;
 #pragma unroll
   for (int k = 0; k < NS - 1; ++k) {
     if (k < steps && k % T::steps_scales == 0) load_scales(k);
-    if (k < full) load_step(k, k);
+    if (k < steps) load_step(k, k);
   }
   constexpr int behind = (NS - 2) * (G::nx + G::nw);
   constexpr int wait_behind = 0x0F70 | (behind & 15) | (behind >> 4) << 14;      // vmcnt alone
@@ -612,7 +635,7 @@ __global__ __launch_bounds__(G::threads) void k_mx_linear_tiles(MxLinArgs a) {
     static_assert(T::rounds == 1, "a phase is a step");
     const bool late = wave >= 4;
     auto arrived = [&](int k) {                            // this wave's loads of step k + 1
-      if (NS > 2 && k + NS - 1 < full) __builtin_amdgcn_s_waitcnt(wait_behind);
+      if (NS > 2 && k + NS - 1 < steps) __builtin_amdgcn_s_waitcnt(wait_behind);
       else __builtin_amdgcn_s_waitcnt(0x0F70);
     };
     auto change = [&]() {
@@ -621,7 +644,7 @@ __global__ __launch_bounds__(G::threads) void k_mx_linear_tiles(MxLinArgs a) {
       __builtin_amdgcn_sched_barrier(0);
     };
     if (full > 0) {
-      if (NS > 2 && full > NS - 2) __builtin_amdgcn_s_waitcnt(wait_behind & ~0x0F00);
+      if (NS > 2 && steps > NS - 2) __builtin_amdgcn_s_waitcnt(wait_behind & ~0x0F00);
       else __builtin_amdgcn_s_waitcnt(0x0070);
       change();
       if (late) change();
@@ -629,7 +652,7 @@ __global__ __launch_bounds__(G::threads) void k_mx_linear_tiles(MxLinArgs a) {
     for (int k = 0; k < full; ++k) {
       const int ahead = k + NS - 1;
       if (ahead < steps && ahead % T::steps_scales == 0) load_scales(ahead);
-      if (ahead < full) load_step(ahead, buf == 0 ? NS - 1 : buf - 1);
+      if (ahead < steps) load_step(ahead, buf == 0 ? NS - 1 : buf - 1);
       Tokens x;
       Weights w[TI];
       read_tokens(k, 0, buf, x);
@@ -650,20 +673,21 @@ __global__ __launch_bounds__(G::threads) void k_mx_linear_tiles(MxLinArgs a) {
       // Step k has arrived when at most the NS - 2 steps after it are still on
       // their way (scales among them only make the wait longer), and this
       // wave's own scales are written.
-      if (k + NS - 2 < full) __builtin_amdgcn_s_waitcnt(wait_behind & ~0x0F00);
+      if (k + NS - 2 < steps) __builtin_amdgcn_s_waitcnt(wait_behind & ~0x0F00);
       else __builtin_amdgcn_s_waitcnt(0x0070);
       barrier_only();
       // into the buffer of step k - 1, which every wave has left
       const int ahead = k + NS - 1;
       if (ahead < steps && ahead % T::steps_scales == 0) load_scales(ahead);
-      if (ahead < full) load_step(ahead, buf == 0 ? NS - 1 : buf - 1);
+      if (ahead < steps) load_step(ahead, buf == 0 ? NS - 1 : buf - 1);
       compute(k, buf);
       if (++buf == NS) buf = 0;
     }
   }
   if (steps > full) {
-    __syncthreads();
-    load_tail(full, buf);
+    __builtin_amdgcn_s_waitcnt(0x0070);
+    barrier_only();
+    keep_step(full, buf);
     __syncthreads();
     compute(full, buf);
   }
