@@ -218,14 +218,14 @@ __device__ __forceinline__ void store_out4(void* y, int64_t at, int n, int N, bo
   }
 }
 
-// Few tokens: bound by the stream of weights.  A wave holds 16 * NT outputs
-// and 16 * MT tokens; WK waves split K step by step and join their sums, in
-// order, in shared memory.  The next step's operands are on their way while
-// one is multiplied.
-template <int XF, int YF, int NT, int MT, int WN, int WK>
+// Up to 16 tokens: bound by the stream of weights.  A wave holds 16 * NT outputs
+// and the tokens; WK waves split K step by step and join their sums, in order,
+// in shared memory.  The next step's operands are on their way while one is
+// multiplied.  16 tokens, 8-bit, 4 shards of 8192 x 2048: 11.2 us, 3.3 TB/s with
+// the launch, which takes 2; one token 10.2 us; 8 shards of 4096 x 512, bf16: 4.2.
+template <int XF, int YF, int NT, int WN, int WK>
 __global__ __launch_bounds__(kWave * WN * WK) void k_mx_linear_rows(MxLinArgs a) {
-  constexpr int tiles = NT * MT;
-  __shared__ f32x4 part[WK > 1 ? WK * WN * tiles * kWave : 1];
+  __shared__ f32x4 part[WK > 1 ? WK * WN * NT * kWave : 1];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wk = wave % WK, wn = wave / WK;
@@ -235,67 +235,50 @@ __global__ __launch_bounds__(kWave * WN * WK) void k_mx_linear_rows(MxLinArgs a)
   b /= a.m_groups;
   const int ng = b % a.n_groups;
   const int r = b / a.n_groups;
-  const int n0 = (ng * WN + wn) * 16 * NT, m0 = mg * MT * 16;
-  const uint8_t *wrow[NT], *wsrow[NT], *xrow[MT], *xsrow[MT];
+  const int n0 = (ng * WN + wn) * 16 * NT, m = mg * 16 + c;
+  const uint8_t *wrow[NT], *wsrow[NT];
 #pragma unroll
   for (int i = 0; i < NT; ++i) {                           // rows past the end read the last one
     const int n = min(n0 + i * 16 + c, a.N - 1);
     wrow[i] = a.w + r * a.w_rank + n * a.w_stride;
     wsrow[i] = a.ws + r * a.ws_rank + n * a.ws_stride;
   }
+  const uint8_t* xrow = a.x + r * a.x_rank + min(m, a.M - 1) * a.x_stride;
+  const uint8_t* xsrow = a.xs + r * a.xs_rank + min(m, a.M - 1) * a.xs_stride;
+  f32x4 acc[NT];
 #pragma unroll
-  for (int j = 0; j < MT; ++j) {
-    const int m = min(m0 + j * 16 + c, a.M - 1);
-    xrow[j] = a.x + r * a.x_rank + m * a.x_stride;
-    xsrow[j] = a.xs + r * a.xs_rank + m * a.xs_stride;
-  }
-  f32x4 acc[NT][MT];
-#pragma unroll
-  for (int i = 0; i < NT; ++i)
-#pragma unroll
-    for (int j = 0; j < MT; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int i = 0; i < NT; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   struct Step {
     WFrag w[NT];
-    XFrag<XF> x[MT];
+    XFrag<XF> x;
   };
   const int full = a.K / 512, steps = (a.nb + 15) / 16;    // the last step may be one that K ends in
   auto load = [&](int st, Step& f) {
     if (st < full) {
 #pragma unroll
       for (int i = 0; i < NT; ++i) load_w<false>(wrow[i], wsrow[i], st, g, a.nb, f.w[i]);
-#pragma unroll
-      for (int j = 0; j < MT; ++j) load_x<XF, false>(xrow[j], xsrow[j], st, g, a.nb, a.K, f.x[j]);
+      load_x<XF, false>(xrow, xsrow, st, g, a.nb, a.K, f.x);
     } else {
 #pragma unroll
       for (int i = 0; i < NT; ++i) load_w<true>(wrow[i], wsrow[i], st, g, a.nb, f.w[i]);
-#pragma unroll
-      for (int j = 0; j < MT; ++j) load_x<XF, true>(xrow[j], xsrow[j], st, g, a.nb, a.K, f.x[j]);
+      load_x<XF, true>(xrow, xsrow, st, g, a.nb, a.K, f.x);
     }
   };
   auto keep = [&](int st, Step& f) {
     if (st < full) return;
 #pragma unroll
     for (int i = 0; i < NT; ++i) f.w[i].s = keep_scales(f.w[i].s, 16 * st, a.nb);
-#pragma unroll
-    for (int j = 0; j < MT; ++j) keep_step<XF>(st, g, a.nb, a.K, f.x[j]);
+    keep_step<XF>(st, g, a.nb, a.K, f.x);
   };
   auto compute = [&](const Step& f) {
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
+    for (int i = 0; i < NT; ++i) acc[i] = multiply<XF, 0>(f.w[i], f.x, shift, acc[i]);
 #pragma unroll
-      for (int j = 0; j < MT; ++j) acc[i][j] = multiply<XF, 0>(f.w[i], f.x[j], shift, acc[i][j]);
+    for (int i = 0; i < NT; ++i) acc[i] = multiply<XF, 1>(f.w[i], f.x, shift, acc[i]);
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
+    for (int i = 0; i < NT; ++i) acc[i] = multiply<XF, 2>(f.w[i], f.x, shift, acc[i]);
 #pragma unroll
-      for (int j = 0; j < MT; ++j) acc[i][j] = multiply<XF, 1>(f.w[i], f.x[j], shift, acc[i][j]);
-#pragma unroll
-    for (int i = 0; i < NT; ++i)
-#pragma unroll
-      for (int j = 0; j < MT; ++j) acc[i][j] = multiply<XF, 2>(f.w[i], f.x[j], shift, acc[i][j]);
-#pragma unroll
-    for (int i = 0; i < NT; ++i)
-#pragma unroll
-      for (int j = 0; j < MT; ++j) acc[i][j] = multiply<XF, 3>(f.w[i], f.x[j], shift, acc[i][j]);
+    for (int i = 0; i < NT; ++i) acc[i] = multiply<XF, 3>(f.w[i], f.x, shift, acc[i]);
   };
   if (wk < steps) {
     Step cur;
@@ -312,42 +295,41 @@ __global__ __launch_bounds__(kWave * WN * WK) void k_mx_linear_rows(MxLinArgs a)
   }
   if constexpr (WK > 1) {
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
-#pragma unroll
-      for (int j = 0; j < MT; ++j)
-        part[((wk * WN + wn) * tiles + i * MT + j) * kWave + lane] = acc[i][j];
+    for (int i = 0; i < NT; ++i) part[((wk * WN + wn) * NT + i) * kWave + lane] = acc[i];
     __syncthreads();
   }
 #pragma unroll
-  for (int i = 0; i < NT; ++i)
+  for (int i = 0; i < NT; ++i) {
+    if (i % WK != wk) continue;                            // the waves of a group share the tiles
+    f32x4 v = acc[i];
+    if constexpr (WK > 1) {
+      v = part[(wn * NT + i) * kWave + lane];
 #pragma unroll
-    for (int j = 0; j < MT; ++j) {
-      const int t = i * MT + j;
-      if (t % WK != wk) continue;                          // the waves of a group share the tiles
-      f32x4 v = acc[i][j];
-      if constexpr (WK > 1) {
-        v = part[(wn * tiles + t) * kWave + lane];
-#pragma unroll
-        for (int k = 1; k < WK; ++k) v += part[((k * WN + wn) * tiles + t) * kWave + lane];
-      }
-      const int m = m0 + j * 16 + c, n = n0 + i * 16 + 4 * g;
-      if (m >= a.M || n >= a.N) continue;
-      if constexpr (XF == AR_E4M3_ROW) {
-        if (a.K > 0) v *= *reinterpret_cast<const float*>(xsrow[j]);
-      }
-      store_out4<YF>(a.y, r * a.y_rank + m * a.y_stride + n, n, a.N, a.vec != 0, v);
+      for (int k = 1; k < WK; ++k) v += part[((k * WN + wn) * NT + i) * kWave + lane];
     }
+    const int n = n0 + i * 16 + 4 * g;
+    if (m >= a.M || n >= a.N) continue;
+    if constexpr (XF == AR_E4M3_ROW) {
+      if (a.K > 0) v *= *reinterpret_cast<const float*>(xsrow);
+    }
+    store_out4<YF>(a.y, r * a.y_rank + m * a.y_stride + n, n, a.N, a.vec != 0, v);
+  }
 }
 
 // ---------------------------------------------------------- many tokens ---
 //
-// Bound by the matrix cores.  A workgroup holds BN outputs by BM tokens; K
-// goes by in steps of 128 elements (64 for bf16 inputs), NS steps' codes in shared
-// memory: while one is multiplied the ones after it are on their way, loaded
-// straight into shared memory, and one barrier a step is enough.  Rows lie there as they come, 16-byte pieces permuted by the
-// row so that the lanes that read at once meet different banks; the loads
-// apply the permutation to their addresses.  Scales come 512 elements at a
-// time, one row a thread.
+// Bound by the matrix cores.  A workgroup holds BN outputs by BM tokens; K goes by
+// in steps, NS steps' codes in shared memory: while one is multiplied the ones
+// after it are on their way, loaded straight into shared memory, and one barrier
+// a step is enough.  Rows lie there as they come, 16-byte pieces permuted by the
+// row so that the lanes that read at once meet different banks; the loads apply
+// the permutation to their addresses.  Scales come 512 elements of K at a time,
+// one row a lane.
+// 4096 x 8192 x 8192: 8-bit tokens 208 us (2.64 PFLOP/s), 4-bit 165 (3.3), bf16
+// 382 (1.44).  With 8-bit tokens the matrix cores are busy 55% of the time: the
+// two operands' way from the L2 into shared memory takes the rest (alone, with
+// no products, 178 us), since a workgroup's two steps on their way are all that
+// shared memory holds.
 
 // 16 bytes a lane from the buffer straight into shared memory, at `lds` (the
 // wave's own address) + 16 * lane.
@@ -788,10 +770,10 @@ static hipError_t launch_rows(const MxLinArgs& a0, int nranks, hipStream_t s) {
   int wk = 1;
   while (wk < 8 && 2 * wk <= steps && tiles * nranks * wk < kRowsWaves) wk *= 2;
   switch (wk) {
-    case 1: return go(k_mx_linear_rows<XF, YF, NT, 1, 4, 1>, 4, 1);
-    case 2: return go(k_mx_linear_rows<XF, YF, NT, 1, 2, 2>, 2, 2);
-    case 4: return go(k_mx_linear_rows<XF, YF, NT, 1, 1, 4>, 1, 4);
-    default: return go(k_mx_linear_rows<XF, YF, NT, 1, 1, 8>, 1, 8);
+    case 1: return go(k_mx_linear_rows<XF, YF, NT, 4, 1>, 4, 1);
+    case 2: return go(k_mx_linear_rows<XF, YF, NT, 2, 2>, 2, 2);
+    case 4: return go(k_mx_linear_rows<XF, YF, NT, 1, 4>, 1, 4);
+    default: return go(k_mx_linear_rows<XF, YF, NT, 1, 8>, 1, 8);
   }
 }
 
