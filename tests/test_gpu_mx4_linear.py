@@ -150,12 +150,13 @@ def test_scale_nan_of_an_input_row_stays_in_its_row(xf, m):
     assert np.isnan(got[1]).all() and np.array_equal(got[keep], want[keep])
 
 
+@pytest.mark.parametrize("m", (3, 40, 300))
 @pytest.mark.parametrize("xf", XF)
-def test_no_inputs_gives_zeros(xf):
-    y = torch.full((3, 24), -77.0, device="cuda")
-    p = abi.linear_params(1, 3, 20, 0, xf, None, 0, 0, None, 0, 0, None, 0, 0, None, 0, 0, "f32", y, 24, 0)
+def test_no_inputs_gives_zeros(xf, m):
+    y = torch.full((m, 24), -77.0, device="cuda")
+    p = abi.linear_params(1, m, 20, 0, xf, None, 0, 0, None, 0, 0, None, 0, 0, None, 0, 0, "f32", y, 24, 0)
     abi.ar_mx4_linear(p)
-    for rows, outs in ((0, 20), (3, 0)):
+    for rows, outs in ((0, 20), (m, 0)):
         q = abi.linear_params(1, rows, outs, 64, xf, None, 0, 0, None, 0, 0, None, 0, 0, None, 0, 0, "f32",
                               None, 24, 0)
         abi.ar_mx4_linear(q)
