@@ -326,10 +326,10 @@ __global__ __launch_bounds__(kWave * WN * WK) void k_mx_linear_rows(MxLinArgs a)
 // the permutation to their addresses.  Scales come 512 elements of K at a time,
 // one row a lane.
 // 4096 x 8192 x 8192: 8-bit tokens 208 us (2.64 PFLOP/s), 4-bit 165 (3.3), bf16
-// 382 (1.44).  With 8-bit tokens the matrix cores are busy 55% of the time: the
-// two operands' way from the L2 into shared memory takes the rest (alone, with
-// no products, 178 us), since a workgroup's two steps on their way are all that
-// shared memory holds.
+// 382 (1.44).  With 8-bit tokens the matrix cores are busy 63% of the time.  The
+// operands' way from the L2 into shared memory and from there into registers
+// takes 178 us by itself, without any product, and the two overlap in part only:
+// the two steps on their way are all that shared memory holds.
 
 // 16 bytes a lane from the buffer straight into shared memory, at `lds` (the
 // wave's own address) + 16 * lane.
