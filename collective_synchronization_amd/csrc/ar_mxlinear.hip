@@ -221,8 +221,8 @@ __device__ __forceinline__ void store_out4(void* y, int64_t at, int n, int N, bo
 // Up to 16 tokens: bound by the stream of weights.  A wave holds 16 * NT outputs
 // and the tokens; WK waves split K step by step and join their sums, in order,
 // in shared memory.  The next step's operands are on their way while one is
-// multiplied.  16 tokens, 8-bit, 4 shards of 8192 x 2048: 11.2 us, 3.3 TB/s with
-// the launch, which takes 2; one token 10.2 us; 8 shards of 4096 x 512, bf16: 4.2.
+// multiplied.  4 shards of 8192 x 2048, 8-bit: one token 8.4 us, 4.2 TB/s with
+// the launch, which takes 2; 8 tokens 9.8; 8 shards of 4096 x 512, bf16: 4.3.
 template <int XF, int YF, int NT, int WN, int WK>
 __global__ __launch_bounds__(kWave * WN * WK) void k_mx_linear_rows(MxLinArgs a) {
   __shared__ f32x4 part[WK > 1 ? WK * WN * NT * kWave : 1];
@@ -325,11 +325,11 @@ __global__ __launch_bounds__(kWave * WN * WK) void k_mx_linear_rows(MxLinArgs a)
 // row so that the lanes that read at once meet different banks; the loads apply
 // the permutation to their addresses.  Scales come 512 elements of K at a time,
 // one row a lane.
-// 4096 x 8192 x 8192: 8-bit tokens 208 us (2.64 PFLOP/s), 4-bit 165 (3.3), bf16
-// 382 (1.44).  With 8-bit tokens the matrix cores are busy 63% of the time.  The
-// operands' way from the L2 into shared memory and from there into registers
-// takes 178 us by itself, without any product, and the two overlap in part only:
-// the two steps on their way are all that shared memory holds.
+// 4096 x 8192 x 8192: 8-bit tokens 204 us (2.7 PFLOP/s), 4-bit 162 (3.4), bf16
+// 375 (1.46).  With 8-bit tokens the matrix cores are busy 63% of the time.  In
+// a form of 208 us, the operands' way into shared memory and registers took 178 us
+// without any product, the products 141 without operands: they overlap in part
+// only, and the two steps on their way are all that shared memory holds.
 
 // 16 bytes a lane from the buffer straight into shared memory, at `lds` (the
 // wave's own address) + 16 * lane.
@@ -786,9 +786,17 @@ static hipError_t launch_tiles(const MxLinArgs& a0, int nranks, hipStream_t s) {
                 dim3(G::threads), s, a);
 }
 
-// Which kernel.  The largest tile that gives every CU (256) one; tiles of 32
+// Which kernel.  Tiles for more than 16 tokens, and for 9 to 16 of 8 or 4 bits
+// where the smallest tiles are more than the CUs (256).  Among tiles the largest
+// that gives every CU one and is at least half full of tokens; tiles of 32
 // tokens with K shared by 4 groups of waves where even those are not more than
 // the CUs.  Measured both ways, 8-bit tokens, in us:
+//   32 x 64 tiles against waves on rows: 4 x 16 x 8192 x 2048 9.7 and 11.2, with
+//   9 tokens 9.7 and 10.0, 8 9.5 and 9.8, 4 9.3 and 8.8; 16 x 8192 x 8192 (128
+//   tiles) 15.9 and 11.5; bf16, 4 x 16 x 8192 x 2048 14.8 and 14.9, 12 14.8 and
+//   13.6;
+//   256 x 256 against 128 x 128 or less: 4096 to 131072, 16 tokens 107 and 69, 64
+//   110 and 95, 128 114 and 91;
 //   256 x 256 against 128 x 128 tiles: 2048 x 8192 x 8192 108 and 131, 1024 x
 //   8192 x 8192 102 (128 tiles) and 66;
 //   128 x 128 against 64 x 64: 4 x 128 x 8192 x 2048 17.5 and 19.4, 256 x 4096 x
@@ -802,13 +810,15 @@ static hipError_t launch_tiles(const MxLinArgs& a0, int nranks, hipStream_t s) {
 // the other kernel at any number of tokens.
 template <int XF, int YF>
 static hipError_t launch_linear(const MxLinArgs& a, int nranks, hipStream_t s) {
-  if (a.M > 16 && a.x_stride < (1 << 23) && a.w_stride < (1 << 23)) {
+  auto tiles = [&](int bm, int bn) -> int64_t {
+    return (int64_t)((a.N + bn - 1) / bn) * ((a.M + bm - 1) / bm) * nranks;
+  };
+  const bool many = a.M > 16 || (XF != AR_BF16 && a.M > 8 && tiles(32, 64) > 256);
+  if (many && a.x_stride < (1 << 23) && a.w_stride < (1 << 23)) {
     constexpr int K1 = XF == AR_BF16 ? 64 : 128;
     constexpr bool x4 = XF == AR_E2M1_MX;                  // small enough for steps of 256
-    auto tiles = [&](int bm, int bn) -> int64_t {
-      return (int64_t)((a.N + bn - 1) / bn) * ((a.M + bm - 1) / bm) * nranks;
-    };
-    if (tiles(256, 256) >= 256) return launch_tiles<Tile<XF, YF, K1, 256, 256, 64, 128, 3>>(a, nranks, s);
+    if (a.M > 128 && tiles(256, 256) >= 256)
+      return launch_tiles<Tile<XF, YF, K1, 256, 256, 64, 128, 3>>(a, nranks, s);
     if (a.M > 64 && tiles(128, 128) >= 256)
       return launch_tiles<Tile<XF, YF, x4 ? 256 : K1, 128, 128, 64, 64, x4 ? 2 : 3>>(a, nranks, s);
     if (tiles(32, 64) <= 256) return launch_tiles<Tile<XF, YF, 4 * K1, 32, 64, 32, 16, 3, 4>>(a, nranks, s);

@@ -350,6 +350,11 @@ __device__ __forceinline__ void reduce_finish(const ReduceNormArgs& a, int64_t r
 // of every rank until they carry their evidence (in whatever order the
 // blocks arrive), adds them in rank order in binary32 and goes on with the
 // norm; the sum is never rounded or written.
+// 8 ranks, [1,4096], LL, to 8-bit blocks: 7.6 us (and 2.4 for the pack); 16 ranks,
+// [8,4096], sentinel, to 8 bits a row: 9.9 (and 2.6).  Bound by one CU's read of
+// its row from every rank, 128 KiB in both, past the L2.  A row stays in one
+// workgroup all the same: sharing it would put an exchange of sums between
+// workgroups, which then must all be resident, into every row.
 template <int P, int NMAX, int NI>
 __global__ __launch_bounds__(kNormThreads) void k_reduce_norm(ReduceNormArgs a) {
   __shared__ NormShared sm;

@@ -106,8 +106,9 @@ __device__ __forceinline__ void values(const Raw<F>& r, int64_t count, int64_t f
 
 // Float rows go past the caches: the next kernel reads them on any XCD, and the
 // lines that they would displace are inputs still to be read.  8192 x 8192 from
-// 4 bits to bf16: 27.8 us against 39.1 with ordinary stores; the norm of 16384 x
-// 8192 to bf16 180 against 185, of 1000 x 4100 fp16 7.8 against 8.4.
+// 4 bits to bf16: 28 us against 39 with ordinary stores (25 since, for other
+// reasons); the norm of 16384 x 8192 to bf16 180 against 185, of 1000 x 4100 fp16
+// 7.8 against 8.4.
 template <typename V>
 __device__ __forceinline__ void store_nt(void* p, V v) {
   __builtin_nontemporal_store(v, reinterpret_cast<V*>(p));

@@ -76,7 +76,10 @@ SIZES = [(1, 1, 16, 32), (1, 1, 1, 1), (2, 3, 17, 33), (8, 1, 4096, 512), (1, 16
          (2, 130, 520, 288), (1, 257, 260, 2048), (1, 300, 1030, 160),
          # each of the tile kernels, by its number of tiles; K in whole steps and not
          (16, 300, 2000, 544), (16, 257, 2050, 96), (8, 700, 2500, 1100), (16, 100, 2000, 1100),
-         (16, 20, 2000, 1100), (16, 32, 1100, 64), (16, 60, 2000, 300), (1, 40, 100, 3500), (3, 100, 200, 2560)]
+         (16, 20, 2000, 1100), (16, 32, 1100, 64), (16, 60, 2000, 300), (1, 40, 100, 3500), (3, 100, 200, 2560),
+         # either side of where the kernel for a few tokens and the largest tiles take over
+         (16, 8, 1100, 544), (16, 9, 1100, 544), (16, 16, 2000, 1100), (8, 13, 2500, 300), (16, 128, 2050, 288),
+         (16, 129, 2050, 288)]
 
 
 @pytest.mark.parametrize("yf", ("bf16", "f32"))
