@@ -88,12 +88,35 @@ struct Gamma {
   }
 };
 
-// 1 / sqrt(x): the binary32 result and one Newton step in binary64.  Infinite
-// and NaN results of the first, and x beyond binary32's range, pass through.
+// 1 / sqrt(x) for x >= 0, right to 2^-50 over all of binary64: the root
+// instruction on x times an even power of two, in [1/2, 2), then one step of
+// the third order.  0, infinities and NaN give inf, 0 and NaN.
 __device__ __forceinline__ double reciprocal_root(double x) {
-  const double r = (double)(1.0f / __builtin_sqrtf((float)x));
-  const double t = __builtin_fma(-x * r, r, 1.0);
-  return (float)x < 3.0e38f && (float)x > 1.2e-38f ? __builtin_fma(0.5 * r, t, r) : r;
+  const int e = __builtin_amdgcn_frexp_exp(x) & ~1;
+  const double xs = __builtin_ldexp(x, -e);
+  const double r = (double)__builtin_amdgcn_rsqf((float)xs);
+  const double t = __builtin_fma(-xs * r, r, 1.0);
+  const double better = __builtin_fma(r * t, __builtin_fma(0.375, t, 0.5), r);
+  return __builtin_ldexp(x > 0.0 && x < __builtin_inf() ? better : r, -(e >> 1));
+}
+
+// A root that binary32 holds with room for a product's rounding error; the
+// products of other rows are binary64.  (Rows of values below 2^-100 with eps 0,
+// or above 2^100.)
+__device__ __forceinline__ bool ordinary_root(double r) { return r > 0x1p-100 && r < 0x1p100; }
+
+__device__ __forceinline__ float product64(float a, double r, float b) {
+  // converted anew: the sum's conversions would hold two registers an element
+  __asm__("" : "+v"(a));
+  return (float)((double)a * r * (double)b);
+}
+
+// A value that all lanes share, in scalar registers.
+__device__ __forceinline__ double scalar(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)u);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(u >> 32));
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 
 // a * (r_hi + r_lo) * b with the products' rounding errors carried along and
@@ -173,15 +196,19 @@ __device__ __forceinline__ void norm_finish(const NormArgs& a, int64_t row, floa
     s = sm.sum[0];
     for (int w = 1; w < waves; ++w) s += sm.sum[w];
   }
-  const double r = reciprocal_root(s * a.inv_hidden + (double)a.eps);
+  const double r = scalar(reciprocal_root(s * a.inv_hidden + (double)a.eps));
   const float r_hi = (float)r, r_lo = (float)(r - (double)r_hi);
+  const bool ordinary = ordinary_root(r);                  // the same for the row
 
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
     const int c = i * threads + t;
     float g[8];
     gamma.get(a, i, g);
-    if constexpr (is_float_format(FY)) {
+    if (!ordinary) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) h[i][k] = product64(h[i][k], r, g[k]);
+    } else if constexpr (is_float_format(FY)) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) h[i][k] = (h[i][k] * r_hi) * g[k];
     } else {

@@ -1,0 +1,71 @@
+"""The residual norm where single roundings show: the ends of the range, and
+values beside the border between two codes.
+
+The kernel's r is right to 2^-50 and each product is rounded once in effect
+(products of the rows that binary32's range does not hold are binary64), so
+its outputs are those of the 64-bit form but where that lies within a few
+2^-50 of a border.  The 64-bit form's own sum and products are off by less than
+2^-48.  NEAR covers both.
+"""
+import numpy as np
+import pytest
+import torch
+
+from collective_synchronization_amd import abi
+from layer_cases import TORCH, check_float, check_quantized, float_rows, out_rows, to_type, untouched
+from oracle import layer
+
+pytestmark = pytest.mark.gpu
+
+NEAR = 2.0 ** -46
+REL = 64 * 2.0 ** -24            # a row's steps when each is a binary32 one
+
+
+def run(x, fmt, y_fmt, gamma=None, eps=0.0, res=None, res_fmt=None):
+    """y rows of the norm of x (+ res), with gamma."""
+    rows, cols = x.shape
+    xd = float_rows(x, fmt)
+    rd = float_rows(res, res_fmt) if res is not None else None
+    y = out_rows(rows, cols, y_fmt)
+    g = torch.from_numpy(np.asarray(gamma)).to(TORCH[fmt]).to("cuda") if gamma is not None else None
+    p = abi.norm_params(rows, cols, eps, fmt, g, res_fmt or fmt, rd.data if rd else None,
+                        rd.stride if rd else 0, None, 0, y_fmt, y.data, y.stride, y.scales,
+                        y.scale_stride)
+    abi.ar_residual_norm(p, xd.data, xd.stride)
+    torch.cuda.synchronize()
+    return y
+
+
+@pytest.mark.parametrize("y_fmt", ("same", "row8", "mx8", "mx4"))
+@pytest.mark.parametrize("fmt", ("f32", "bf16"))
+@pytest.mark.parametrize("cols", (40, 4096, 12000))
+def test_rows_at_the_ends_of_the_range(cols, fmt, y_fmt):
+    """Rows whose mean square leaves binary32's range either way: v is of
+    the order of 1 all the same."""
+    rng = np.random.default_rng(cols)
+    sizes = np.array([1e19, 3e19, 1e25, 5e37, 1e-18, 1e-19, 3e-21, 1e-22, 1e-23, 1e-30, 2e-37, 1.0])
+    x = to_type(np.clip(rng.standard_normal((len(sizes), cols)), -6, 6) * sizes[:, None], fmt)
+    y_fmt = fmt if y_fmt == "same" else y_fmt
+    y = run(x, fmt, y_fmt)
+    v = layer.norm(x, None, 0.0)
+    if y_fmt in TORCH:
+        check_float(y.data[:, :cols].double().cpu().numpy(), v, y_fmt, REL)
+    else:
+        check_quantized(y, y_fmt, v, REL)
+    assert untouched(y)
+
+
+def test_subnormal_rows():
+    """Rows of binary32's smallest numbers, eps 0."""
+    x = np.ldexp(np.arange(1.0, 65.0)[None], np.array([[-149], [-140], [-131]]))
+    y = run(x, "f32", "f32")
+    check_float(y.data[:, :64].double().cpu().numpy(), layer.norm(x, None, 0.0), "f32", REL)
+
+
+def test_eps_beside_a_small_mean_square():
+    """A mean square below binary32's range and an eps like it."""
+    rng = np.random.default_rng(2)
+    x = to_type(rng.standard_normal((4, 300)) * 1e-20, "f32")
+    eps = np.float32(1e-40)
+    y = run(x, "f32", "f32", eps=float(eps))
+    check_float(y.data[:, :300].double().cpu().numpy(), layer.norm(x, None, float(eps)), "f32", REL)
