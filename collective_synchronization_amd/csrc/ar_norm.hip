@@ -100,17 +100,6 @@ __device__ __forceinline__ double reciprocal_root(double x) {
   return __builtin_ldexp(x > 0.0 && x < __builtin_inf() ? better : r, -(e >> 1));
 }
 
-// A root that binary32 holds with room for a product's rounding error; the
-// products of other rows are binary64.  (Rows of values below 2^-100 with eps 0,
-// or above 2^100.)
-__device__ __forceinline__ bool ordinary_root(double r) { return r > 0x1p-100 && r < 0x1p100; }
-
-__device__ __forceinline__ float product64(float a, double r, float b) {
-  // converted anew: the sum's conversions would hold two registers an element
-  __asm__("" : "+v"(a));
-  return (float)((double)a * r * (double)b);
-}
-
 // A value that all lanes share, in scalar registers.
 __device__ __forceinline__ double scalar(double v) {
   const uint64_t u = __builtin_bit_cast(uint64_t, v);
@@ -119,40 +108,98 @@ __device__ __forceinline__ double scalar(double v) {
   return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 
-// a * (r_hi + r_lo) * b with the products' rounding errors carried along and
-// added at the end: one rounding in effect.  ODD: towards zero with the last
-// bit set where that is not exact.  Infinite and NaN products end as NaN.
-template <bool ODD>
-__device__ __forceinline__ float product3(float a, float r_hi, float r_lo, float b) {
-  const float p = a * r_hi;
-  const float e = __builtin_fmaf(a, r_lo, __builtin_fmaf(a, r_hi, -p));
-  const float q = p * b;
-  const float c = __builtin_fmaf(e, b, __builtin_fmaf(p, b, -q));
-  const float t = q + c;
-  if constexpr (!ODD) return t;
-  const float d = c - (t - q);                             // what t lacks
-  uint32_t u = __float_as_uint(t);
-  if (d * t < 0.0f) --u;
-  if (d != 0.0f) u |= 1u;
+// The row's factor: r, and r in two binary32 parts with room for a product's
+// rounding error, unless the row is not an ordinary one (values below 2^-100
+// with eps 0, or above 2^100).
+struct Root {
+  double r;
+  float hi, lo;
+  bool ordinary;
+  __device__ __forceinline__ explicit Root(double v)
+      : r(scalar(v)), hi((float)r), lo((float)(r - (double)hi)), ordinary(r > 0x1p-100 && r < 0x1p100) {}
+};
+
+// A value that is rounded once more must not come out on the other side of a
+// border between two neighbours of the output format.  Borders of 8- and 4-bit
+// floats (and powers of two, those of the scales) have 19 trailing zeros in
+// binary32; kNear steps cover the error of two products and of r.hi, 3 * 2^-24.
+constexpr uint32_t kNear = 4;
+template <int FY>
+constexpr bool has_borders() { return is_mx_format(FY); }
+__device__ __forceinline__ uint32_t from_border(float v) { return (__float_as_uint(v) + kNear) & 0x7FFFFu; }
+
+// a * r * b in binary64, to binary32: to nearest, or for formats with a border
+// towards zero with the last bit set where that is not exact.
+template <int FY>
+__device__ __forceinline__ float product64(float a, double r, float b) {
+  // converted anew: the sum's conversions would hold two registers an element
+  __asm__("" : "+v"(a));
+  const double d = (double)a * r * (double)b;
+  const float f = (float)d;
+  if constexpr (!has_borders<FY>()) return f;
+  const double back = (double)f;
+  uint32_t u = __float_as_uint(f);
+  const bool inexact = (back < d || back > d) && abs_bits(f) < kInfBits;
+  if (inexact && __builtin_fabs(back) > __builtin_fabs(d)) --u;
+  if (inexact) u |= 1u;
   return __uint_as_float(u);
 }
 
-// Values for an 8- or 4-bit format.  One that lies just beside a border between
-// two codes and rounds to the border itself would then round the wrong way:
-// borders have at least 19 trailing zeros, and a chunk with such a value is
-// taken again with ODD.
+// a * (hi + lo) * b with the products' rounding errors carried along and added
+// at the end: one rounding in effect, for products above 2^-100, below which an
+// error may be less than binary32 holds.
+__device__ __forceinline__ float product3(float a, const Root& r, float b, float& p, float& q) {
+  p = a * r.hi;
+  const float e = __builtin_fmaf(a, r.lo, __builtin_fmaf(a, r.hi, -p));
+  q = p * b;
+  const float c = __builtin_fmaf(e, b, __builtin_fmaf(p, b, -q));
+  return q + c;
+}
+
+// The first attempt at a product, and what shows whether it is to be trusted.
 template <int FY>
-__device__ __forceinline__ void products8(float (&h)[8], float r_hi, float r_lo, const float (&g)[8]) {
-  float v[8];
-  uint32_t least = 0xFFFFFFFFu;
+__device__ __forceinline__ float product(float a, const Root& r, float b, float& p, float& q) {
+  if constexpr (!has_borders<FY>()) return product3(a, r, b, p, q);
+  p = a * r.hi;
+  return q = p * b;
+}
+
+// h = (h * r) * g for an 8- or 4-bit format.  A chunk with a value near a border
+// (0.8% of the waves' chunks of random rows), or with a small product that is not
+// a zero of its own, is taken again in binary64.  All in binary64, 16384 x 8192
+// takes 188 us instead of 165: about 45 instructions an element are what the
+// vector units do in the memory's time.
+template <int FY>
+__device__ __forceinline__ void products8(float (&h)[8], const Root& r, const float (&g)[8]) {
+  float v[8], p, q, least_p = r.ordinary ? __builtin_inff() : 0.0f, least_q = __builtin_inff();
+  uint32_t border = 0xFFFFFFFFu;
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
-    v[k] = product3<false>(h[k], r_hi, r_lo, g[k]);
-    least = min(least, __float_as_uint(v[k]) & 0x7FFFFu);
+    v[k] = product<FY>(h[k], r, g[k], p, q);
+    least_p = fminf(least_p, fabsf(p));
+    least_q = fminf(least_q, fabsf(q));
+    if constexpr (has_borders<FY>()) border = min(border, from_border(v[k]));
   }
-  if (is_mx_format(FY) && least == 0u) {
+  bool again = false;
+  if (__builtin_expect(least_p < 0x1p-100f || least_q < 0x1p-100f || border <= 2 * kNear, 0)) {
+    again = !r.ordinary;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = product3<true>(h[k], r_hi, r_lo, g[k]);
+    for (int k = 0; k < 8; ++k) {
+      float a = h[k];
+      __asm__("" : "+v"(a));                               // p and q anew, not held
+      product<FY>(a, r, g[k], p, q);
+      const bool small = fminf(fabsf(p), fabsf(q)) < 0x1p-100f;
+      const bool near = has_borders<FY>() && from_border(v[k]) <= 2 * kNear;
+      again = again || ((small || near) && h[k] != 0.0f && g[k] != 0.0f);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+  if (__builtin_expect(again, 0)) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      v[k] = product64<FY>(h[k], r.r, g[k]);
+      __builtin_amdgcn_sched_barrier(0);                   // one at a time: few registers
+    }
   }
 #pragma unroll
   for (int k = 0; k < 8; ++k) h[k] = v[k];
@@ -180,9 +227,7 @@ __device__ __forceinline__ void norm_finish(const NormArgs& a, int64_t row, floa
   }
   // The sum and r are binary64, and 8- and 4-bit outputs round products that are
   // right to the last bit of binary32: with binary32 steps throughout, a few of
-  // 4 million codes came out a step off.  (Products in binary64 give the same
-  // codes but take 188 us for 16384 x 8192 instead of 162: about 45
-  // instructions an element are what the vector units do in the memory's time.)
+  // 4 million codes came out a step off.
   double s = 0.0;
 #pragma unroll
   for (int i = 0; i < NI; ++i)
@@ -196,28 +241,32 @@ __device__ __forceinline__ void norm_finish(const NormArgs& a, int64_t row, floa
     s = sm.sum[0];
     for (int w = 1; w < waves; ++w) s += sm.sum[w];
   }
-  const double r = scalar(reciprocal_root(s * a.inv_hidden + (double)a.eps));
-  const float r_hi = (float)r, r_lo = (float)(r - (double)r_hi);
-  const bool ordinary = ordinary_root(r);                  // the same for the row
+  const Root r(reciprocal_root(s * a.inv_hidden + (double)a.eps));
 
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
     const int c = i * threads + t;
+    const int left = (int)H - c * 8;                       // elements of the row from here on
     float g[8];
     gamma.get(a, i, g);
-    if (!ordinary) {
+    if constexpr (is_float_format(FY)) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) h[i][k] = product64(h[i][k], r, g[k]);
-    } else if constexpr (is_float_format(FY)) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) h[i][k] = (h[i][k] * r_hi) * g[k];
+      for (int k = 0; k < 8; ++k)
+        h[i][k] = r.ordinary ? (h[i][k] * r.hi) * g[k] : product64<FY>(h[i][k], r.r, g[k]);
     } else {
-      products8<FY>(h[i], r_hi, r_lo, g);
-    }
-    // a row whose r is not finite makes NaN of the zeros past its end
-    if ((int64_t)c * 8 + 8 > H) {
+      if (left < 8) {                                      // zeros would be taken for small products
 #pragma unroll
-      for (int k = 0; k < 8; ++k) h[i][k] = (int64_t)c * 8 + k < H ? h[i][k] : 0.0f;
+        for (int k = 0; k < 8; ++k) {
+          h[i][k] = k < left ? h[i][k] : 1.0f;
+          g[k] = k < left ? g[k] : 1.0f;
+        }
+      }
+      products8<FY>(h[i], r, g);
+    }
+    // back to zeros; a row whose r is not finite makes NaN of zeros too
+    if (left < 8) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) h[i][k] = k < left ? h[i][k] : 0.0f;
     }
   }
 

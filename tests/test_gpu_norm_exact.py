@@ -69,3 +69,64 @@ def test_eps_beside_a_small_mean_square():
     eps = np.float32(1e-40)
     y = run(x, "f32", "f32", eps=float(eps))
     check_float(y.data[:, :300].double().cpu().numpy(), layer.norm(x, None, float(eps)), "f32", REL)
+
+
+def _beside_borders(rng, cols, fmt, s):
+    """(x, gamma) of one binary32 row, eps 0, whose values in units of 2^s lie
+    within half a binary32 step of the format's borders, on either side; the
+    first of each 32 is the block's largest.  gamma is the binary32 number
+    nearest to border / (h * r)."""
+    grid = layer.GRID[fmt]
+    borders = (grid[1:] + grid[:-1]) / 2
+    x = to_type(rng.uniform(1.0, 2.0, (1, cols)) * rng.choice([-1.0, 1.0], (1, cols)), "f32")
+    b = rng.choice(borders, cols)
+    b[::32] = 1.25 * 2.0 ** layer.EMAX[fmt]
+    r = 1.0 / np.sqrt((x * x).sum() / cols)
+    return x, to_type(np.ldexp(b / (np.abs(x[0]) * r), s), "f32")
+
+
+@pytest.mark.parametrize("fmt", ("mx8", "mx4"))
+@pytest.mark.parametrize("s", (0, 60, -20, -58, -61, -70, -95, -110, -118, -125, -127))
+def test_codes_beside_borders(s, fmt):
+    rng = np.random.default_rng(200 + s)
+    cols = 16384
+    x, gamma = _beside_borders(rng, cols, fmt, s)
+    y = run(x, "f32", fmt, gamma=gamma)
+    check_quantized(y, fmt, layer.norm(x, gamma, 0.0), NEAR)
+
+
+@pytest.mark.parametrize("y_fmt", ("mx8", "mx4"))
+@pytest.mark.parametrize("fmt,res_fmt", (("bf16", "bf16"), ("bf16", "f32"), ("f16", "f16"), ("f32", "f32")))
+@pytest.mark.parametrize("rows,cols", ((400, 4096), (60, 8200), (2000, 520), (70, 30011)))
+def test_codes_of_ordinary_rows(rows, cols, fmt, res_fmt, y_fmt):
+    """Every code and scale is the 64-bit form's."""
+    rng = np.random.default_rng(rows + cols)
+    x = to_type(rng.standard_normal((rows, cols)), fmt)
+    res = to_type(rng.standard_normal((rows, cols)) * 2, res_fmt)
+    gamma = to_type(rng.uniform(0.5, 1.5, cols), fmt)
+    eps = np.float32(1e-5)
+    y = run(x, fmt, y_fmt, gamma=gamma, eps=float(eps), res=res, res_fmt=res_fmt)
+    h = (res.astype(np.float32) + x.astype(np.float32)).astype(np.float64)
+    check_quantized(y, y_fmt, layer.norm(h, gamma, float(eps)), NEAR)
+
+
+@pytest.mark.parametrize("y_fmt", ("mx8", "mx4", "row8"))
+def test_zeros_among_values(y_fmt):
+    """Zeros in the row and in gamma, small products and a gamma that takes a
+    value past binary32's range: the block of that one is NaN."""
+    cols = 320
+    rng = np.random.default_rng(5)
+    x = to_type(rng.standard_normal((3, cols)), "f32")
+    x[0, ::3] = 0.0
+    x[1, 64:] = -0.0
+    x[2, 5] = 2.0 ** -140
+    gamma = to_type(rng.uniform(0.5, 1.5, cols), "f32")
+    gamma[::5] = 0.0
+    gamma[5], gamma[100], gamma[130] = 2.0 ** 100, 2.0 ** -120, 2.0 ** 126
+    x[2, 130] = 60.0
+    y = run(x, "f32", y_fmt, gamma=gamma)
+    with np.errstate(over="ignore"):
+        v = layer.norm(x, gamma, 0.0)
+    v = np.where(np.abs(v) >= 2.0 ** 128, np.inf, v)
+    assert np.isinf(v[2, 130])
+    check_quantized(y, y_fmt, v, NEAR)
