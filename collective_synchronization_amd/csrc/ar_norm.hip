@@ -4,8 +4,8 @@
 //     h = residual + x,  r = 1 / sqrt(sum(h^2) / hidden + eps),
 //     v = (h * r) * gamma;  residual_out = round(h);  y = v in y's format.
 //
-// h is binary32 and not rounded before the norm, the sum is binary64, and each
-// output is rounded once.
+// h is binary32 and not rounded before the norm, the sum and r are binary64; how
+// v is rounded goes by the format (products8 below).
 //
 // What bounds it: for many rows the memory system (x and the residual read
 // once, both outputs written once; a row stays in registers between the sum
@@ -100,105 +100,110 @@ __device__ __forceinline__ double reciprocal_root(double x) {
   return __builtin_ldexp(x > 0.0 && x < __builtin_inf() ? better : r, -(e >> 1));
 }
 
-// A value that all lanes share, in scalar registers.
-__device__ __forceinline__ double scalar(double v) {
-  const uint64_t u = __builtin_bit_cast(uint64_t, v);
-  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)u);
-  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(u >> 32));
-  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
-}
-
-// The row's factor: r, and r in two binary32 parts with room for a product's
-// rounding error, unless the row is not an ordinary one (values below 2^-100
-// with eps 0, or above 2^100).
+// The row's factor, in scalar registers: r, and r in two binary32 parts with room
+// for a product's rounding error, unless the row is not an ordinary one (values
+// below 2^-100 with eps 0, or above 2^100).
 struct Root {
   double r;
   float hi, lo;
   bool ordinary;
-  __device__ __forceinline__ explicit Root(double v)
-      : r(scalar(v)), hi((float)r), lo((float)(r - (double)hi)), ordinary(r > 0x1p-100 && r < 0x1p100) {}
+  __device__ __forceinline__ explicit Root(double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);    // the same in all lanes
+    const uint32_t low = __builtin_amdgcn_readfirstlane((uint32_t)u);
+    const uint32_t high = __builtin_amdgcn_readfirstlane((uint32_t)(u >> 32));
+    r = __builtin_bit_cast(double, (uint64_t)high << 32 | low);
+    hi = (float)r;
+    lo = (float)(r - (double)hi);
+    ordinary = (high >> 20) - (1023u - 100u) < 200u;       // 2^-100 <= r < 2^100
+  }
 };
 
-// A value that is rounded once more must not come out on the other side of a
-// border between two neighbours of the output format.  Borders of 8- and 4-bit
-// floats (and powers of two, those of the scales) have 19 trailing zeros in
-// binary32; kNear steps cover the error of two products and of r.hi, 3 * 2^-24.
-constexpr uint32_t kNear = 4;
-template <int FY>
-constexpr bool has_borders() { return is_mx_format(FY); }
-__device__ __forceinline__ uint32_t from_border(float v) { return (__float_as_uint(v) + kNear) & 0x7FFFFu; }
+// a * r * b = q + c, for products above 2^-100, below which an error may be less
+// than binary32 holds.
+struct Product {
+  float p, q, c;
+  __device__ __forceinline__ Product(float a, const Root& r, float b) : p(a * r.hi), q(p * b) {
+    const float e = __builtin_fmaf(a, r.lo, __builtin_fmaf(a, r.hi, -p));
+    c = __builtin_fmaf(e, b, __builtin_fmaf(p, b, -q));
+  }
+  // Right to binary32's last bit; an infinite q, whose c is as infinite the other
+  // way, stays.
+  __device__ __forceinline__ float nearest() const {
+    return q + __builtin_amdgcn_fmed3f(c, -0x1.fffffep127f, 0x1.fffffep127f);
+  }
+  // Towards zero with the last bit set where that is not exact.
+  __device__ __forceinline__ float odd() const {
+    const float t = q + c, d = c - (t - q);                // what t lacks
+    const bool above = (int)(__float_as_uint(d) ^ __float_as_uint(t)) < 0;
+    return d == 0.0f ? t : __uint_as_float((__float_as_uint(t) - (above ? 1u : 0u)) | 1u);
+  }
+};
 
-// a * r * b in binary64, to binary32: to nearest, or for formats with a border
-// towards zero with the last bit set where that is not exact.
-template <int FY>
+// a * r * b in binary64, to binary32: to nearest, or as odd() does.
+template <bool ODD>
 __device__ __forceinline__ float product64(float a, double r, float b) {
-  // converted anew: the sum's conversions would hold two registers an element
-  __asm__("" : "+v"(a));
+  __asm__("" : "+v"(a));                                   // the sum's conversions are not held for it
   const double d = (double)a * r * (double)b;
   const float f = (float)d;
-  if constexpr (!has_borders<FY>()) return f;
+  if constexpr (!ODD) return f;
   const double back = (double)f;
-  uint32_t u = __float_as_uint(f);
-  const bool inexact = (back < d || back > d) && abs_bits(f) < kInfBits;
-  if (inexact && __builtin_fabs(back) > __builtin_fabs(d)) --u;
-  if (inexact) u |= 1u;
-  return __uint_as_float(u);
+  if (!(back < d || back > d) || abs_bits(f) >= kInfBits) return f;
+  return __uint_as_float((__float_as_uint(f) - (__builtin_fabs(back) > __builtin_fabs(d) ? 1u : 0u)) | 1u);
 }
 
-// a * (hi + lo) * b with the products' rounding errors carried along and added
-// at the end: one rounding in effect, for products above 2^-100, below which an
-// error may be less than binary32 holds.
-__device__ __forceinline__ float product3(float a, const Root& r, float b, float& p, float& q) {
-  p = a * r.hi;
-  const float e = __builtin_fmaf(a, r.lo, __builtin_fmaf(a, r.hi, -p));
-  q = p * b;
-  const float c = __builtin_fmaf(e, b, __builtin_fmaf(p, b, -q));
-  return q + c;
-}
-
-// The first attempt at a product, and what shows whether it is to be trusted.
-template <int FY>
-__device__ __forceinline__ float product(float a, const Root& r, float b, float& p, float& q) {
-  if constexpr (!has_borders<FY>()) return product3(a, r, b, p, q);
-  p = a * r.hi;
-  return q = p * b;
-}
-
-// h = (h * r) * g for an 8- or 4-bit format.  A chunk with a value near a border
-// (0.8% of the waves' chunks of random rows), or with a small product that is not
-// a zero of its own, is taken again in binary64.  All in binary64, 16384 x 8192
-// takes 188 us instead of 165: about 45 instructions an element are what the
-// vector units do in the memory's time.
+// h = (h * r) * g.  For a 16-bit type, whose own rounding is 2^13 times as large or
+// more, two plain products, off by at most 3 * 2^-24 (r.hi's error among them); the
+// exact ones cost 1000 x 4100 fp16 8.1 us instead of 7.6.  Otherwise right to
+// binary32's last bit, unless h * r is below 2^-100, and then to its last few.  All
+// in binary64, 16384 x 8192 to 8 bits takes 188 us instead of 165: about 45
+// instructions an element are what the vector units do in the memory's time.
 template <int FY>
 __device__ __forceinline__ void products8(float (&h)[8], const Root& r, const float (&g)[8]) {
-  float v[8], p, q, least_p = r.ordinary ? __builtin_inff() : 0.0f, least_q = __builtin_inff();
-  uint32_t border = 0xFFFFFFFFu;
+  if (__builtin_expect(r.ordinary, 1)) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      h[k] = FY == AR_BF16 || FY == AR_F16 ? (h[k] * r.hi) * g[k] : Product(h[k], r, g[k]).nearest();
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) h[k] = product64<false>(h[k], r.r, g[k]);
+  }
+}
+
+// The same for an MX format.  A value that lies just beside a border between two
+// codes must not come out on its other side.  Borders, and powers of two, those of
+// the scales, have 19 trailing zeros in binary32: two plain products do for a
+// chunk without a value within kNear steps of such a place, which cover their
+// error and that of r.hi, 3 * 2^-24.  The others (0.8% of the waves' chunks of
+// random rows, and those with zeros) are rounded to odd, in binary64 where a
+// product that is not a zero of its own is small.
+constexpr uint32_t kNear = 4;
+__device__ __forceinline__ void products8_mx(float (&h)[8], const Root& r, const float (&g)[8]) {
+  float v[8], least_p = r.ordinary ? __builtin_inff() : 0.0f, least_q = __builtin_inff();
+  uint32_t near = 0xFFFFFFFFu;
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
-    v[k] = product<FY>(h[k], r, g[k], p, q);
+    const float p = h[k] * r.hi;
+    v[k] = p * g[k];
     least_p = fminf(least_p, fabsf(p));
-    least_q = fminf(least_q, fabsf(q));
-    if constexpr (has_borders<FY>()) border = min(border, from_border(v[k]));
+    least_q = fminf(least_q, fabsf(v[k]));
+    near = min(near, (__float_as_uint(v[k]) + kNear) & 0x7FFFFu);
   }
-  bool again = false;
-  if (__builtin_expect(least_p < 0x1p-100f || least_q < 0x1p-100f || border <= 2 * kNear, 0)) {
-    again = !r.ordinary;
+  if (__builtin_expect(least_p < 0x1p-100f || least_q < 0x1p-100f || near <= 2 * kNear, 0)) {
+    bool wide = !r.ordinary;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      float a = h[k];
-      __asm__("" : "+v"(a));                               // p and q anew, not held
-      product<FY>(a, r, g[k], p, q);
-      const bool small = fminf(fabsf(p), fabsf(q)) < 0x1p-100f;
-      const bool near = has_borders<FY>() && from_border(v[k]) <= 2 * kNear;
-      again = again || ((small || near) && h[k] != 0.0f && g[k] != 0.0f);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-  }
-  if (__builtin_expect(again, 0)) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      v[k] = product64<FY>(h[k], r.r, g[k]);
+      const Product x(h[k], r, g[k]);
+      v[k] = x.odd();
+      const bool small = fminf(fabsf(x.p), fabsf(x.q)) < 0x1p-100f && h[k] != 0.0f && g[k] != 0.0f;
+      wide = wide || small || !(fabsf(x.q) < __builtin_inff());
       __builtin_amdgcn_sched_barrier(0);                   // one at a time: few registers
+    }
+    if (__builtin_expect(wide, 0)) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        v[k] = product64<true>(h[k], r.r, g[k]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
   }
 #pragma unroll
@@ -225,9 +230,8 @@ __device__ __forceinline__ void norm_finish(const NormArgs& a, int64_t row, floa
       if (c < chunks) store8<FR>(hr, H, (int64_t)c * 8, h[i]);
     }
   }
-  // The sum and r are binary64, and 8- and 4-bit outputs round products that are
-  // right to the last bit of binary32: with binary32 steps throughout, a few of
-  // 4 million codes came out a step off.
+  // The sum and r are binary64: with binary32 steps throughout, a few of 4 million
+  // 8-bit codes came out a step off.
   double s = 0.0;
 #pragma unroll
   for (int i = 0; i < NI; ++i)
@@ -249,11 +253,7 @@ __device__ __forceinline__ void norm_finish(const NormArgs& a, int64_t row, floa
     const int left = (int)H - c * 8;                       // elements of the row from here on
     float g[8];
     gamma.get(a, i, g);
-    if constexpr (is_float_format(FY)) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        h[i][k] = r.ordinary ? (h[i][k] * r.hi) * g[k] : product64<FY>(h[i][k], r.r, g[k]);
-    } else {
+    if constexpr (is_mx_format(FY)) {
       if (left < 8) {                                      // zeros would be taken for small products
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
@@ -261,6 +261,8 @@ __device__ __forceinline__ void norm_finish(const NormArgs& a, int64_t row, floa
           g[k] = k < left ? g[k] : 1.0f;
         }
       }
+      products8_mx(h[i], r, g);
+    } else {
       products8<FY>(h[i], r, g);
     }
     // back to zeros; a row whose r is not finite makes NaN of zeros too

@@ -1,11 +1,11 @@
 """The residual norm where single roundings show: the ends of the range, and
 values beside the border between two codes.
 
-The kernel's r is right to 2^-50 and each product is rounded once in effect
-(products of the rows that binary32's range does not hold are binary64), so
-its outputs are those of the 64-bit form but where that lies within a few
-2^-50 of a border.  The 64-bit form's own sum and products are off by less than
-2^-48.  NEAR covers both.
+The kernel's r is right to 2^-50 and its products to 2^-46 before they are
+rounded (to binary32, or for the MX formats to odd, which keeps every border
+between two codes), so its outputs, those of 16-bit types apart, are those of the
+64-bit form but where that lies within 2^-46 of a border.  The 64-bit form's own sum and products are off by
+less than 2^-48.  NEAR covers both.
 """
 import numpy as np
 import pytest
@@ -130,3 +130,82 @@ def test_zeros_among_values(y_fmt):
     v = np.where(np.abs(v) >= 2.0 ** 128, np.inf, v)
     assert np.isinf(v[2, 130])
     check_quantized(y, y_fmt, v, NEAR)
+
+
+# significant bits, exponent of the smallest normal number, largest finite value
+TYPES = {"bf16": (8, -126, 2.0 ** 128 - 2.0 ** 120), "f16": (11, -14, 65504.0), "f32": (24, -126, 2.0 ** 128 - 2.0 ** 104)}
+
+
+def rounded(v, fmt):
+    """binary64 values to a float type, nearest even, in one rounding."""
+    bits, emin, largest = TYPES[fmt]
+    _, e = np.frexp(v)
+    step = np.ldexp(1.0, np.maximum(e - 1, emin) - bits + 1)
+    q = np.rint(v / step) * step                       # exact: a power of two
+    return np.where(np.abs(q) > largest, np.copysign(np.inf, q), q)
+
+
+def check_float_rows(y, v):
+    """Every output lies between the roundings of v a little smaller and larger:
+    for binary32 by the 64-bit form's own error, for 16-bit types by r's
+    rounding to binary32 and that of two products, 3 * 2^-24.  Below 2^-100 the
+    correction of binary32's last bit is lost: one step more."""
+    fmt = {k: f for f, k in abi.FORMATS.items()}[y.fmt]
+    got = y.data[:, :y.cols].double().cpu().numpy()
+    rel = np.where(np.abs(v) < 2.0 ** -100, 2.0 ** -22, NEAR) if fmt == "f32" else 3 * 2.0 ** -24
+    off = np.abs(v) * rel + np.where(np.abs(v) < 2.0 ** -100, 2.0 ** -149, 0.0)
+    with np.errstate(invalid="ignore"):
+        lo, hi = rounded(v - off, fmt), rounded(v + off, fmt)
+    bad = ~((got >= lo) & (got <= hi)) & ~(np.isnan(got) & np.isnan(v))
+    assert not bad.any(), (np.argwhere(bad)[:5], got[bad][:5], v[bad][:5])
+    assert untouched(y)
+
+
+@pytest.mark.parametrize("fmt,res_fmt", (("bf16", "bf16"), ("bf16", "f32"), ("f16", "f16"), ("f32", "f32")))
+@pytest.mark.parametrize("rows,cols", ((400, 4096), (60, 8200), (2000, 523), (70, 30011)))
+def test_float_rows(rows, cols, fmt, res_fmt):
+    rng = np.random.default_rng(rows + cols)
+    x = to_type(rng.standard_normal((rows, cols)), fmt)
+    res = to_type(rng.standard_normal((rows, cols)) * 2, res_fmt)
+    gamma = to_type(rng.uniform(0.5, 1.5, cols), fmt)
+    eps = np.float32(1e-5)
+    y = run(x, fmt, fmt, gamma=gamma, eps=float(eps), res=res, res_fmt=res_fmt)
+    h = (res.astype(np.float32) + x.astype(np.float32)).astype(np.float64)
+    check_float_rows(y, layer.norm(h, gamma, float(eps)))
+
+
+@pytest.mark.parametrize("s", (0, 100, -30, -95, -110, -124, -128, -134))
+@pytest.mark.parametrize("fmt", ("bf16", "f16", "f32"))
+def test_float_values_beside_borders(fmt, s):
+    """Of 40 gammas for each element the one whose product comes nearest to the
+    border between two neighbours of the type, in sizes from 2^100 to its
+    subnormal numbers."""
+    if fmt == "f16":
+        if s > 0 or s < -30:
+            pytest.skip("past the type's range")
+        s = max(s, -16)
+    rng = np.random.default_rng(300 + s)
+    cols = 32768
+    x = to_type(rng.uniform(1.0, 2.0, (1, cols)) * rng.choice([-1.0, 1.0], (1, cols)), fmt)
+    r = 1.0 / np.sqrt((x * x).sum() / cols)
+    bits, emin, _ = TYPES[fmt]
+    g = to_type(np.ldexp(rng.uniform(0.7, 1.4, (40, cols)), s), fmt)
+    step = np.ldexp(1.0, np.maximum(np.frexp(x * r * g)[1] - 1, emin) - bits + 1)
+    off = np.abs(x * r * g / step % 1.0 - 0.5)
+    gamma = g[off.argmin(0), np.arange(cols)]
+    y = run(x, fmt, fmt, gamma=gamma)
+    check_float_rows(y, layer.norm(x, gamma, 0.0))
+
+
+def test_infinite_products_are_infinite():
+    """v past the type's range, next to zeros."""
+    x = np.ones((1, 64))
+    x[0, 0], x[0, 1], x[0, 2] = 4.0, 0.0, -4.0
+    gamma = np.ones(64)
+    gamma[[0, 2, 5]] = 3.3e38
+    for fmt in ("bf16", "f32"):
+        xs, gs = to_type(x, fmt), to_type(gamma, fmt)
+        y = run(xs, fmt, fmt, gamma=gs)
+        check_float_rows(y, layer.norm(xs, gs, 0.0))
+        got = y.data[0, :64].double().cpu().numpy()
+        assert got[0] == np.inf and got[2] == -np.inf and got[1] == 0.0 and np.isfinite(got[5])
