@@ -173,6 +173,9 @@ inline hipError_t launch_typed(void (*kernel)(KArgs...), dim3 grid, dim3 block,
                          argv, 0, s);
 }
 
+// Workgroups that one launch takes: its threads are fewer than 2^32.
+inline int64_t most_blocks(int threads) { return ((int64_t(1) << 32) - 1) / threads; }
+
 // Every argument is converted to the kernel's own parameter type first.
 template <typename... KArgs, typename... Args>
 inline hipError_t launch(void (*kernel)(KArgs...), dim3 grid, dim3 block,

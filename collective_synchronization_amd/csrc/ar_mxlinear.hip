@@ -836,6 +836,47 @@ static hipError_t launch_linear_y(const MxLinArgs& a, int yf, int nranks, hipStr
                       : launch_linear<XF, AR_BF16>(a, nranks, s);
 }
 
+static hipError_t launch_linear_x(const MxLinArgs& a, int xf, int yf, int nranks, hipStream_t s) {
+  switch (xf) {
+    case AR_BF16: return launch_linear_y<AR_BF16>(a, yf, nranks, s);
+    case AR_E4M3_ROW: return launch_linear_y<AR_E4M3_ROW>(a, yf, nranks, s);
+    case AR_E4M3_MX: return launch_linear_y<AR_E4M3_MX>(a, yf, nranks, s);
+    default: return launch_linear_y<AR_E2M1_MX>(a, yf, nranks, s);
+  }
+}
+
+// Output the size of more than one launch (no kernel here has more than 512
+// threads for 16 x 16 outputs, unless its workgroups are few) goes by ranks, then by
+// halves of the longer side, in whole tiles.
+static hipError_t launch_pieces(const MxLinArgs& a, int xf, int yf, int nranks, hipStream_t s) {
+  const int64_t rows = ceil_div64(a.M, 16), outs = ceil_div64(a.N, 16);
+  if (rows * outs * nranks <= most_blocks(512)) return launch_linear_x(a, xf, yf, nranks, s);
+  const int64_t size = yf == AR_F32 ? 4 : 2;
+  auto from = [&](int r, int m, int n) {
+    MxLinArgs b = a;
+    b.x += r * a.x_rank + m * a.x_stride;
+    if (b.xs) b.xs += r * a.xs_rank + m * a.xs_stride;
+    b.w += r * a.w_rank + n * a.w_stride;
+    b.ws += r * a.ws_rank + n * a.ws_stride;
+    b.y = static_cast<uint8_t*>(a.y) + (r * a.y_rank + m * a.y_stride + n) * size;
+    b.M -= m;
+    b.N -= n;
+    return b;
+  };
+  hipError_t e = hipSuccess;
+  if (nranks > 1) {
+    for (int r = 0; r < nranks && e == hipSuccess; ++r) e = launch_pieces(from(r, 0, 0), xf, yf, 1, s);
+    return e;
+  }
+  const int m = rows >= outs ? (int)ceil_div64(a.M, 512) * 256 : 0;
+  const int n = rows >= outs ? 0 : (int)ceil_div64(a.N, 512) * 256;
+  MxLinArgs first = a;
+  if (m) first.M = m;
+  else first.N = n;
+  e = launch_pieces(first, xf, yf, 1, s);
+  return e == hipSuccess ? launch_pieces(from(0, m, n), xf, yf, 1, s) : e;
+}
+
 }  // namespace ar
 
 using namespace ar;
@@ -846,7 +887,6 @@ int ar_mx4_linear(const ar_linear_params* p, void* stream) {
   const int rc = check_linear(p);
   if (rc) return rc;
   if (p->rows == 0 || p->outputs == 0) return AR_OK;
-  // workgroups of the kernel with the smallest tiles
   const int64_t tiles = ceil_div64(p->outputs, 16) * ceil_div64(p->rows, 16) * p->nranks;
   if (tiles > INT32_MAX) return AR_ESIZE;
   MxLinArgs a{};
@@ -874,12 +914,7 @@ int ar_mx4_linear(const ar_linear_params* p, void* stream) {
   a.vec = aligned(p->y, p->y_format == AR_F32 ? 16 : 8) && p->y_stride % 4 == 0 &&
           (p->nranks == 1 || p->y_rank_stride % 4 == 0);
   hipStream_t s = static_cast<hipStream_t>(stream);
-  switch (p->x_format) {
-    case AR_BF16: return map_hip(launch_linear_y<AR_BF16>(a, p->y_format, p->nranks, s));
-    case AR_E4M3_ROW: return map_hip(launch_linear_y<AR_E4M3_ROW>(a, p->y_format, p->nranks, s));
-    case AR_E4M3_MX: return map_hip(launch_linear_y<AR_E4M3_MX>(a, p->y_format, p->nranks, s));
-    default: return map_hip(launch_linear_y<AR_E2M1_MX>(a, p->y_format, p->nranks, s));
-  }
+  return map_hip(launch_pieces(a, p->x_format, p->y_format, p->nranks, s));
 }
 
 }  // extern "C"

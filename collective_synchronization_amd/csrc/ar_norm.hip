@@ -19,6 +19,8 @@
 
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "../../include/ar.h"
 #include "ar_host.h"
 #include "ar_rows.h"
@@ -624,14 +626,29 @@ static NormArgs norm_args(const ar_norm_params* p) {
   return a;
 }
 
+// A workgroup a row: one launch, or several where the rows are more than it takes.
 template <int FX, int FR, int FY>
-static hipError_t launch_norm_ni(const NormArgs& a, int64_t rows, NormShape g, hipStream_t s) {
-  const dim3 grid((unsigned)rows), block(g.threads);
+static hipError_t launch_norm_ni(NormArgs a, int64_t rows, NormShape g, hipStream_t s) {
+  auto later = [](auto*& p, int64_t bytes) {
+    if (p) p = static_cast<std::remove_reference_t<decltype(p)>>((void*)((uintptr_t)p + bytes));
+  };
+  auto go = [&](void (*kernel)(NormArgs)) {
+    const int64_t most = most_blocks(g.threads);
+    for (;; rows -= most) {
+      const hipError_t e = launch(kernel, dim3((unsigned)(rows < most ? rows : most)), dim3(g.threads), s, a);
+      if (e != hipSuccess || rows <= most) return e;
+      later(a.x, most * format_bytes(FX, a.x_stride));
+      later(a.res, most * format_bytes(FR, a.res_stride));
+      later(a.h, most * format_bytes(FR, a.h_stride));
+      later(a.y, most * format_bytes(FY, a.y_stride));
+      later(a.scales, most * (FY == AR_E4M3_ROW ? 4 : a.scale_stride));
+    }
+  };
   switch (g.ni) {
-    case 1: return launch(k_residual_norm<FX, FR, FY, 1>, grid, block, s, a);
-    case 2: return launch(k_residual_norm<FX, FR, FY, 2>, grid, block, s, a);
-    case 4: return launch(k_residual_norm<FX, FR, FY, 4>, grid, block, s, a);
-    default: return launch(k_residual_norm<FX, FR, FY, 8>, grid, block, s, a);
+    case 1: return go(k_residual_norm<FX, FR, FY, 1>);
+    case 2: return go(k_residual_norm<FX, FR, FY, 2>);
+    case 4: return go(k_residual_norm<FX, FR, FY, 4>);
+    default: return go(k_residual_norm<FX, FR, FY, 8>);
   }
 }
 
@@ -709,6 +726,8 @@ int ar_reduce_norm(const ar_desc* d, void* scratch, const ar_norm_params* p, ar_
   if (d->count == 0) return AR_OK;
   if (p->hidden % 8 != 0) return AR_EALIGN;
   if (p->hidden > AR_REDUCE_NORM_MAX_HIDDEN) return AR_ESIZE;
+  const NormShape g = norm_shape(p->hidden);
+  if (p->rows * d->nconsumers > most_blocks(g.threads)) return AR_ESIZE;
   if (!scratch || !ctrl) return AR_EINVAL;
   if (!aligned(scratch, 256) || !aligned(ctrl, 256)) return AR_EALIGN;
   DeviceInfo di;
@@ -728,7 +747,6 @@ int ar_reduce_norm(const ar_desc* d, void* scratch, const ar_norm_params* p, ar_
   a.rearm = (flags & AR_FLAG_REARM) && d->proto == kSentinel;
   a.res_format = p->res_format;
   a.y_format = p->y_format;
-  const NormShape g = norm_shape(p->hidden);
   const unsigned blocks = (unsigned)(p->rows * d->nconsumers);
   hipStream_t s = static_cast<hipStream_t>(stream);
   hipError_t err;

@@ -240,6 +240,11 @@ __device__ __forceinline__ void store8_mx(uint8_t* __restrict__ row, uint8_t* __
 
 inline int64_t mx_blocks(int64_t cols) { return ceil_div64(cols, kMxBlock); }
 
+// Bytes of a stride in a format's units (elements, or bytes of codes).
+inline int64_t format_bytes(int32_t f, int64_t stride) {
+  return f == AR_F32 ? 4 * stride : (is_float_format(f) ? 2 * stride : stride);
+}
+
 // Bytes a row of `cols` elements takes in a format (its scales apart).
 inline int64_t format_row_bytes(int32_t f, int64_t cols) {
   switch (f) {
@@ -258,9 +263,8 @@ inline int64_t format_row_bytes(int32_t f, int64_t cols) {
 inline int check_format_rows(int32_t f, const void* p, int64_t stride, int64_t rows, int64_t cols) {
   if (rows == 0 || cols == 0) return AR_OK;
   if (!p) return AR_EINVAL;
-  const int64_t size = f == AR_F32 ? 4 : (is_float_format(f) ? 2 : 1);
   if (stride <= 0 || stride >= (int64_t(1) << 40)) return stride <= 0 ? AR_EINVAL : AR_ESIZE;
-  if (stride * size < format_row_bytes(f, cols)) return AR_EINVAL;
+  if (format_bytes(f, stride) < format_row_bytes(f, cols)) return AR_EINVAL;
   if (!aligned(p, 16) || stride % (is_float_format(f) ? 8 : 16) != 0) return AR_EALIGN;
   return AR_OK;
 }

@@ -427,8 +427,9 @@ int ar_residual_norm(const ar_norm_params* p, const void* x, int64_t x_stride, v
  *   d: AR_ALLREDUCE, any protocol; d->count = rows*hidden.
  *   p: format AR_BF16; hidden a multiple of 8 (AR_EALIGN) and at most
  *      AR_REDUCE_NORM_MAX_HIDDEN (AR_ESIZE).  Every row buffer holds
- *      nconsumers*rows rows, consumer c's from row c*rows on.  residual_out
- *      may be residual.
+ *      nconsumers*rows rows, consumer c's from row c*rows on.  A row takes
+ *      64 to 512 threads, and all of them are fewer than 2^32 (AR_ESIZE).
+ *      residual_out may be residual.
  *   scratch, e, ctrl, timeout_ns, flags and errors as for
  *   ar_reduce_validate; a row any of whose blocks failed is not written.
  */
@@ -484,7 +485,7 @@ typedef struct {
  * past `inputs` in rows of x and w does not count.  The order of every sum is
  * fixed by the sizes, so equal calls give equal bits.  inputs 0:
  * zeros are written; rows or outputs 0: nothing is.  AR_ESIZE: a size above
- * 2^30.
+ * 2^30, or 2^31 or more 16 x 16 tiles of all ranks' y.
  */
 int ar_mx4_linear(const ar_linear_params* p, void* stream);
 
