@@ -5,9 +5,10 @@
 //
 // 8- and 4-bit inputs go through the block-scaled matrix instruction, which
 // takes the e8m0 scales of both operands as they are; bf16 inputs through
-// the bf16 one, the weights converted in registers (every e2m1 value times a
-// power of two is a bf16 value).  The weights are the first operand, so a
-// lane ends with 4 consecutive outputs of one token.
+// the bf16 one, the weights converted in registers.  That is exact but at the top
+// of the scales: 4 and 6 under 2^127 and 6 under 2^126, 2^128 and more, are past
+// bf16's range (and binary32's) and become infinities.  The weights are the first
+// operand, so a lane ends with 4 consecutive outputs of one token.
 #include <hip/hip_runtime.h>
 
 #include <stdint.h>
@@ -81,10 +82,15 @@ constexpr int elem_bits() { return XF == AR_BF16 ? 16 : (XF == AR_E2M1_MX ? 4 : 
 
 // 16 bytes of an input row from element `at` on, with zeros at and past element
 // K: what lies there in x does not count, and then neither does what lies there
-// in w, whose values are finite.
+// in w, whose values are finite but for bf16 tokens (keep_weights).
 template <int XF>
 __device__ __forceinline__ u32x4 keep_inputs(u32x4 v, int64_t at, int64_t K) {
   return keep_bits(v, (K - at) * elem_bits<XF>());
+}
+
+// The same for 32 weights, which as bf16 may be infinite.
+__device__ __forceinline__ u32x4 keep_weights(u32x4 v, int64_t at, int64_t K) {
+  return keep_bits(v, (K - at) * 4);
 }
 
 // One lane's operands of a 512-element step: 4 blocks of K, one in each of 4
@@ -267,7 +273,14 @@ __global__ __launch_bounds__(kWave * WN * WK) void k_mx_linear_rows(MxLinArgs a)
   auto keep = [&](int st, Step& f) {
     if (st < full) return;
 #pragma unroll
-    for (int i = 0; i < NT; ++i) f.w[i].s = keep_scales(f.w[i].s, 16 * st, a.nb);
+    for (int i = 0; i < NT; ++i) {
+      f.w[i].s = keep_scales(f.w[i].s, 16 * st, a.nb);
+      if constexpr (XF == AR_BF16) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          f.w[i].d[q] = keep_weights(f.w[i].d[q], (int64_t)(16 * st + 4 * q + g) * 32, a.K);
+      }
+    }
     keep_step<XF>(st, g, a.nb, a.K, f.x);
   };
   auto compute = [&](const Step& f) {
@@ -464,7 +477,7 @@ __global__ __launch_bounds__(G::threads) void k_mx_linear_tiles(MxLinArgs a) {
       load_to_lds(wr, at + G::xbytes + (i * G::threads + wave * kWave) % G::pw * 16, wo[i],
                   (uint32_t)k * T::WB);
   };
-  // In a step that K ends in, once it has arrived: zeros for x past K.  (What
+  // In a step that K ends in, once it has arrived: zeros past K.  (What
   // was read there lies in the row, or in the next one, or is the zeros that a
   // read past the buffer's range gives.)
   auto keep_step = [&](int k, int buf) {
@@ -477,6 +490,17 @@ __global__ __launch_bounds__(G::threads) void k_mx_linear_tiles(MxLinArgs a) {
       const int64_t first = (int64_t)k * T::XB + place<T::XC>(row, slot % T::XC) * 16;  // byte of the row
       u32x4* p = reinterpret_cast<u32x4*>(at + slot * 16);
       *p = keep_inputs<XF>(*p, first * 8 / elem_bits<XF>(), a.K);
+    }
+    if constexpr (XF == AR_BF16) {
+#pragma unroll
+      for (int i = 0; i < (G::pw + G::threads - 1) / G::threads; ++i) {
+        const int slot = i * G::threads + tid;
+        if (slot >= G::pw) break;
+        const int row = slot / T::WC;
+        const int64_t first = (int64_t)k * T::WB + place<T::WC>(row, slot % T::WC) * 16;
+        u32x4* p = reinterpret_cast<u32x4*>(at + G::xbytes + slot * 16);
+        *p = keep_weights(*p, first * 2, a.K);
+      }
     }
   };
   // Scales of the run of steps that begins with step k: 16 of each row, those

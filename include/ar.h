@@ -482,7 +482,8 @@ typedef struct {
  * ranks may be slices of one row (x_rank_stride = inputs).  y: any stride
  * that holds a row, aligned to its element; it may not overlap the inputs,
  * nor the ranks' y each other.  A scale NaN makes its products NaN; what lies
- * past `inputs` in rows of x and w does not count.  The order of every sum is
+ * past `inputs` in rows of x and w does not count.  With AR_BF16 x, weights of
+ * 2^128 and more (4 and 6 under the scale 2^127, 6 under 2^126) are infinite.  The order of every sum is
  * fixed by the sizes, so equal calls give equal bits.  inputs 0:
  * zeros are written; rows or outputs 0: nothing is.  AR_ESIZE: a size above
  * 2^30, or 2^31 or more 16 x 16 tiles of all ranks' y.
