@@ -346,9 +346,9 @@ __global__ __launch_bounds__(kWave * WN * WK) void k_mx_linear_rows(MxLinArgs a)
 
 // 16 bytes a lane from the buffer straight into shared memory, at `lds` (the
 // wave's own address) + 16 * lane.
-__device__ __forceinline__ void load_to_lds(rsrc_t r, uint8_t* lds, uint32_t lane_off, uint32_t off) {
+__device__ __forceinline__ void load_to_lds(rsrc_t r, uint8_t* lds, uint32_t lane_off) {
   typedef __attribute__((address_space(3))) void lds_void;
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)lds, 16, lane_off, off, 0, 0);
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)lds, 16, lane_off, 0, 0, 0);
 }
 
 __device__ __forceinline__ void load_to_lds(const uint8_t* p, uint8_t* lds) {
@@ -455,7 +455,9 @@ __global__ __launch_bounds__(G::threads) void k_mx_linear_tiles(MxLinArgs a) {
   const int64_t wrange = min(nlast, BN - 1) * a.w_stride + (int64_t)a.nb * 16;
   const rsrc_t xr = make_rsrc(xbase, (uint32_t)xrange), wr = make_rsrc(wbase, (uint32_t)wrange);
 
-  // this thread's pieces of a step: source offsets at step 0
+  // This thread's pieces: source offsets in the next step to be loaded.  The step
+  // is part of them, not a scalar offset beside them: what ends a read at the
+  // buffer's range is sure to look at this one.
   uint32_t xo[G::nx], wo[G::nw];
 #pragma unroll
   for (int i = 0; i < G::nx; ++i) {
@@ -467,15 +469,18 @@ __global__ __launch_bounds__(G::threads) void k_mx_linear_tiles(MxLinArgs a) {
     const int at = (i * G::threads + tid) % G::pw, row = at / T::WC;
     wo[i] = (uint32_t)min(row, nlast) * (uint32_t)a.w_stride + place<T::WC>(row, at % T::WC) * 16;
   }
-  auto load_step = [&](int k, int buf) {
+  auto load_next = [&](int buf) {
     uint8_t* at = smem + buf * G::stage;
 #pragma unroll
-    for (int i = 0; i < G::nx; ++i)
-      load_to_lds(xr, at + (i * G::threads + wave * kWave) % G::px * 16, xo[i], (uint32_t)k * T::XB);
+    for (int i = 0; i < G::nx; ++i) {
+      load_to_lds(xr, at + (i * G::threads + wave * kWave) % G::px * 16, xo[i]);
+      xo[i] += T::XB;
+    }
 #pragma unroll
-    for (int i = 0; i < G::nw; ++i)
-      load_to_lds(wr, at + G::xbytes + (i * G::threads + wave * kWave) % G::pw * 16, wo[i],
-                  (uint32_t)k * T::WB);
+    for (int i = 0; i < G::nw; ++i) {
+      load_to_lds(wr, at + G::xbytes + (i * G::threads + wave * kWave) % G::pw * 16, wo[i]);
+      wo[i] += T::WB;
+    }
   };
   // In a step that K ends in, once it has arrived: zeros past K.  (What
   // was read there lies in the row, or in the next one, or is the zeros that a
@@ -625,7 +630,7 @@ __global__ __launch_bounds__(G::threads) void k_mx_linear_tiles(MxLinArgs a) {
 #pragma unroll
   for (int k = 0; k < NS - 1; ++k) {
     if (k < steps && k % T::steps_scales == 0) load_scales(k);
-    if (k < steps) load_step(k, k);
+    if (k < steps) load_next(k);
   }
   constexpr int behind = (NS - 2) * (G::nx + G::nw);
   constexpr int wait_behind = 0x0F70 | (behind & 15) | (behind >> 4) << 14;      // vmcnt alone
@@ -658,7 +663,7 @@ __global__ __launch_bounds__(G::threads) void k_mx_linear_tiles(MxLinArgs a) {
     for (int k = 0; k < full; ++k) {
       const int ahead = k + NS - 1;
       if (ahead < steps && ahead % T::steps_scales == 0) load_scales(ahead);
-      if (ahead < steps) load_step(ahead, buf == 0 ? NS - 1 : buf - 1);
+      if (ahead < steps) load_next(buf == 0 ? NS - 1 : buf - 1);
       Tokens x;
       Weights w[TI];
       read_tokens(k, 0, buf, x);
@@ -685,7 +690,7 @@ __global__ __launch_bounds__(G::threads) void k_mx_linear_tiles(MxLinArgs a) {
       // into the buffer of step k - 1, which every wave has left
       const int ahead = k + NS - 1;
       if (ahead < steps && ahead % T::steps_scales == 0) load_scales(ahead);
-      if (ahead < steps) load_step(ahead, buf == 0 ? NS - 1 : buf - 1);
+      if (ahead < steps) load_next(buf == 0 ? NS - 1 : buf - 1);
       compute(k, buf);
       if (++buf == NS) buf = 0;
     }
