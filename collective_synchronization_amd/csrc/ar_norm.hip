@@ -462,13 +462,13 @@ __global__ __launch_bounds__(kNormThreads) void k_reduce_norm(ReduceNormArgs a) 
   }
   float h[NI][8];
   int st = 0;
+  Waiter wt(a.timeout_ticks, a.ctrl);                      // one deadline for all of the wave's chunks
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
     const int64_t first = ((int64_t)i * threads + t) * 8;
     const bool active = first < H;
     const uint32_t e = (uint32_t)row * (uint32_t)H + (uint32_t)first;
     Raw8<P> raw[NMAX];
-    Waiter wt(a.timeout_ticks, a.ctrl);
     if (P == kLL128 && st == 0) {
       // the line flags first, the data only after they have been seen
       while (true) {

@@ -432,6 +432,7 @@ int ar_residual_norm(const ar_norm_params* p, const void* x, int64_t x_stride, v
  *      residual_out may be residual.
  *   scratch, e, ctrl, timeout_ns, flags and errors as for
  *   ar_reduce_validate; a row any of whose blocks failed is not written.
+ *   timeout_ns is a row's whole wait.
  */
 int ar_reduce_norm(const ar_desc* d, void* scratch, const ar_norm_params* p, ar_epoch e,
                    void* ctrl, uint64_t timeout_ns, int32_t flags, void* stream);
