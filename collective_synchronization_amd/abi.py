@@ -393,11 +393,15 @@ def norm_params(rows, hidden, eps, fmt, gamma, res_fmt, residual, residual_strid
                 residual_out, residual_out_stride, y_fmt, y, y_stride, scales=None,
                 scale_stride=0) -> ar_norm_params:
     """The norm of ar_residual_norm and ar_reduce_norm: formats by name or id
-    (FORMATS); gamma, residual and residual_out may be None."""
-    g, r, h, o, s = _gpu_ptrs("norm_params", gamma, residual, residual_out, y, scales)
-    return ar_norm_params(rows, hidden, eps, format_id(fmt), g, format_id(res_fmt),
-                          format_id(y_fmt), r, residual_stride, h, residual_out_stride, o,
-                          y_stride, s, scale_stride, 0)
+    (FORMATS); gamma, residual and residual_out may be None.  The result keeps
+    the tensors; their types and sizes are not looked at."""
+    tensors = gamma, residual, residual_out, y, scales
+    g, r, h, o, s = _gpu_ptrs("norm_params", *tensors)
+    p = ar_norm_params(rows, hidden, eps, format_id(fmt), g, format_id(res_fmt),
+                       format_id(y_fmt), r, residual_stride, h, residual_out_stride, o,
+                       y_stride, s, scale_stride, 0)
+    p.tensors = tensors
+    return p
 
 
 def ar_residual_norm(params: ar_norm_params, x, x_stride, stream=None) -> None:
@@ -434,12 +438,16 @@ def linear_params(nranks, rows, outputs, inputs, x_fmt, x, x_stride, x_rank_stri
                   w_scale_stride, w_scale_rank_stride, y_fmt, y, y_stride,
                   y_rank_stride) -> ar_linear_params:
     """One ar_mx4_linear: y_r [rows, outputs] = x_r [rows, inputs] times the
-    transpose of w_r [outputs, inputs] for every rank."""
-    x, xs, w, ws, y = _gpu_ptrs("linear_params", x, x_scales, w, w_scales, y)
-    return ar_linear_params(nranks, 0, rows, outputs, inputs, format_id(x_fmt), format_id(y_fmt),
-                            x, x_stride, x_rank_stride, xs, x_scale_stride, x_scale_rank_stride,
-                            w, w_stride, w_rank_stride, ws, w_scale_stride, w_scale_rank_stride,
-                            y, y_stride, y_rank_stride)
+    transpose of w_r [outputs, inputs] for every rank.  The result keeps the
+    tensors; their types and sizes are not looked at."""
+    tensors = x, x_scales, w, w_scales, y
+    x, xs, w, ws, y = _gpu_ptrs("linear_params", *tensors)
+    p = ar_linear_params(nranks, 0, rows, outputs, inputs, format_id(x_fmt), format_id(y_fmt),
+                         x, x_stride, x_rank_stride, xs, x_scale_stride, x_scale_rank_stride,
+                         w, w_stride, w_rank_stride, ws, w_scale_stride, w_scale_rank_stride,
+                         y, y_stride, y_rank_stride)
+    p.tensors = tensors
+    return p
 
 
 def ar_mx4_linear(params: ar_linear_params, stream=None) -> None:
