@@ -214,8 +214,9 @@ def _ptr(x) -> Optional[int]:
     return x.data_ptr()
 
 
-_current_device = torch._C._cuda_getDevice
-_current_stream = torch._C._cuda_getCurrentRawStream
+# (a torch that was built without a GPU has neither; no call on a GPU gets here then)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _gpu_ptrs(where: str, *xs):

@@ -1,10 +1,15 @@
 """The binding of the layer operators, without a GPU."""
 import gc
+import os
+import subprocess
+import sys
 import weakref
 
 import pytest
 
 from collective_synchronization_amd import abi
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 class Held:
@@ -46,3 +51,22 @@ def test_parameters_keep_their_tensors(make, device):
     del p
     gc.collect()
     assert all(r() is None for r in refs)
+
+
+def test_import_without_gpu_names_in_torch():
+    """A torch built for the CPU alone: the module is there, a tensor that is
+    not on a GPU is refused as always."""
+    code = """
+import torch
+for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+    delattr(torch._C, name)
+from collective_synchronization_amd import abi
+assert abi.ar_slot_bytes("ll", 8) > 0
+try:
+    abi.norm_params(1, 8, 0.0, "f32", None, "f32", None, 0, None, 0, "f32", torch.zeros(1, 8), 8)
+except abi.ArError as e:
+    assert e.code == abi.AR_EINVAL
+else:
+    raise SystemExit("not refused")
+"""
+    subprocess.run([sys.executable, "-c", code], cwd=ROOT, check=True, timeout=120)
