@@ -230,8 +230,9 @@ __device__ __forceinline__ void store_out4(void* y, int64_t at, int n, int N, bo
 // Up to 16 tokens: bound by the stream of weights.  A wave holds 16 * NT outputs
 // and the tokens; WK waves split K step by step and join their sums, in order,
 // in shared memory.  The next step's operands are on their way while one is
-// multiplied.  4 shards of 8192 x 2048, 8-bit: one token 8.4 us, 4.2 TB/s with
-// the launch, which takes 2; 8 tokens 9.8; 8 shards of 4096 x 512, bf16: 4.3.
+// multiplied.  4 shards of 8192 x 2048, 8-bit: one token 10.3 us with the weights
+// in HBM, 3.5 TB/s with the launch, which takes 2, and 8.7 with them in the last
+// cache; 8 tokens 11.4 and 10.0; 8 shards of 4096 x 512, bf16: 5.3 and 4.3.
 template <int XF, int YF, int NT, int WN, int WK>
 __global__ __launch_bounds__(kWave * WN * WK) void k_mx_linear_rows(MxLinArgs a) {
   __shared__ f32x4 part[WK > 1 ? WK * WN * NT * kWave : 1];
@@ -341,11 +342,13 @@ __global__ __launch_bounds__(kWave * WN * WK) void k_mx_linear_rows(MxLinArgs a)
 // row so that the lanes that read at once meet different banks; the loads apply
 // the permutation to their addresses.  Scales come 512 elements of K at a time,
 // one row a lane.
-// 4096 x 8192 x 8192: 8-bit tokens 204 us (2.7 PFLOP/s), 4-bit 162 (3.4), bf16
-// 375 (1.46).  With 8-bit tokens the matrix cores are busy 63% of the time.  In
-// a form of 208 us, the operands' way into shared memory and registers took 178 us
-// without any product, the products 141 without operands: they overlap in part
-// only, and the two steps on their way are all that shared memory holds.
+// 4096 x 8192 x 8192: 8-bit tokens 198 to 217 us from run to run (2.5 to 2.8
+// PFLOP/s), 4-bit 162 to 180 (3.1 to 3.4), bf16 375 to 405 (1.36 to 1.46); the
+// instructions alone, on registers, do 4.6, 8.3 and 2.2.  With 8-bit tokens the
+// matrix cores are busy 62% of the time.  In a form of 208 us, the operands' way
+// into shared memory and registers took 178 us without any product, the products
+// 141 without operands: they overlap in part only, and the two steps on their way
+// are all that shared memory holds.
 
 // 16 bytes a lane from the buffer straight into shared memory, at `lds` (the
 // wave's own address) + 16 * lane.
@@ -783,9 +786,10 @@ static int check_linear(const ar_linear_params* p) {
 // Up to 16 tokens.  Waves of 32 outputs read x half as often as waves of 16,
 // and K is split until 2048 waves (two for each SIMD) share the stream of
 // weights; where even 8 parts do not give that many, waves take 16 outputs.
-// 16 tokens, 8-bit, 4 x 8192 x 2048: 11.1 us with 32 outputs, 14.3 with 16; one
-// token, 4096 x 4096: 3.9 us with 16 outputs and 4 parts, 5.4 with 32 and 8; 16
-// tokens, 8192 x 8192: 11.3 us with 8 parts, 11.9 with 4, 19 with 2.
+// With the weights in the last cache: 16 tokens, 8-bit, 4 x 8192 x 2048: 11.1 us
+// with 32 outputs, 14.3 with 16; one token, 4096 x 4096: 3.9 us with 16 outputs and
+// 4 parts, 5.4 with 32 and 8; 16 tokens, 8192 x 8192: 11.3 us with 8 parts, 11.9
+// with 4, 19 with 2.
 constexpr int64_t kRowsWaves = 2048;
 
 template <int XF, int YF, int NT>
@@ -822,7 +826,8 @@ static hipError_t launch_tiles(const MxLinArgs& a0, int nranks, hipStream_t s) {
 // where the smallest tiles are more than the CUs (256).  Among tiles the largest
 // that gives every CU one and is at least half full of tokens; tiles of 32
 // tokens with K shared by 4 groups of waves where even those are not more than
-// the CUs.  Measured both ways, 8-bit tokens, in us:
+// the CUs.  Measured both ways, 8-bit tokens, weights in the last cache but for the
+// 131072 outputs (290 MB), in us:
 //   32 x 64 tiles against waves on rows: 4 x 16 x 8192 x 2048 9.7 and 11.2, with
 //   9 tokens 9.7 and 10.0, 8 9.5 and 9.8, 4 9.3 and 8.8; 16 x 8192 x 8192 (128
 //   tiles) 15.9 and 11.5; bf16, 4 x 16 x 8192 x 2048 14.8 and 14.9, 12 14.8 and

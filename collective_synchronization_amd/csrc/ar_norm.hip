@@ -9,9 +9,9 @@
 //
 // What bounds it: for many rows the memory system (x and the residual read
 // once, both outputs written once; a row stays in registers between the sum
-// and the scaling): 16384 x 8192, bf16, to 8-bit blocks 162 us, 5.8 TB/s, to
+// and the scaling): 16384 x 8192, bf16, to 8-bit blocks 164 us, 5.8 TB/s, to
 // bf16 180 us, 6.0 TB/s, where a plain copy reaches 5.1.  For few rows the launch
-// and one trip to memory: one row of 4096 3.0 us.  One
+// and one trip to memory: one row of 4096 2.9 us.  One
 // workgroup a row: 8 consecutive elements a thread and step, so a wave reads
 // 1 KiB of a 16-bit row in one instruction, and the 4 lanes of an aligned
 // group hold one 32-element block of the MX formats.
@@ -430,9 +430,11 @@ __device__ __forceinline__ void reduce_finish(const ReduceNormArgs& a, int64_t r
 // of every rank until they carry their evidence (in whatever order the
 // blocks arrive), adds them in rank order in binary32 and goes on with the
 // norm; the sum is never rounded or written.
-// 8 ranks, [1,4096], LL, to 8-bit blocks: 7.6 us (and 2.4 for the pack); 16 ranks,
-// [8,4096], sentinel, to 8 bits a row: 9.9 (and 2.6).  Bound by one CU's read of
-// its row from every rank, 128 KiB in both, past the L2.  A row stays in one
+// 8 ranks, [1,4096], to 8-bit blocks: LL 7.6 us, LL128 6.8, sentinel 5.8, plain
+// 4.2 (and 2.4 to 2.8 for the pack); 16 ranks, [8,4096], to 8 bits a row: 12.5, 11.8,
+// 9.5, 6.5.  Plain slots are as long as the sentinel's, so in the 16-rank case 3 us
+// are checks and re-arming; LL reads twice as much.  The rest is one CU's read of
+// its row from every rank, past the L2, and the norm.  A row stays in one
 // workgroup all the same: sharing it would put an exchange of sums between
 // workgroups, which then must all be resident, into every row.
 template <int P, int NMAX, int NI>
