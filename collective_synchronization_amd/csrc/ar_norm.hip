@@ -156,9 +156,9 @@ __device__ __forceinline__ float product64(float a, double r, float b) {
 // h = (h * r) * g.  For a 16-bit type, whose own rounding is 2^13 times as large or
 // more, two plain products, off by at most 3 * 2^-24 (r.hi's error among them); the
 // exact ones cost 1000 x 4100 fp16 8.1 us instead of 7.6.  Otherwise right to
-// binary32's last bit, unless h * r is below 2^-100, and then to its last few.  All
-// in binary64, 16384 x 8192 to 8 bits takes 188 us instead of 165: about 45
-// instructions an element are what the vector units do in the memory's time.
+// binary32's last bit, unless h * r or the result is below 2^-100.  All in binary64,
+// 16384 x 8192 to 8 bits takes 188 us instead of 165: about 45 instructions an
+// element are what the vector units do in the memory's time.
 template <int FY>
 __device__ __forceinline__ void products8(float (&h)[8], const Root& r, const float (&g)[8]) {
   if (__builtin_expect(r.ordinary, 1)) {

@@ -408,8 +408,9 @@ typedef struct {
  * with h in binary32 and the sum and r in binary64.  residual_out is h rounded
  * once to its format.  y: MX codes and scales are those of v itself; AR_F32 is v
  * rounded once, and AR_E4M3_ROW takes v so rounded; AR_BF16 and AR_F16 round v
- * known to 3 * 2^-24 of itself.  (But for MX, where h*r or v is below 2^-100 the
- * last few bits of binary32 may be off.)  A v beyond binary32's range is infinite.
+ * known to 3 * 2^-24 of itself.  (Not so for MX: where h*r is below 2^-126 it is
+ * rounded to binary32's subnormal numbers before gamma, and where it or v is below
+ * 2^-100 binary32's last bit may be off.)  A v beyond binary32's range is infinite.
  * x: device, rows at x + i*x_stride elements.  y and residual_out may be x
  * where formats and strides agree; other overlaps are not allowed.  The
  * order of the sum is fixed by the shape, so equal calls give equal bits.
