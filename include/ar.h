@@ -481,9 +481,9 @@ typedef struct {
  * bits below the exponent of the largest: each of the others may lose up to
  * 2^-13 of that one (off by 1.3 to 5.4 * 2^-24 of sum |x*w| in the mean, for
  * rows of normal numbers and inputs of 8192 to 512; more where a few values
- * stand out).  AR_BF16 and AR_E2M1_MX x lose nothing there; 8-bit rows become
- * bf16 rows without loss (ar_dequantize_mx, or their codes with the row's
- * scale left for y).  It is the producer of one all-reduce: with y_stride = outputs and
+ * stand out).  AR_BF16 and AR_E2M1_MX x lose nothing there; 8-bit rows within
+ * bf16's range become bf16 rows without loss (ar_dequantize_mx, or their codes
+ * with the row's scale left for y).  It is the producer of one all-reduce: with y_stride = outputs and
  * y_rank_stride a row stride of ar_pack_*, rank r's y is its payload.
  * Strides of x and w as for their formats; rank strides in the same units
  * and with the same alignment, 0 where the ranks share a tensor.  x of all
