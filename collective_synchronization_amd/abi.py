@@ -42,6 +42,7 @@ FORMATS = {"bf16": AR_BF16, "f16": AR_F16, "f32": AR_F32, "row8": AR_E4M3_ROW,
            "mx8": AR_E4M3_MX, "mx4": AR_E2M1_MX}
 AR_NORM_MAX_HIDDEN = 32768
 AR_REDUCE_NORM_MAX_HIDDEN = 16384
+AR_CACHE_MAX_DIM = 256
 
 
 class ar_desc(ctypes.Structure):
@@ -92,6 +93,30 @@ class ar_linear_params(ctypes.Structure):
                 ("w_scales", ctypes.c_void_p), ("w_scale_stride", ctypes.c_int64),
                 ("w_scale_rank_stride", ctypes.c_int64), ("y", ctypes.c_void_p),
                 ("y_stride", ctypes.c_int64), ("y_rank_stride", ctypes.c_int64)]
+
+
+class ar_kv_cache(ctypes.Structure):
+    _fields_ = [("format", ctypes.c_int32), ("page", ctypes.c_int32),
+                ("pages", ctypes.c_int64), ("kv_heads", ctypes.c_int32),
+                ("dim", ctypes.c_int32), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("page_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("k_scales", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("scale_page_stride", ctypes.c_int64),
+                ("scale_token_stride", ctypes.c_int64), ("scale_head_stride", ctypes.c_int64)]
+
+
+class ar_attention_params(ctypes.Structure):
+    _fields_ = [("cache", ar_kv_cache), ("sequences", ctypes.c_int64),
+                ("queries", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("format", ctypes.c_int32),
+                ("q", ctypes.c_void_p), ("q_stride", ctypes.c_int64),
+                ("q_head_stride", ctypes.c_int64), ("out", ctypes.c_void_p),
+                ("out_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64),
+                ("lse", ctypes.c_void_p), ("lse_stride", ctypes.c_int64),
+                ("prefix", ctypes.c_int64), ("prefix_pages", ctypes.c_void_p),
+                ("lengths", ctypes.c_void_p), ("pages", ctypes.c_void_p),
+                ("pages_stride", ctypes.c_int64), ("max_pages", ctypes.c_int64),
+                ("reserved", ctypes.c_int32)]
 
 
 class ar_cost_entry(ctypes.Structure):
@@ -160,6 +185,10 @@ _SIGS = {
     "ar_dequantize_mx": ([_i64, _i64, _i32, _vp, _i64, _vp, _i64, _i32, _vp, _i64, _vp],
                          ctypes.c_int),
     "ar_mx4_linear": ([ctypes.POINTER(ar_linear_params), _vp], ctypes.c_int),
+    "ar_cache_append": ([ctypes.POINTER(ar_kv_cache), _i64, _i32, _i32, _vp, _i64, _i64, _vp, _i64,
+                         _i64, _vp, _vp, _i64, _i64, _vp], ctypes.c_int),
+    "ar_prefix_attention": ([ctypes.POINTER(ar_attention_params), _vp, _i64, _vp], ctypes.c_int),
+    "ar_prefix_attention_work_bytes": ([ctypes.POINTER(ar_attention_params)], _i64),
     "ar_sim_run": ([ctypes.POINTER(ar_sim_params), _vp], ctypes.c_int),
     "ar_sim_run_static": ([ctypes.POINTER(ar_sim_params), _vp, _vp], ctypes.c_int),
     "ar_sim_chain_run": ([ctypes.POINTER(ar_sim_params), _vp, _vp], ctypes.c_int),
@@ -453,6 +482,56 @@ def linear_params(nranks, rows, outputs, inputs, x_fmt, x, x_stride, x_rank_stri
 
 def ar_mx4_linear(params: ar_linear_params, stream=None) -> None:
     _check(_lib.ar_mx4_linear(ctypes.byref(params), _stream(stream)), "ar_mx4_linear")
+
+
+def cache_params(fmt, pages, page, kv_heads, dim, k, v, page_stride, token_stride, head_stride,
+                 k_scales=None, v_scales=None, scale_page_stride=0, scale_token_stride=0,
+                 scale_head_stride=0) -> ar_kv_cache:
+    """A paged cache of keys and values (buffers.PagedCache allocates one).  The
+    result keeps the tensors; their types and sizes are not looked at."""
+    tensors = k, v, k_scales, v_scales
+    k, v, ks, vs = _gpu_ptrs("cache_params", *tensors)
+    c = ar_kv_cache(format_id(fmt), page, pages, kv_heads, dim, k, v, page_stride, token_stride,
+                    head_stride, ks, vs, scale_page_stride, scale_token_stride, scale_head_stride)
+    c.tensors = tensors
+    return c
+
+
+def ar_cache_append(cache: ar_kv_cache, sequences, queries, fmt, k, k_stride, k_head_stride, v,
+                    v_stride, v_head_stride, lengths, pages, pages_stride, max_pages,
+                    stream=None) -> None:
+    k, v, lengths, pages = _gpu_ptrs("ar_cache_append", k, v, lengths, pages)
+    _check(_lib.ar_cache_append(ctypes.byref(cache), sequences, queries, format_id(fmt), k, k_stride,
+                                k_head_stride, v, v_stride, v_head_stride, lengths, pages,
+                                pages_stride, max_pages, _stream(stream)), "ar_cache_append")
+
+
+def attention_params(cache: ar_kv_cache, sequences, queries, heads, scale, fmt, q, q_stride,
+                     q_head_stride, out, out_stride, out_head_stride, lse, lse_stride, prefix,
+                     prefix_pages, lengths, pages, pages_stride, max_pages) -> ar_attention_params:
+    """One ar_prefix_attention; lse may be None.  The result keeps the tensors,
+    the cache's among them; their types and sizes are not looked at."""
+    tensors = q, out, lse, prefix_pages, lengths, pages
+    q, out, lse, prefix_pages, lengths, pages = _gpu_ptrs("attention_params", *tensors)
+    p = ar_attention_params(cache, sequences, queries, heads, scale, format_id(fmt), q, q_stride,
+                            q_head_stride, out, out_stride, out_head_stride, lse, lse_stride,
+                            prefix, prefix_pages, lengths, pages, pages_stride, max_pages, 0)
+    p.tensors = tensors + getattr(cache, "tensors", ())
+    return p
+
+
+def ar_prefix_attention_work_bytes(params: ar_attention_params) -> int:
+    return _check(_lib.ar_prefix_attention_work_bytes(ctypes.byref(params)),
+                  "ar_prefix_attention_work_bytes")
+
+
+def ar_prefix_attention(params: ar_attention_params, work, stream=None) -> None:
+    """work: a device tensor of at least ar_prefix_attention_work_bytes(params)
+    bytes, of this call alone while it runs (None where that is 0)."""
+    w, = _gpu_ptrs("ar_prefix_attention", work)
+    nbytes = 0 if work is None else work.numel() * work.element_size()
+    _check(_lib.ar_prefix_attention(ctypes.byref(params), w, nbytes, _stream(stream)),
+           "ar_prefix_attention")
 
 
 def sim_params(desc, nops, inp, in_stride, out, out_stride, scratch, ctrl, epoch,

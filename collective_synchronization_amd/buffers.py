@@ -71,6 +71,45 @@ class FormatRows:
             self.scales = torch.zeros((rows, self.scale_stride), dtype=torch.uint8, device=device)
 
 
+class PagedCache:
+    """A paged cache of keys and values on a device, [pages, page, kv_heads, dim]
+    of bf16 or f16, or of e4m3 codes with a binary32 scale for each row (fmt
+    "row8"), zero-filled; `params` is what the C ABI takes."""
+
+    def __init__(self, pages: int, page: int, kv_heads: int, dim: int, fmt, device="cuda"):
+        self.fmt = abi.format_id(fmt)
+        if self.fmt not in (abi.AR_BF16, abi.AR_F16, abi.AR_E4M3_ROW):
+            raise ValueError(f"no cache of format {fmt}")
+        dtype = {abi.AR_BF16: torch.bfloat16, abi.AR_F16: torch.float16}.get(self.fmt, torch.uint8)
+        self.pages, self.page, self.kv_heads, self.dim = pages, page, kv_heads, dim
+        self.k = torch.zeros((pages, page, kv_heads, dim), dtype=dtype, device=device)
+        self.v = torch.zeros_like(self.k)
+        self.k_scales = self.v_scales = None
+        strides = ()
+        if self.fmt == abi.AR_E4M3_ROW:
+            self.k_scales = torch.zeros((pages, page, kv_heads), dtype=torch.float32, device=device)
+            self.v_scales = torch.zeros_like(self.k_scales)
+            strides = self.k_scales.stride()
+        self.params = abi.cache_params(self.fmt, pages, page, kv_heads, dim, self.k, self.v,
+                                       *self.k.stride()[:3], self.k_scales, self.v_scales, *strides)
+
+    def append(self, k, v, lengths, pages, stream=None) -> None:
+        """A step's keys and values, [sequences * queries, kv_heads, dim] each:
+        the last tokens of sequences of `lengths` tokens (int32) on `pages`
+        (int32 [sequences, pages of each])."""
+        fmt = {torch.bfloat16: abi.AR_BF16, torch.float16: abi.AR_F16}.get(k.dtype)
+        sequences = pages.shape[0]
+        if fmt is None or v.dtype != k.dtype or k.shape != v.shape or sequences == 0 or \
+                k.shape[0] % sequences or k.shape[1:] != (self.kv_heads, self.dim) or \
+                lengths.dtype != torch.int32 or pages.dtype != torch.int32 or \
+                lengths.numel() != sequences or \
+                k.stride(2) != 1 or v.stride(2) != 1 or pages.stride(1) != 1 or lengths.stride(0) != 1:
+            raise ValueError("append: types or shapes that do not fit the cache")
+        abi.ar_cache_append(self.params, sequences, k.shape[0] // sequences, fmt, k, k.stride(0),
+                            k.stride(1), v, v.stride(0), v.stride(1), lengths, pages,
+                            pages.stride(0), pages.shape[1], stream)
+
+
 class Workspace:
     """Receive buffers and control block for one descriptor on one device.
 

@@ -1,0 +1,894 @@
+// ar_attention.hip -- decode attention over a shared prefix and every sequence's
+// own tokens, both in one paged cache (gfx950):
+//     out = softmax(scale * q K^T) V
+// The sequences of a batch that share a prefix are, for each head of the cache,
+// many rows of one product with the same keys: those keys are read once, for
+// all of them.  A sequence's own tokens meet the heads of its group alone.
+//
+// Two kernels.  The first one takes ranges of keys, prefix and own ones in one
+// launch, and leaves for each row and range the sum of its values under the
+// weights 2^(s - r), the sum l of those weights and the reference r; the second
+// joins a row's ranges.
+// Scores are kept in units of log2: s = q.k * scale * log2(e).
+//
+// The products take keys as their first operand, so a lane holds scores of one
+// row (its column), and those registers are the second operand of the product
+// with the values as they are: keys may be summed in any order, and the values
+// are read from shared memory, transposed on the way, in the order that the
+// scores came in.  Sums, maxima and the joined outputs are binary32; the weights
+// are rounded to 16 bits for the matrix cores, which is what their operands
+// are: each by at most half a step, and their sum l is of the unrounded ones.
+#include <hip/hip_runtime.h>
+
+#include <stdint.h>
+
+#include "../../include/ar.h"
+#include "ar_cache.h"
+#include "ar_host.h"
+#include "ar_rows.h"
+
+namespace ar {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kAttnThreads = 256;
+constexpr int kAttnWaves = kAttnThreads / kWave;
+constexpr int kTileRows = 32 * kAttnWaves;   // rows of a workgroup in the tile form
+constexpr int kFewRows = 16;                 // up to these, the other form
+
+// Strides in bytes for the cache, in elements for q, out and lse.
+struct AttnArgs {
+  CacheView kv;
+  const uint8_t* q;
+  int64_t q_stride, q_head;
+  void* out;
+  int64_t out_stride, out_head;
+  float* lse;
+  int64_t lse_stride;
+  const int32_t* prefix_pages;
+  const int32_t* lengths;
+  const int32_t* tables;
+  int64_t table_stride;
+  float* part_o;                     // [parts][rows][dim]
+  float* part_m;                     // [parts][rows][2]: r, l
+  float c;                           // scale * log2(e)
+  int32_t prefix, capacity;          // tokens shared, and most own ones
+  int32_t sequences, queries, heads, group;
+  int32_t rows;                      // sequences * queries * heads
+  int32_t prefix_splits, prefix_chunk, prefix_tiles, prefix_blocks;
+  int32_t own_splits, own_tiles, own_blocks;
+};
+
+// ------------------------------------------------------- 16-bit operands ---
+
+template <int F>
+__device__ __forceinline__ f32x16 mma32(u32x4 a, u32x4 b, f32x16 c) {
+  if constexpr (F == AR_BF16)
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+template <int F>
+__device__ __forceinline__ f32x4 mma16(u32x4 a, u32x4 b, f32x4 c) {
+  if constexpr (F == AR_BF16)
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+
+// Two values of a 16-bit type, nearest even.
+template <int F>
+__device__ __forceinline__ uint32_t pair16(float lo, float hi) {
+  if constexpr (F == AR_BF16) return bf16_pair(lo, hi);
+  else return __builtin_bit_cast(uint32_t, f16x2{(_Float16)lo, (_Float16)hi});
+}
+
+// ... and what they leave of binary32 values, in the same type.
+template <int F>
+__device__ __forceinline__ uint32_t rest16(float lo, float hi, uint32_t pair) {
+  static_assert(F == AR_BF16, "");
+  return bf16_pair(lo - bf_lo(pair), hi - bf_hi(pair));
+}
+
+// 8 e4m3 codes in a 16-bit type, without loss.
+template <int F>
+__device__ __forceinline__ u32x4 wide8(uint32_t lo, uint32_t hi) {
+  if constexpr (F == AR_BF16)
+    return u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true))};
+  else
+    return u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, false)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, true)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, false)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, true))};
+}
+
+// 4 consecutive rows' elements of one column: lane i of 16 names row i / 4,
+// columns 4 * (i % 4) on, and receives column i.
+__device__ __forceinline__ u32x2 read_transposed(const uint8_t* p) {
+  typedef __attribute__((address_space(3))) s16x4 lds_t;
+  return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t*)p));
+}
+
+__device__ __forceinline__ float other_half_max(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float other_half_sum(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+__device__ __forceinline__ float other_row_max(float v) {     // lanes l and l ^ 16
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float other_row_sum(float v) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// Where the maximum of a row has grown by less than 2^kSlack since the weights'
+// reference was taken, the reference stays: no sum has to be scaled, and the
+// weights stay below 2^kSlack.  In fp16 they are 2^kF16Up times as large, so
+// that those down to 2^-30 of the largest keep their bits.
+constexpr float kSlack = 8.0f;
+constexpr float kF16Up = 6.0f;
+template <int F> constexpr float weights_up() { return F == AR_F16 ? kF16Up : 0.0f; }
+
+constexpr int pow2_up(int n) { int p = 1; while (p < n) p *= 2; return p; }
+
+// What a workgroup works on: `rows` rows that meet the same keys [k0, k1).
+struct Piece {
+  const int32_t* table;
+  int32_t kh;                        // head of the cache
+  int32_t k0, k1;
+  int32_t rows, row0;                // and the first one of this workgroup
+  int32_t token0;                    // token of row 0
+  int32_t limit0;                    // keys that the first token sees, one more with each next ...
+  bool causal;                       // ... or all of them the same
+  int32_t part;
+};
+
+// ---------------------------------------------------------------- forms ---
+
+template <int QF, bool C8, int DT>
+struct Attn {
+  static constexpr int VF = C8 ? AR_BF16 : QF;             // type of weights and values
+  // Weights times the scales of 8-bit values can have any exponent, so they are
+  // bf16; for fp16 outputs in two parts, since one alone has 3 bits too few.
+  static constexpr bool two = C8 && QF == AR_F16;
+  static constexpr int KT = DT > 128 ? 32 : 64;            // keys of a tile
+  static constexpr int CB = C8 ? 16 : 8;                   // elements of 16 bytes of the cache
+  static constexpr int CH = pow2_up(DT / CB);              // lanes to a row
+  static constexpr int wave_keys = kWave / CH;             // rows that a wave loads at once: at most 16, on one page
+  static constexpr int passes = KT * CH / kAttnThreads;
+  // Rows in shared memory: 16 rows' 16-byte reads, and 8 rows' 32-byte ones,
+  // fall into different banks.
+  static constexpr int KS = DT * 2 + 16, VS = DT * 2 + 32;
+  static constexpr int tile = KT * (KS + VS) + (C8 ? KT * 8 : 0);
+  static constexpr int few_wave = 32 * VS + (C8 ? 32 * 8 : 0);
+  static constexpr int few_join = kAttnWaves * (16 * DT * 4 + 16 * 8);
+  static constexpr int few = kAttnWaves * few_wave > few_join ? kAttnWaves * few_wave : few_join;
+  static constexpr int lds = 2 * tile > few ? 2 * tile : few;
+  static_assert(wave_keys <= 16 && KT * CH % kAttnThreads == 0, "");
+
+  // 16 bytes of a token's row for every lane of a wave: lane / CH-th token
+  // after `key`, which is a multiple of 16 and less; zeros for what is not there.
+  static __device__ __forceinline__ u32x4 load(const AttnArgs& a, const Piece& p, const uint8_t* base, int key, int lane) {
+    u32x4 v = u32x4{0u, 0u, 0u, 0u};
+    if (key >= p.k1) return v;
+    const int page = ld_const(p.table, key >> a.kv.page_shift);
+    if ((uint32_t)page >= (uint32_t)a.kv.pages) return v;
+    const int t = lane / CH, c = lane % CH;
+    const uint8_t* at = base + page * a.kv.page_stride + ((key & (a.kv.page - 1)) + t) * a.kv.token_stride +
+                        p.kh * a.kv.head_stride + c * 16;
+    if (key + t < p.k1 && c * CB < a.kv.dim) v = ldg16(at);
+    return v;
+  }
+  // The scale of one token's row, for each lane's own key.
+  static __device__ __forceinline__ float load_scale(const AttnArgs& a, const Piece& p, const float* base, int key) {
+    if (key >= p.k1) return 0.0f;
+    const int page = p.table[key >> a.kv.page_shift];
+    if ((uint32_t)page >= (uint32_t)a.kv.pages) return 0.0f;
+    return base[page * a.kv.scale_page_stride + (key & (a.kv.page - 1)) * a.kv.scale_token_stride +
+                p.kh * a.kv.scale_head_stride];
+  }
+  // Which 16-key runs of `n` keys from `key` on are on no page.
+  static __device__ __forceinline__ uint32_t missing(const AttnArgs& a, const Piece& p, int key, int n) {
+    uint32_t m = 0;
+    for (int i = 0; i < n / 16; ++i) {
+      const int k = key + 16 * i;
+      if (k < p.k1 && (uint32_t)ld_const(p.table, k >> a.kv.page_shift) >= (uint32_t)a.kv.pages) m |= 1u << i;
+    }
+    return m;
+  }
+  // As 16-bit values in shared memory.
+  template <int F>
+  static __device__ __forceinline__ void store(uint8_t* row, int c, u32x4 v) {
+    if (c * CB >= DT) return;
+    if constexpr (C8) {
+      *reinterpret_cast<u32x4*>(row + c * 32) = wide8<F>(v.x, v.y);
+      *reinterpret_cast<u32x4*>(row + c * 32 + 16) = wide8<F>(v.z, v.w);
+    } else {
+      *reinterpret_cast<u32x4*>(row + c * 16) = v;
+    }
+  }
+
+  static __device__ __forceinline__ const uint8_t* query(const AttnArgs& a, const Piece& p, int row) {
+    row = min(row, p.rows - 1);
+    const int token = p.token0 + row / a.group, head = p.kh * a.group + row % a.group;
+    return a.q + (token * a.q_stride + head * a.q_head) * 2;
+  }
+  static __device__ __forceinline__ u32x4 query8(const AttnArgs& a, const uint8_t* row, int d) {
+    return d < a.kv.dim ? ldg16(row + d * 2) : u32x4{0u, 0u, 0u, 0u};
+  }
+  // Row of the parts' arrays.
+  static __device__ __forceinline__ int64_t out_row(const AttnArgs& a, const Piece& p, int row) {
+    return (int64_t)p.part * a.rows + (int64_t)(p.token0 + row / a.group) * a.heads + p.kh * a.group + row % a.group;
+  }
+
+  // Many rows: bound by the matrix cores and the exponentials beside them.  Each
+  // wave has 32 rows, and tiles of KT keys pass through shared memory, the next
+  // one on its way in registers while one is multiplied.
+  static __device__ void many_rows(const AttnArgs& a, const Piece& p, uint8_t* smem) {
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int col = lane & 31, half = lane >> 5;
+    const int first = p.row0 + wave * 32, row = first + col;
+    const bool idle = first >= p.rows;
+    u32x4 q[DT / 16];
+    {
+      const uint8_t* at = query(a, p, row);
+#pragma unroll
+      for (int s = 0; s < DT / 16; ++s) q[s] = query8(a, at, 16 * s + 8 * half);
+    }
+    const int limit = p.causal ? min(p.k1, p.limit0 + min(row, p.rows - 1) / a.group) : p.k1;
+    const int least = p.causal ? min(p.k1, p.limit0 + p.row0 / a.group) : p.k1;
+    f32x16 o[DT / 32];
+#pragma unroll
+    for (int i = 0; i < DT / 32; ++i)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) o[i][r] = 0.0f;
+    float top = -__builtin_inff(), ref = 0.0f, l = 0.0f;
+
+    u32x4 kr[passes], vr[passes];
+    float scale = 0.0f;
+    auto load_tile = [&](int key) {
+#pragma unroll
+      for (int i = 0; i < passes; ++i) {
+        const int k = key + i * (kAttnThreads / CH) + wave * wave_keys;
+        kr[i] = load(a, p, a.kv.k, k, lane);
+        vr[i] = load(a, p, a.kv.v, k, lane);
+      }
+      if constexpr (C8) {
+        if (tid < 2 * KT) scale = load_scale(a, p, tid < KT ? a.kv.k_scales : a.kv.v_scales, key + tid % KT);
+      }
+    };
+    auto store_tile = [&](int buf) {
+      uint8_t* at = smem + buf * tile;
+#pragma unroll
+      for (int i = 0; i < passes; ++i) {
+        const int k = i * (kAttnThreads / CH) + tid / CH, c = tid % CH;
+        store<QF>(at + k * KS, c, kr[i]);
+        store<VF>(at + KT * KS + k * VS, c, vr[i]);
+      }
+      if constexpr (C8) {
+        if (tid < 2 * KT) reinterpret_cast<float*>(at + KT * (KS + VS))[tid] = scale;
+      }
+    };
+
+    load_tile(p.k0);
+    uint32_t gone = missing(a, p, p.k0, KT);
+    store_tile(0);
+    __syncthreads();
+    int buf = 0;
+    for (int key = p.k0; key < p.k1; key += KT, buf ^= 1) {
+      const bool more = key + KT < p.k1;
+      uint32_t next_gone = 0;
+      if (more) {
+        load_tile(key + KT);
+        next_gone = missing(a, p, key + KT, KT);
+      }
+      if (!idle) {
+        const uint8_t* ks = smem + buf * tile;
+        const uint8_t* vs = ks + KT * KS;
+        const float* sc = reinterpret_cast<const float*>(ks + KT * (KS + VS));
+        f32x16 s[KT / 32];
+#pragma unroll
+        for (int t = 0; t < KT / 32; ++t) {
+#pragma unroll
+          for (int r = 0; r < 16; ++r) s[t][r] = 0.0f;
+#pragma unroll
+          for (int i = 0; i < DT / 16; ++i)
+            s[t] = mma32<QF>(*reinterpret_cast<const u32x4*>(ks + (32 * t + col) * KS + 32 * i + 16 * half), q[i], s[t]);
+        }
+        if constexpr (C8) {
+#pragma unroll
+          for (int t = 0; t < KT / 32; ++t)
+#pragma unroll
+            for (int r = 0; r < 16; r += 4) {
+              const f32x4 m = *reinterpret_cast<const f32x4*>(sc + 32 * t + 2 * r + 4 * half);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) s[t][r + j] *= m[j];
+            }
+        }
+        if (gone != 0 || key + KT > least) {
+#pragma unroll
+          for (int t = 0; t < KT / 32; ++t)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+              const int at = 32 * t + 8 * (r >> 2) + 4 * half + (r & 3);
+              if (key + at >= limit || (gone >> (at >> 4) & 1)) s[t][r] = -__builtin_inff();
+            }
+        }
+        float m = s[0][0];
+#pragma unroll
+        for (int t = 0; t < KT / 32; ++t)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) m = fmaxf(m, s[t][r]);
+        m = other_half_max(m) * a.c;
+        if (__any(m > top + kSlack)) {
+          const bool up = m > top;
+          const float next = up ? m - weights_up<VF>() : ref;
+          const float f = top == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(ref - next);
+          if (up) top = m;
+          ref = next;
+          l *= f;
+#pragma unroll
+          for (int i = 0; i < DT / 32; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) o[i][r] *= f;
+        }
+        u32x4 w[KT / 16], w2[two ? KT / 16 : 1];
+#pragma unroll
+        for (int t = 0; t < KT / 32; ++t) {
+          float e[16];
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            e[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][r], a.c, -ref));
+            l += e[r];
+          }
+          if constexpr (C8) {
+#pragma unroll
+            for (int r = 0; r < 16; r += 4) {
+              const f32x4 v = *reinterpret_cast<const f32x4*>(sc + KT + 32 * t + 2 * r + 4 * half);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) e[r + j] *= v[j];
+            }
+          }
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float a0 = e[8 * u + 2 * j], a1 = e[8 * u + 2 * j + 1];
+              w[2 * t + u][j] = pair16<VF>(a0, a1);
+              if constexpr (two) w2[2 * t + u][j] = rest16<VF>(a0, a1, w[2 * t + u][j]);
+            }
+        }
+        // group of 16 lanes: columns 16 * (group % 2) on, keys 4 * half on and 8 after them
+        const uint8_t* at = vs + (4 * half + (lane & 15) / 4) * VS + 32 * (lane >> 4 & 1) + (lane & 3) * 8;
+#pragma unroll
+        for (int t = 0; t < KT / 16; ++t)
+#pragma unroll
+          for (int i = 0; i < DT / 32; ++i) {
+            const u32x2 lo = read_transposed(at + 16 * t * VS + 64 * i);
+            const u32x2 hi = read_transposed(at + (16 * t + 8) * VS + 64 * i);
+            o[i] = mma32<VF>(u32x4{lo.x, lo.y, hi.x, hi.y}, w[t], o[i]);
+            if constexpr (two) o[i] = mma32<VF>(u32x4{lo.x, lo.y, hi.x, hi.y}, w2[t], o[i]);
+          }
+      }
+      if (more) {
+        store_tile(buf ^ 1);
+        gone = next_gone;
+      }
+      __syncthreads();
+    }
+    l = other_half_sum(l);
+    if (row < p.rows) {
+      const int64_t at = out_row(a, p, row);
+      if (half == 0) *reinterpret_cast<f32x2*>(a.part_m + 2 * at) = f32x2{ref, l};
+      float* dst = a.part_o + at * a.kv.dim;
+#pragma unroll
+      for (int i = 0; i < DT / 32; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; r += 4) {
+          const int d = 32 * i + 2 * r + 4 * half;
+          if (d < a.kv.dim)
+            *reinterpret_cast<f32x4*>(dst + d) = f32x4{o[i][r], o[i][r + 1], o[i][r + 2], o[i][r + 3]};
+        }
+    }
+  }
+
+  // Up to 16 rows: bound by the stream of the cache.  The waves take 32 keys in
+  // turn, each on its own: keys straight into registers as the operand that they
+  // are, values through the wave's own part of shared memory, to be transposed.
+  // The next 32 are on their way meanwhile.
+  static __device__ void few_rows(const AttnArgs& a, const Piece& p, uint8_t* smem) {
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int col = lane & 15, g = lane >> 4;
+    constexpr int steps = DT / 32;                         // of 32 elements of a row
+    constexpr int vloads = 32 / wave_keys;
+    // which elements group g has in step i: 8 of each 32, of 8-bit rows 16 of each 64
+    auto elem = [&](int i) { return C8 && DT % 64 == 0 ? 64 * (i / 2) + 16 * g + 8 * (i & 1) : 32 * i + 8 * g; };
+    u32x4 q[steps];
+    {
+      const uint8_t* at = query(a, p, col);
+#pragma unroll
+      for (int i = 0; i < steps; ++i) q[i] = query8(a, at, elem(i));
+    }
+    const int limit = p.causal ? min(p.k1, p.limit0 + min(col, p.rows - 1) / a.group) : p.k1;
+    const int least = p.causal ? min(p.k1, p.limit0) : p.k1;
+    f32x4 o[DT / 16];
+#pragma unroll
+    for (int i = 0; i < DT / 16; ++i) o[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    float top = -__builtin_inff(), ref = 0.0f, l = 0.0f;
+    uint8_t* vs = smem + wave * few_wave;
+    float* sc = reinterpret_cast<float*>(vs + 32 * VS);
+
+    struct Keys {
+      u32x4 k[2][steps];
+      u32x4 v[vloads];
+      float scale;
+      uint32_t gone;
+    };
+    auto load_keys = [&](int key, Keys& f) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const int k = key + 16 * t;
+        const int page = k < p.k1 ? ld_const(p.table, k >> a.kv.page_shift) : -1;
+        const bool there = (uint32_t)page < (uint32_t)a.kv.pages && k + col < p.k1;
+        const uint8_t* at = a.kv.k + page * a.kv.page_stride + ((k & (a.kv.page - 1)) + col) * a.kv.token_stride +
+                            p.kh * a.kv.head_stride;
+#pragma unroll
+        for (int i = 0; i < steps; ++i) {
+          f.k[t][i] = u32x4{0u, 0u, 0u, 0u};
+          if constexpr (C8 && DT % 64 == 0) {
+            if (i % 2 == 0 && there && elem(i) < a.kv.dim) f.k[t][i] = ldg16(at + elem(i));
+          } else if constexpr (C8) {
+            if (there && elem(i) < a.kv.dim) {
+              const u32x2 d = *reinterpret_cast<const u32x2*>(at + elem(i));
+              f.k[t][i].x = d.x;
+              f.k[t][i].y = d.y;
+            }
+          } else {
+            if (there && elem(i) < a.kv.dim) f.k[t][i] = ldg16(at + elem(i) * 2);
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < vloads; ++i) f.v[i] = load(a, p, a.kv.v, key + i * wave_keys, lane);
+      if constexpr (C8) f.scale = load_scale(a, p, lane < 32 ? a.kv.k_scales : a.kv.v_scales, key + (lane & 31));
+      f.gone = missing(a, p, key, 32);
+    };
+
+    Keys cur;
+    int key = p.k0 + 32 * wave;
+    if (key < p.k1) load_keys(key, cur);
+    for (; key < p.k1; key += 32 * kAttnWaves) {
+      const uint32_t gone = cur.gone;
+#pragma unroll
+      for (int i = 0; i < vloads; ++i) store<VF>(vs + (i * wave_keys + lane / CH) * VS, lane % CH, cur.v[i]);
+      if constexpr (C8) sc[lane] = cur.scale;
+      u32x4 k[2][steps];
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int i = 0; i < steps; ++i) {
+          if constexpr (C8 && DT % 64 == 0)
+            k[t][i] = i % 2 == 0 ? wide8<QF>(cur.k[t][i].x, cur.k[t][i].y) : wide8<QF>(cur.k[t][i - 1].z, cur.k[t][i - 1].w);
+          else if constexpr (C8) k[t][i] = wide8<QF>(cur.k[t][i].x, cur.k[t][i].y);
+          else k[t][i] = cur.k[t][i];
+        }
+      if (key + 32 * kAttnWaves < p.k1) load_keys(key + 32 * kAttnWaves, cur);
+      f32x4 s[2];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        s[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < steps; ++i) s[t] = mma16<QF>(k[t][i], q[i], s[t]);
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      if constexpr (C8) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) s[t] *= *reinterpret_cast<const f32x4*>(sc + 16 * t + 4 * g);
+      }
+      if (gone != 0 || key + 32 > least) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (key + 16 * t + 4 * g + r >= limit || (gone >> t & 1)) s[t][r] = -__builtin_inff();
+      }
+      float m = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
+                      fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3])));
+      m = other_half_max(other_row_max(m)) * a.c;
+      if (__any(m > top + kSlack)) {
+        const bool up = m > top;
+        const float next = up ? m - weights_up<VF>() : ref;
+        const float f = top == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(ref - next);
+        if (up) top = m;
+        ref = next;
+        l *= f;
+#pragma unroll
+        for (int i = 0; i < DT / 16; ++i) o[i] *= f;
+      }
+      f32x4 e[2];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          e[t][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][r], a.c, -ref));
+          l += e[t][r];
+        }
+        if constexpr (C8) e[t] *= *reinterpret_cast<const f32x4*>(sc + 32 + 16 * t + 4 * g);
+      }
+      const u32x4 w = u32x4{pair16<VF>(e[0][0], e[0][1]), pair16<VF>(e[0][2], e[0][3]),
+                            pair16<VF>(e[1][0], e[1][1]), pair16<VF>(e[1][2], e[1][3])};
+      u32x4 w2 = w;
+      if constexpr (two)
+        w2 = u32x4{rest16<VF>(e[0][0], e[0][1], w.x), rest16<VF>(e[0][2], e[0][3], w.y),
+                   rest16<VF>(e[1][0], e[1][1], w.z), rest16<VF>(e[1][2], e[1][3], w.w)};
+      const uint8_t* at = vs + (4 * g + col / 4) * VS + (col & 3) * 8;
+#pragma unroll
+      for (int i = 0; i < DT / 16; ++i) {
+        const u32x2 lo = read_transposed(at + 32 * i), hi = read_transposed(at + 16 * VS + 32 * i);
+        o[i] = mma16<VF>(u32x4{lo.x, lo.y, hi.x, hi.y}, w, o[i]);
+        if constexpr (two) o[i] = mma16<VF>(u32x4{lo.x, lo.y, hi.x, hi.y}, w2, o[i]);
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
+    l = other_half_sum(other_row_sum(l));
+    // the waves' sums, joined in shared memory
+    __syncthreads();
+    float* po = reinterpret_cast<float*>(smem);            // [wave][row][DT]
+    float* pm = po + kAttnWaves * 16 * DT;                 // [wave][row][2]
+#pragma unroll
+    for (int i = 0; i < DT / 16; ++i)
+      *reinterpret_cast<f32x4*>(po + (wave * 16 + col) * DT + 16 * i + 4 * g) = o[i];
+    if (g == 0) *reinterpret_cast<f32x2*>(pm + 2 * (wave * 16 + col)) = f32x2{ref, l};
+    __syncthreads();
+    for (int i = tid; i < p.rows * (DT / 4); i += kAttnThreads) {
+      const int row = i / (DT / 4), d = i % (DT / 4) * 4;
+      f32x2 m[kAttnWaves];
+      float most = -__builtin_inff();
+#pragma unroll
+      for (int w = 0; w < kAttnWaves; ++w) {
+        m[w] = *reinterpret_cast<const f32x2*>(pm + 2 * (w * 16 + row));
+        if (m[w].y != 0.0f) most = fmaxf(most, m[w].x);
+      }
+      f32x4 v = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      float sum = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kAttnWaves; ++w) {
+        if (m[w].y == 0.0f) continue;
+        const float f = __builtin_amdgcn_exp2f(m[w].x - most);
+        sum += f * m[w].y;
+        v += f * *reinterpret_cast<const f32x4*>(po + (w * 16 + row) * DT + d);
+      }
+      const int64_t at = out_row(a, p, row);
+      if (d == 0) *reinterpret_cast<f32x2*>(a.part_m + 2 * at) = f32x2{most == -__builtin_inff() ? 0.0f : most, sum};
+      if (d < a.kv.dim) *reinterpret_cast<f32x4*>(a.part_o + at * a.kv.dim + d) = v;
+    }
+  }
+};
+
+// One range of keys of one head of the cache: of the prefix for a tile of all
+// sequences' rows, or of one sequence's own tokens.  Workgroups go round the 8
+// XCDs one by one; each XCD takes a run of pieces, those with the same keys
+// next to each other, in its own L2.
+template <int QF, bool C8, int DT>
+__global__ __launch_bounds__(kAttnThreads, DT > 128 ? 1 : 2) void k_attention(AttnArgs a) {
+  using G = Attn<QF, C8, DT>;
+  __shared__ __align__(256) uint8_t smem[G::lds];
+  Piece p;
+  int b = blockIdx.x;
+  const bool shared = b < a.prefix_blocks;
+  const int total = shared ? a.prefix_blocks : a.own_blocks;
+  if (!shared) b -= a.prefix_blocks;
+  {
+    const int per = total / 8, extra = total % 8, xcd = b % 8;
+    b = xcd * per + min(xcd, extra) + b / 8;
+  }
+  const int kv = a.kv.kv_heads;
+  if (shared) {
+    const int tile = b % a.prefix_tiles;
+    b /= a.prefix_tiles;
+    p.part = b % a.prefix_splits;
+    p.kh = b / a.prefix_splits;
+    p.table = a.prefix_pages;
+    p.k0 = p.part * a.prefix_chunk;
+    p.k1 = min(a.prefix, p.k0 + a.prefix_chunk);
+    p.rows = a.sequences * a.queries * a.group;
+    p.row0 = tile * kTileRows;
+    p.token0 = 0;
+    p.limit0 = 0;
+    p.causal = false;
+  } else {
+    const int tile = b % a.own_tiles;
+    b /= a.own_tiles;
+    p.kh = b % kv;
+    b /= kv;
+    const int split = b % a.own_splits, seq = b / a.own_splits;
+    const int length = ld_const(a.lengths, seq);
+    const int most = max(min(length, a.capacity), 0);
+    const int chunk = ((most + a.own_splits - 1) / a.own_splits + 127) / 128 * 128;
+    p.part = a.prefix_splits + split;
+    p.table = a.tables + seq * a.table_stride;
+    p.k0 = min(most, split * chunk);
+    p.k1 = min(most, p.k0 + chunk);
+    p.rows = a.queries * a.group;
+    p.row0 = tile * kTileRows;
+    p.token0 = seq * a.queries;
+    p.limit0 = length - a.queries + 1;
+    p.causal = true;
+    if (p.k0 >= p.k1) {
+      for (int i = p.row0 + threadIdx.x; i < min(p.rows, p.row0 + kTileRows); i += kAttnThreads)
+        *reinterpret_cast<f32x2*>(a.part_m + 2 * G::out_row(a, p, i)) = f32x2{0.0f, 0.0f};
+      return;
+    }
+  }
+  if (p.rows <= kFewRows) G::few_rows(a, p, smem);
+  else G::many_rows(a, p, smem);
+}
+
+// A row's ranges joined: a wave for each row, 4 elements a lane, so that
+// kWave / LR ranges are read at once, and those of up to 4 rounds are on their
+// way together.  Ranges that nothing was seen in are passed over.
+template <int QF, int LR>
+__global__ __launch_bounds__(kBlock) void k_attention_join(AttnArgs a) {
+  constexpr int at_once = kWave / LR;
+  const int lane = threadIdx.x & 63;
+  const int row = blockIdx.x * kWavesPerBlock + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (row >= a.rows) return;
+  const int token = row / a.heads, head = row % a.heads;
+  const int parts = a.prefix_splits + a.own_splits;
+  const f32x2* ml = reinterpret_cast<const f32x2*>(a.part_m) + row;
+  const int d = lane % LR * 4, turn = lane / LR;
+  const float* po = a.part_o + (int64_t)row * a.kv.dim + d;
+  const int64_t part_stride = (int64_t)a.rows * a.kv.dim;
+  const bool mine = d < a.kv.dim;
+  f32x4 o = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  float most = -__builtin_inff(), l = 0.0f;
+  for (int s0 = 0; s0 < parts; s0 += kWave) {              // 64 ranges, one a lane
+    f32x2 m = f32x2{0.0f, 0.0f};
+    if (s0 + lane < parts) m = ml[(int64_t)(s0 + lane) * a.rows];
+    float next = m.y != 0.0f ? m.x : -__builtin_inff();
+#pragma unroll
+    for (int i = 32; i > 0; i /= 2) next = fmaxf(next, __shfl_xor(next, i));
+    next = fmaxf(next, most);
+    if (next > most) {
+      const float f = most == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(most - next);
+      l *= f;
+      o *= f;
+      most = next;
+    }
+    const float w = m.y != 0.0f ? __builtin_amdgcn_exp2f(m.x - most) : 0.0f;
+    float sum = m.y != 0.0f ? w * m.y : 0.0f;
+#pragma unroll
+    for (int i = 32; i > 0; i /= 2) sum += __shfl_xor(sum, i);
+    l += sum;
+    const uint64_t seen = __ballot(m.y != 0.0f);
+    const int count = min(kWave, parts - s0);
+    for (int s = 0; s < count; s += 4 * at_once) {
+      f32x4 v[4];
+      float f[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int k = min(s + u * at_once + turn, kWave - 1);
+        f[u] = __shfl(w, k);
+        v[u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        if (s + u * at_once + turn < count && (seen >> k & 1) && mine)
+          v[u] = *reinterpret_cast<const f32x4*>(po + (s0 + k) * part_stride);
+        else f[u] = 0.0f;
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) o += f[u] * v[u];
+    }
+  }
+#pragma unroll
+  for (int i = LR; i < kWave; i *= 2)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] += __shfl_xor(o[e], i);
+  if (ld_const(a.lengths, token / a.queries) < 0) return;
+  if (lane < LR && mine) {
+    o *= l == 0.0f ? 0.0f : 1.0f / l;
+    uint16_t* dst = static_cast<uint16_t*>(a.out) + token * a.out_stride + head * a.out_head + d;
+    *reinterpret_cast<u32x2*>(dst) = u32x2{pair16<QF>(o[0], o[1]), pair16<QF>(o[2], o[3])};
+  }
+  // the logarithm of the sum, whose reference `most` is
+  if (a.lse && lane == 0)
+    a.lse[token * a.lse_stride + head] =
+        l == 0.0f ? -__builtin_inff() : (most + __builtin_log2f(l)) * 0.69314718055994531f;
+}
+
+// ================================================================ host side
+
+static int check_attention(const ar_attention_params* p) {
+  if (!p) return AR_EINVAL;
+  if (p->reserved != 0 || p->sequences < 0 || p->queries < 1 || p->heads < 1 || p->prefix < 0 || p->max_pages < 0)
+    return AR_EINVAL;
+  if (p->format != AR_BF16 && p->format != AR_F16) return AR_EINVAL;
+  if (!(p->scale > 0.0f) || p->scale > 3.0e38f) return AR_EINVAL;
+  int rc = check_cache(&p->cache);
+  if (rc) return rc;
+  if (p->heads % p->cache.kv_heads != 0) return AR_EINVAL;
+  if (p->cache.format != AR_E4M3_ROW && p->cache.format != p->format) return AR_EINVAL;
+  const int64_t most = int64_t(1) << 30;
+  if (p->sequences > most || p->prefix > most || p->max_pages > most) return AR_ESIZE;
+  if (p->max_pages * p->cache.page > most) return AR_ESIZE;
+  // rows of all parts stay within 31 bits
+  if ((double)p->sequences * p->queries * p->heads >= (double)(1 << 26)) return AR_ESIZE;
+  return AR_OK;
+}
+
+static int check_attention_rows(const ar_attention_params* p) {
+  const int64_t most = int64_t(1) << 40;
+  const int64_t tokens = p->sequences * p->queries;
+  if (!p->q || !p->out || !p->lengths) return AR_EINVAL;
+  if (p->max_pages > 0 && (!p->pages || (p->sequences > 1 && p->pages_stride < p->max_pages))) return AR_EINVAL;
+  if (p->prefix > 0 && !p->prefix_pages) return AR_EINVAL;
+  if (p->q_stride < 0 || p->q_head_stride < 0 || p->out_stride < 0 || p->out_head_stride < 0 || p->lse_stride < 0)
+    return AR_EINVAL;
+  if (p->q_stride >= most || p->q_head_stride >= most || p->out_stride >= most || p->out_head_stride >= most ||
+      p->lse_stride >= most || p->pages_stride >= most)
+    return AR_ESIZE;
+  // outputs may not overlap each other
+  const int64_t dim = p->cache.dim, heads = p->heads;
+  auto apart = [&](int64_t ts, int64_t hs, int64_t width) {
+    if (heads > 1 && hs < width) return false;
+    if (tokens <= 1) return true;
+    return ts >= (heads - 1) * hs + width || (ts >= width && hs >= (tokens - 1) * ts + width);
+  };
+  if (!apart(p->out_stride, p->out_head_stride, dim)) return AR_EINVAL;
+  if (p->lse && tokens > 1 && p->lse_stride < heads) return AR_EINVAL;
+  if (!aligned(p->q, 16) || p->q_stride % 8 || p->q_head_stride % 8 || !aligned(p->out, 16) || p->out_stride % 8 ||
+      p->out_head_stride % 8 || !aligned(p->lengths, 4) || !aligned(p->pages, 4) || !aligned(p->prefix_pages, 4) ||
+      !aligned(p->lse, 4))
+    return AR_EALIGN;
+  return AR_OK;
+}
+
+// How the keys are split.
+struct AttnPlan {
+  int32_t prefix_splits, prefix_chunk, prefix_tiles, own_splits, own_tiles;
+};
+
+// Pieces of keys.  A piece costs a step for each 64 keys of a tile of many rows,
+// or for each 128 that the waves of few rows take together; all are made as
+// long as fills the chip's 512 places for workgroups (two to a CU) once, or
+// twice where pieces are long, so that they end together.
+static AttnPlan plan_attention(const ar_attention_params* p) {
+  AttnPlan s{};
+  const int64_t kv = p->cache.kv_heads, group = p->heads / kv;
+  const int64_t rows = p->sequences * p->queries * group, own_rows = p->queries * group;
+  const int64_t capacity = p->max_pages * p->cache.page;
+  auto tiles = [](int64_t r) { return r <= kFewRows ? 1 : ceil_div64(r, kTileRows); };
+  auto step = [](int64_t r) { return r <= kFewRows ? 128 : 64; };
+  s.prefix_tiles = (int32_t)tiles(rows);
+  s.own_tiles = (int32_t)tiles(own_rows);
+  const int64_t shared = kv * s.prefix_tiles * ceil_div64(p->prefix, step(rows));
+  const int64_t own = p->sequences * kv * s.own_tiles * ceil_div64(capacity, step(own_rows));
+  int64_t steps = ceil_div64(shared + own, 512);
+  if (steps >= 32) steps = ceil_div64(steps, 2);
+  if (p->prefix > 0) {
+    const int64_t n = ceil_div64(p->prefix, steps * step(rows));
+    s.prefix_chunk = (int32_t)(ceil_div64(ceil_div64(p->prefix, n), 64) * 64);
+    s.prefix_splits = (int32_t)ceil_div64(p->prefix, s.prefix_chunk);
+  }
+  if (capacity > 0) s.own_splits = (int32_t)ceil_div64(capacity, steps * step(own_rows));
+  return s;
+}
+
+static int64_t attention_bytes(const ar_attention_params* p, const AttnPlan& s) {
+  const int64_t rows = p->sequences * p->queries * p->heads;
+  const int64_t parts = s.prefix_splits + s.own_splits;
+  return (parts * rows * (p->cache.dim + 2) * 4 + 255) / 256 * 256;
+}
+
+template <int QF, bool C8, int DT>
+static hipError_t launch_parts(const AttnArgs& a, hipStream_t s) {
+  return launch(k_attention<QF, C8, DT>, dim3((unsigned)(a.prefix_blocks + a.own_blocks)), dim3(kAttnThreads), s, a);
+}
+template <int QF, bool C8>
+static hipError_t launch_parts_dim(const AttnArgs& a, hipStream_t s) {
+  if (a.kv.dim <= 64) return launch_parts<QF, C8, 64>(a, s);
+  if (a.kv.dim <= 96) return launch_parts<QF, C8, 96>(a, s);
+  if (a.kv.dim <= 128) return launch_parts<QF, C8, 128>(a, s);
+  if (a.kv.dim <= 192) return launch_parts<QF, C8, 192>(a, s);
+  return launch_parts<QF, C8, 256>(a, s);
+}
+template <int QF>
+static hipError_t launch_join(const AttnArgs& a, hipStream_t s) {
+  const dim3 grid((unsigned)ceil_div64(a.rows, kWavesPerBlock)), block(kBlock);
+  if (a.kv.dim <= 64) return launch(k_attention_join<QF, 16>, grid, block, s, a);
+  if (a.kv.dim <= 128) return launch(k_attention_join<QF, 32>, grid, block, s, a);
+  return launch(k_attention_join<QF, 64>, grid, block, s, a);
+}
+template <int QF>
+static hipError_t launch_attention(const AttnArgs& a, bool c8, hipStream_t s) {
+  hipError_t e = hipSuccess;
+  if (a.prefix_blocks + a.own_blocks > 0)
+    e = c8 ? launch_parts_dim<QF, true>(a, s) : launch_parts_dim<QF, false>(a, s);
+  return e == hipSuccess ? launch_join<QF>(a, s) : e;
+}
+
+}  // namespace ar
+
+using namespace ar;
+
+extern "C" {
+
+int64_t ar_prefix_attention_work_bytes(const ar_attention_params* p) {
+  const int rc = check_attention(p);
+  if (rc) return rc;
+  if (p->sequences == 0) return 0;
+  return attention_bytes(p, plan_attention(p));
+}
+
+int ar_prefix_attention(const ar_attention_params* p, void* work, int64_t work_bytes, void* stream) {
+  int rc = check_attention(p);
+  if (rc) return rc;
+  if (p->sequences == 0) return AR_OK;
+  rc = check_attention_rows(p);
+  if (rc) return rc;
+  if (p->prefix > 0 || p->max_pages > 0) {
+    rc = check_cache_rows(&p->cache);
+    if (rc) return rc;
+  }
+  const AttnPlan plan = plan_attention(p);
+  const int64_t bytes = attention_bytes(p, plan);
+  if (bytes > 0) {
+    if (!work) return AR_EINVAL;
+    if (!aligned(work, 256)) return AR_EALIGN;
+    if (work_bytes < bytes) return AR_ESIZE;
+  }
+  AttnArgs a{};
+  const int64_t kv = p->cache.kv_heads;
+  a.kv = cache_view(&p->cache);
+  a.q = static_cast<const uint8_t*>(p->q);
+  a.q_stride = p->q_stride;
+  a.q_head = p->q_head_stride;
+  a.out = p->out;
+  a.out_stride = p->out_stride;
+  a.out_head = p->out_head_stride;
+  a.lse = p->lse;
+  a.lse_stride = p->lse_stride;
+  a.prefix_pages = p->prefix_pages;
+  a.lengths = p->lengths;
+  a.tables = p->pages;
+  a.table_stride = p->pages_stride;
+  a.c = (float)((double)p->scale * 1.4426950408889634);
+  a.prefix = (int32_t)p->prefix;
+  a.capacity = (int32_t)(p->max_pages * p->cache.page);
+  a.sequences = (int32_t)p->sequences;
+  a.queries = p->queries;
+  a.heads = p->heads;
+  a.group = (int32_t)(p->heads / kv);
+  a.rows = (int32_t)(p->sequences * p->queries * p->heads);
+  a.prefix_splits = plan.prefix_splits;
+  a.prefix_chunk = plan.prefix_chunk;
+  a.prefix_tiles = plan.prefix_tiles;
+  a.own_splits = plan.own_splits;
+  a.own_tiles = plan.own_tiles;
+  const int64_t pb = kv * plan.prefix_tiles * plan.prefix_splits;
+  const int64_t ob = p->sequences * kv * plan.own_tiles * plan.own_splits;
+  if (pb + ob > most_blocks(kAttnThreads)) return AR_ESIZE;
+  a.prefix_blocks = (int32_t)pb;
+  a.own_blocks = (int32_t)ob;
+  const int64_t parts = plan.prefix_splits + plan.own_splits;
+  a.part_o = static_cast<float*>(work);
+  a.part_m = a.part_o + parts * a.rows * p->cache.dim;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const bool c8 = p->cache.format == AR_E4M3_ROW;
+  return map_hip(p->format == AR_BF16 ? launch_attention<AR_BF16>(a, c8, s) : launch_attention<AR_F16>(a, c8, s));
+}
+
+}  // extern "C"

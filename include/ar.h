@@ -498,6 +498,111 @@ typedef struct {
  */
 int ar_mx4_linear(const ar_linear_params* p, void* stream);
 
+/*
+ * A paged cache of keys and values.  A page holds `page` tokens; token t of
+ * page p has for every head h of the cache a row of `dim` keys at
+ * k + p*page_stride + t*token_stride + h*head_stride and one of values at the
+ * same place of v.  Rows are of AR_BF16, AR_F16 or AR_E4M3_ROW (strides in
+ * elements or bytes), 16-byte aligned, strides multiples of 8 elements or 16
+ * bytes; AR_E4M3_ROW has a binary32 scale for each row, with strides of its
+ * own in floats.  Rows may lie in any order but not overlap.
+ */
+#define AR_CACHE_MAX_DIM 256
+typedef struct {
+    int32_t format;             /* AR_BF16, AR_F16 or AR_E4M3_ROW */
+    int32_t page;               /* a power of two, 16 .. 2^20 */
+    int64_t pages;              /* how many there are */
+    int32_t kv_heads;           /* >= 1 */
+    int32_t dim;                /* a multiple of 16, 16 .. AR_CACHE_MAX_DIM */
+    void* k;
+    void* v;
+    int64_t page_stride, token_stride, head_stride;
+    float* k_scales;            /* AR_E4M3_ROW only */
+    float* v_scales;
+    int64_t scale_page_stride, scale_token_stride, scale_head_stride;
+} ar_kv_cache;
+
+/*
+ * ar_cache_append -- a step's keys and values into the cache: each of
+ * `sequences` sequences has `queries` new tokens, and lengths[b] tokens with
+ * them, so token i of sequence b (row b*queries + i of k and v) is its token
+ * lengths[b] - queries + i.  Sequence b's token t lies in page
+ * pages[b*pages_stride + t / page].
+ *   format: of k and v: the cache's, or with an AR_E4M3_ROW cache AR_BF16 or
+ *      AR_F16: s as above, every code the nearest to 448 v / max|v| (to v / s
+ *      where s is 2^-126), which is v over s before its rounding.
+ *   k, v: device, token rows at k + row*k_stride, head h's at h*k_head_stride
+ *      after it, alignment as for rows of their format.
+ *   lengths: device int32[sequences]; pages: device int32, max_pages for each
+ *      sequence.  A token whose number is negative (a sequence shorter than
+ *      `queries`, or of negative length: one that is not there), or past the
+ *      table's last page, or whose page is none of 0 .. cache->pages - 1, is
+ *      not written.
+ * No two tokens may have the same place.  AR_ESIZE: sizes or strides of 2^30
+ * and more.
+ */
+int ar_cache_append(const ar_kv_cache* cache, int64_t sequences, int32_t queries, int32_t format,
+                    const void* k, int64_t k_stride, int64_t k_head_stride,
+                    const void* v, int64_t v_stride, int64_t v_head_stride,
+                    const int32_t* lengths, const int32_t* pages, int64_t pages_stride,
+                    int64_t max_pages, void* stream);
+
+typedef struct {
+    ar_kv_cache cache;
+    int64_t sequences;          /* >= 0 */
+    int32_t queries;            /* tokens of each, its last ones; >= 1 */
+    int32_t heads;              /* a multiple of cache.kv_heads */
+    float scale;                /* of the scores; > 0, finite */
+    int32_t format;             /* of q and out: AR_BF16 or AR_F16 */
+    const void* q;              /* row b*queries + i, head h: q + row*q_stride + h*q_head_stride */
+    int64_t q_stride, q_head_stride;
+    void* out;
+    int64_t out_stride, out_head_stride;
+    float* lse;                 /* NULL: not written; row*lse_stride + h */
+    int64_t lse_stride;
+    int64_t prefix;             /* tokens that all sequences share, >= 0 */
+    const int32_t* prefix_pages;/* device: their pages, ceil(prefix / page) */
+    const int32_t* lengths;     /* device int32[sequences]: own tokens of each */
+    const int32_t* pages;       /* device: their pages, as for ar_cache_append */
+    int64_t pages_stride, max_pages;
+    int32_t reserved;           /* must be 0 */
+} ar_attention_params;
+
+/*
+ * ar_prefix_attention -- attention of a batch's tokens over a prefix that its
+ * sequences share, whose keys and values are read once for all of them, and
+ * each sequence's own tokens: for every token row and head h, with head h /
+ * (heads / kv_heads) of the cache,
+ *     out = sum over t of w_t v_t,  w = softmax over t of scale * (q . k_t)
+ * where t goes over the prefix's tokens and the first lengths[b] - queries + 1
+ * + i own tokens of sequence b (token i of the step sees itself and what comes
+ * before it).  lse: the logarithm of the softmax's sum.
+ *   format: cache.format, or either with an AR_E4M3_ROW cache.
+ *   lengths[b] may be less than `queries`: the step's first tokens then see
+ *      the prefix alone.  A token that sees nothing gets zeros, and lse -inf.
+ *      Negative: sequence b is not there, and its rows of out and lse are left
+ *      as they are.  What lies past max_pages pages does not count, nor do
+ *      tokens on a page that is none of 0 .. cache.pages - 1.
+ *   What lies in the cache behind a sequence's last token does not count,
+ *      whatever it is.
+ *   work: device, 256-byte aligned, at least
+ *      ar_prefix_attention_work_bytes(p) bytes (AR_ESIZE); used for the time
+ *      of the call, so calls that may overlap need each their own.
+ * Products of 16-bit operands in the matrix cores, sums, maxima and the joined
+ * rows in binary32.  The weights are rounded to `format` for their products with
+ * the values (with an AR_E4M3_ROW cache to bf16, for fp16 outputs in two parts):
+ * out is off by at most 2^-8 (fp16: 2^-11) of sum w |v| for that, and rounded
+ * once.  The order
+ * of every sum is fixed by the sizes and lengths, so equal calls give equal
+ * bits.  out may not overlap the inputs.  sequences 0: nothing is written.
+ * AR_ESIZE: sequences, prefix or max_pages * page above 2^30, 2^26 or more
+ * rows of all heads, strides of 2^40 and more.
+ */
+int ar_prefix_attention(const ar_attention_params* p, void* work, int64_t work_bytes, void* stream);
+
+/* Bytes of its work buffer, by sizes alone (not lengths); < 0 on bad parameters. */
+int64_t ar_prefix_attention_work_bytes(const ar_attention_params* p);
+
 /* ------------------------------------------------------------ simulator --- */
 /*
  * ar_sim_run -- `nops` back-to-back one-shot all-reduces in one persistent
