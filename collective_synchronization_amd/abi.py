@@ -42,6 +42,7 @@ FORMATS = {"bf16": AR_BF16, "f16": AR_F16, "f32": AR_F32, "row8": AR_E4M3_ROW,
            "mx8": AR_E4M3_MX, "mx4": AR_E2M1_MX}
 AR_NORM_MAX_HIDDEN = 32768
 AR_REDUCE_NORM_MAX_HIDDEN = 16384
+AR_ADAPTER_MAX_RANK = 128
 AR_CACHE_MAX_DIM = 256
 
 
@@ -93,6 +94,16 @@ class ar_linear_params(ctypes.Structure):
                 ("w_scales", ctypes.c_void_p), ("w_scale_stride", ctypes.c_int64),
                 ("w_scale_rank_stride", ctypes.c_int64), ("y", ctypes.c_void_p),
                 ("y_stride", ctypes.c_int64), ("y_rank_stride", ctypes.c_int64)]
+
+
+class ar_adapter_params(ctypes.Structure):
+    _fields_ = [("adapters", ctypes.c_int32), ("rank", ctypes.c_int32),
+                ("index", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+                ("a", ctypes.c_void_p), ("a_stride", ctypes.c_int64),
+                ("a_adapter_stride", ctypes.c_int64), ("a_rank_stride", ctypes.c_int64),
+                ("b", ctypes.c_void_p), ("b_stride", ctypes.c_int64),
+                ("b_adapter_stride", ctypes.c_int64), ("b_rank_stride", ctypes.c_int64),
+                ("reserved", ctypes.c_int32)]
 
 
 class ar_kv_cache(ctypes.Structure):
@@ -185,6 +196,10 @@ _SIGS = {
     "ar_dequantize_mx": ([_i64, _i64, _i32, _vp, _i64, _vp, _i64, _i32, _vp, _i64, _vp],
                          ctypes.c_int),
     "ar_mx4_linear": ([ctypes.POINTER(ar_linear_params), _vp], ctypes.c_int),
+    "ar_mx4_linear_adapters": ([ctypes.POINTER(ar_linear_params), ctypes.POINTER(ar_adapter_params),
+                                _vp, _i64, _vp], ctypes.c_int),
+    "ar_adapter_work_bytes": ([ctypes.POINTER(ar_linear_params), ctypes.POINTER(ar_adapter_params)],
+                              _i64),
     "ar_cache_append": ([ctypes.POINTER(ar_kv_cache), _i64, _i32, _i32, _vp, _i64, _i64, _vp, _i64,
                          _i64, _vp, _vp, _i64, _i64, _vp], ctypes.c_int),
     "ar_prefix_attention": ([ctypes.POINTER(ar_attention_params), _vp, _i64, _vp], ctypes.c_int),
@@ -482,6 +497,34 @@ def linear_params(nranks, rows, outputs, inputs, x_fmt, x, x_stride, x_rank_stri
 
 def ar_mx4_linear(params: ar_linear_params, stream=None) -> None:
     _check(_lib.ar_mx4_linear(ctypes.byref(params), _stream(stream)), "ar_mx4_linear")
+
+
+def adapter_params(adapters, rank, index, scale, a, a_stride, a_adapter_stride, a_rank_stride, b,
+                   b_stride, b_adapter_stride, b_rank_stride) -> ar_adapter_params:
+    """The low-rank adapters of one ar_mx4_linear_adapters: index int32 [rows],
+    scale float32 [adapters] or None, a and b bf16.  The result keeps the
+    tensors; their types and sizes are not looked at."""
+    tensors = index, scale, a, b
+    index, scale, a, b = _gpu_ptrs("adapter_params", *tensors)
+    p = ar_adapter_params(adapters, rank, index, scale, a, a_stride, a_adapter_stride,
+                          a_rank_stride, b, b_stride, b_adapter_stride, b_rank_stride, 0)
+    p.tensors = tensors
+    return p
+
+
+def ar_adapter_work_bytes(linear: ar_linear_params, adapters: ar_adapter_params) -> int:
+    return _check(_lib.ar_adapter_work_bytes(ctypes.byref(linear), ctypes.byref(adapters)),
+                  "ar_adapter_work_bytes")
+
+
+def ar_mx4_linear_adapters(linear: ar_linear_params, adapters: ar_adapter_params, work,
+                           stream=None) -> None:
+    """work: a device tensor of at least ar_adapter_work_bytes(linear, adapters)
+    bytes, of this call alone while it runs (None where that is 0)."""
+    w, = _gpu_ptrs("ar_mx4_linear_adapters", work)
+    nbytes = 0 if work is None else work.numel() * work.element_size()
+    _check(_lib.ar_mx4_linear_adapters(ctypes.byref(linear), ctypes.byref(adapters), w, nbytes,
+                                       _stream(stream)), "ar_mx4_linear_adapters")
 
 
 def cache_params(fmt, pages, page, kv_heads, dim, k, v, page_stride, token_stride, head_stride,

@@ -90,8 +90,6 @@ inline int check_cache_rows(const ar_kv_cache* c) {
   return aligned(c->k_scales, 4) && aligned(c->v_scales, 4) ? AR_OK : AR_EALIGN;
 }
 
-__device__ __forceinline__ u32x4 ldg16(const uint8_t* p) { return *reinterpret_cast<const u32x4*>(p); }
-
 // An element that is the same for all lanes, through the scalar cache: page
 // tables and lengths, which no kernel of this library writes.
 __device__ __forceinline__ int ld_const(const int32_t* p, int64_t i) {

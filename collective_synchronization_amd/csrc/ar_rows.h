@@ -19,6 +19,8 @@ constexpr float kE4m3Max = 448.0f;
 __host__ __device__ constexpr bool is_float_format(int f) { return f >= AR_BF16 && f <= AR_F32; }
 __host__ __device__ constexpr bool is_mx_format(int f) { return f == AR_E4M3_MX || f == AR_E2M1_MX; }
 
+__device__ __forceinline__ u32x4 ldg16(const uint8_t* p) { return *reinterpret_cast<const u32x4*>(p); }
+
 // ------------------------------------------------------------- chunks ---
 // A chunk is 8 elements of one row, 16-byte aligned in a 16-bit row.  Rows
 // are written below `count` only; a chunk that ends past it goes element by

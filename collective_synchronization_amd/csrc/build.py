@@ -17,12 +17,13 @@ SOURCES = [os.path.join(HERE, "ar_kernels.hip"), os.path.join(HERE, "ar_collecti
            os.path.join(HERE, "ar_static.hip"), os.path.join(HERE, "ar_state.hip"),
            os.path.join(HERE, "ar_linear.hip"), os.path.join(HERE, "ar_norm.hip"),
            os.path.join(HERE, "ar_mx.hip"), os.path.join(HERE, "ar_mxlinear.hip"),
+           os.path.join(HERE, "ar_adapters.hip"),
            os.path.join(HERE, "ar_cache.hip"), os.path.join(HERE, "ar_attention.hip"),
            os.path.join(HERE, "ar_select.cpp")]
 INCLUDE = os.path.join(os.path.dirname(PKG), "include")
 HEADERS = [os.path.join(INCLUDE, "ar_device.h"), os.path.join(INCLUDE, "ar_protocols.h"),
            os.path.join(HERE, "ar_host.h"), os.path.join(HERE, "ar_rows.h"),
-           os.path.join(HERE, "ar_cache.h"),
+           os.path.join(HERE, "ar_cache.h"), os.path.join(HERE, "ar_mxlinear.h"),
            os.path.join(INCLUDE, "ar.h"),
            os.path.join(INCLUDE, "ar_dev.h")]
 ARCH = os.environ.get("AR_OFFLOAD_ARCH", "gfx950")

@@ -498,6 +498,52 @@ typedef struct {
  */
 int ar_mx4_linear(const ar_linear_params* p, void* stream);
 
+/* Largest rank ar_mx4_linear_adapters takes. */
+#define AR_ADAPTER_MAX_RANK 128
+
+typedef struct {
+    int32_t adapters;           /* how many there are, >= 0 */
+    int32_t rank;               /* of all of them, 0 .. AR_ADAPTER_MAX_RANK */
+    const int32_t* index;       /* device int32[rows]: each token's adapter */
+    const float* scale;         /* device float[adapters]; NULL: ones */
+    const void* a;              /* AR_BF16: rank r's adapter i, row j of `rank` rows of `inputs` */
+    int64_t a_stride, a_adapter_stride, a_rank_stride;
+    const void* b;              /* AR_BF16: row n of `outputs` rows of `rank` */
+    int64_t b_stride, b_adapter_stride, b_rank_stride;
+    int32_t reserved;           /* must be 0 */
+} ar_adapter_params;
+
+/*
+ * ar_mx4_linear_adapters -- ar_mx4_linear with a low-rank adapter of each
+ * token's own beside the weights that all share (the requests of a batch have
+ * different ones): for every rank r and token m with adapter i = index[m],
+ *     y_r[m][n] += sum over j of t[j] * b_{r,i}[n][j],
+ *     t[j] = scale[i] * sum over k of x_r[m][k] * a_{r,i}[j][k],
+ * added to the sum that ar_mx4_linear forms, before its one rounding to y.  An
+ * index outside 0 .. adapters - 1: no adapter.  Tokens of one adapter may stand
+ * anywhere; they cost least next to each other.  Smaller adapters have zeros in
+ * the rest of their rows.
+ *   a, b: row j of rank r's adapter i at a + r*a_rank_stride +
+ *      i*a_adapter_stride + j*a_stride, alignment as for AR_BF16 rows; rank
+ *      strides 0 where the ranks share them: b of a shard that is split over
+ *      its inputs (t is then a part of the sum over ranks as y is), a of one
+ *      that is split over its outputs, whose ranks share the tokens too.
+ *   work: device, 256-byte aligned, at least ar_adapter_work_bytes(p, q) bytes
+ *      (AR_ESIZE); used for the time of the call, so calls that may overlap
+ *      need each their own.
+ * The values of x go as bf16 (8- and 4-bit ones without loss within its range)
+ * times a into binary32 sums; t enters its second product as bf16 parts, off
+ * by at most 2^-15 of itself for AR_BF16 y and 2^-23 for AR_F32; so its products
+ * with infinities in b may be NaN.  The order of every sum is fixed by the
+ * sizes, so equal calls give equal bits, and a token's bits do not depend on the
+ * other tokens' adapters.  adapters, rank or inputs 0: ar_mx4_linear alone.
+ */
+int ar_mx4_linear_adapters(const ar_linear_params* p, const ar_adapter_params* q, void* work,
+                           int64_t work_bytes, void* stream);
+
+/* Bytes of its work buffer, by sizes, strides and y_format; < 0 on bad parameters. */
+int64_t ar_adapter_work_bytes(const ar_linear_params* p, const ar_adapter_params* q);
+
 /*
  * A paged cache of keys and values.  A page holds `page` tokens; token t of
  * page p has for every head h of the cache a row of `dim` keys at
