@@ -21,10 +21,10 @@ struct TokenArgs {
   const int32_t* index;
   const float* scale;
   uint8_t* t;
-  int64_t t_stride, t_rank;
-  int32_t M, K, nb;
+  int64_t t_stride, t_part, t_rank;  // part p of rank r's row m: t + p * t_part + r * t_rank + m * t_stride
+  int32_t M, K;
   int32_t count, rank;
-  int32_t slots, r_groups, m_tiles;
+  int32_t splits, slots, r_groups, m_groups;
 };
 
 // A lane's operands of 128 elements of K: group g has 32 of them, from 32g on,
@@ -32,11 +32,11 @@ struct TokenArgs {
 // at a time in every format.
 template <int XF>
 constexpr int row_pieces() { return elem_bits<XF>() / 4; }
-template <int XF, int NR>
+template <int XF, int TT>
 struct TokenStep {
-  u32x4 x[row_pieces<XF>()];
-  uint32_t s;
-  u32x4 a[NR][4];
+  u32x4 x[TT][row_pieces<XF>()];
+  uint32_t s[TT];
+  u32x4 a[4];
 };
 
 template <int XF>
@@ -55,131 +55,367 @@ __device__ __forceinline__ u32x4 token_operand(const u32x4 (&x)[row_pieces<XF>()
   }
 }
 
-// A binary32 value as P bf16 values whose sum it is, to 16 bits for 2 and to all
-// 24 for 3: the leading ones cut, so none of them overflows, the last rounded.
-// Infinities and NaNs are in the first alone.
-template <int P>
-__device__ __forceinline__ void bf16_parts(float v, uint32_t (&p)[P]) {
-  const uint32_t bits = __float_as_uint(v);
-  const bool fine = abs_bits(v) < kInfBits;
-  p[0] = abs_bits(v) > kInfBits ? 0x7FC0u : bits >> 16;
-  float rest = fine ? v - __uint_as_float(bits & 0xFFFF0000u) : 0.0f;
-  if constexpr (P == 3) {
-    const uint32_t next = __float_as_uint(rest) & 0xFFFF0000u;
-    p[1] = next >> 16;
-    rest -= __uint_as_float(next);
+// 8 elements of a token's row from `at` on, as it lies in memory, and their values.
+template <int XF>
+struct Token8 {
+  u32x4 d;
+  uint32_t s;
+};
+template <int XF>
+__device__ __forceinline__ Token8<XF> load_token8(const uint8_t* x, const uint8_t* xs, int at) {
+  Token8<XF> t{};
+  const uint8_t* p = x + (int64_t)at * elem_bits<XF>() / 8;
+  if constexpr (XF == AR_BF16) {
+    t.d = ldg16(p);
+  } else if constexpr (XF == AR_E2M1_MX) {
+    t.d.x = *reinterpret_cast<const uint32_t*>(p);
+  } else {
+    const u32x2 v = *reinterpret_cast<const u32x2*>(p);
+    t.d.x = v.x;
+    t.d.y = v.y;
   }
-  p[P - 1] = bf16_pair(rest, 0.0f) & 0xFFFFu;
+  if constexpr (is_mx_format(XF)) t.s = xs[at / 32];
+  return t;
+}
+template <int XF>
+__device__ __forceinline__ void token8(const Token8<XF>& t, float (&v)[8]) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  const float s = XF == AR_E4M3_ROW ? 1.0f : __uint_as_float(t.s << 23);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    f32x2 p;
+    if constexpr (XF == AR_BF16) {
+      p = f32x2{bf_lo(t.d[k]), bf_hi(t.d[k])};
+    } else if constexpr (XF == AR_E2M1_MX) {
+      if (k == 0) p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(t.d.x, s, 0);
+      if (k == 1) p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(t.d.x, s, 1);
+      if (k == 2) p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(t.d.x, s, 2);
+      if (k == 3) p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(t.d.x, s, 3);
+    } else {
+      p = k % 2 == 0 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(t.d[k / 2], s, false)
+                     : __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(t.d[k / 2], s, true);
+    }
+    v[2 * k] = p.x;
+    v[2 * k + 1] = p.y;
+  }
 }
 
-constexpr int kTokenWaves = 8;
-
-// t of 16 tokens in 16 * NR of an adapter's dimensions.  Bound by the way of a
-// and x to the CU: the waves share K, a step of 128 each in turn, the next one on
-// its way while one is multiplied, and join their sums in shared memory.  The
-// tokens' adapters go one after the other, `slots` workgroups taking turns.
-template <int XF, int NR, int P>
-__global__ __launch_bounds__(kWave * kTokenWaves) void k_adapter_tokens(TokenArgs s) {
-  __shared__ f32x4 part[kTokenWaves * NR * kWave];
-  const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+// t of one token, 4 dimensions a wave, for up to kFewTokens tokens: each has rows
+// of a to itself, so they are read as they are multiplied, in binary32, 512
+// elements of K at a time.  WK waves share K; without, a workgroup has 16
+// dimensions.  Bound by the loads' latency: index, then x and a, then the join.
+constexpr int kFewTokens = 32;
+constexpr int64_t kFewProducts = int64_t(1) << 25;
+template <int XF, int WK>
+__global__ __launch_bounds__(kBlock) void k_adapter_few_tokens(TokenArgs s) {
+  static_assert(WK == 1 || WK == kWavesPerBlock, "");
+  __shared__ f32x4 part[kWavesPerBlock];
+  const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  constexpr int per = WK == 1 ? 16 : 4;                    // dimensions of a workgroup
   int b = blockIdx.x;
-  const int slot = b % s.slots;
-  b /= s.slots;
-  const int j0 = b % s.r_groups * 16 * NR;
+  const int j0 = b % s.r_groups * per + (WK == 1 ? 4 * wave : 0);
   b /= s.r_groups;
-  const int m = b % s.m_tiles * 16 + c, r = b / s.m_tiles;
-  const int mine = m < s.M ? s.index[m] : -1;
-  const int row = min(m, s.M - 1);
-  const uint8_t* x = s.x + r * s.x_rank + row * s.x_stride;
-  const uint8_t* xs = s.xs + r * s.xs_rank + row * s.xs_stride;
-  uint32_t left = (uint32_t)__ballot((uint32_t)mine < (uint32_t)s.count) & 0xFFFFu;
-  for (int turn = 0; left != 0; ++turn) {
-    const int which = __builtin_amdgcn_readlane(mine, __builtin_ctz(left));
-    const bool take = mine == which;
-    left &= ~(uint32_t)__ballot(take);
-    if (turn % s.slots != slot) continue;
-    const uint8_t* a[NR];
-    f32x4 acc[NR];
+  const int m = b % s.M, r = b / s.M;
+  const int which = s.index[m];
+  if ((uint32_t)which >= (uint32_t)s.count) return;
+  const uint8_t* x = s.x + r * s.x_rank + m * s.x_stride;
+  const uint8_t* xs = s.xs + r * s.xs_rank + m * s.xs_stride;
+  const uint8_t* a[4];
+  f32x4 sum = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int i = 0; i < NR; ++i) {
-      a[i] = s.a + r * s.a_rank + which * s.a_adapter + min(j0 + 16 * i + c, s.rank - 1) * s.a_stride;
-      acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    }
-    auto load = [&](int st, TokenStep<XF, NR>& f) {
-      const int at = st * 128 + 32 * g;
-      constexpr int per = 128 / elem_bits<XF>();
-      const bool whole = st * 128 + 128 <= s.K;
+  for (int e = 0; e < 4; ++e)
+    a[e] = s.a + r * s.a_rank + which * s.a_adapter + min(j0 + e, s.rank - 1) * s.a_stride;
+  const float scale = s.scale ? s.scale[which] : 1.0f;
+  for (int k0 = (WK == 1 ? 0 : wave) * 512; k0 < s.K; k0 += WK * 512) {
+    const int at = k0 + lane * 8;
+    if (at >= s.K) continue;
+    const Token8<XF> t = load_token8<XF>(x, xs, at);
+    u32x4 w[4];
 #pragma unroll
-      for (int q = 0; q < row_pieces<XF>(); ++q) {
-        f.x[q] = u32x4{0u, 0u, 0u, 0u};
-        if (whole || at + q * per < s.K) f.x[q] = ldg16(x + (int64_t)(at + q * per) * elem_bits<XF>() / 8);
-      }
-      f.s = 127;
-      if constexpr (is_mx_format(XF)) {
-        if (whole || at < s.K) f.s = xs[at / 32];
-      }
+    for (int e = 0; e < 4; ++e) w[e] = ldg16(a[e] + (int64_t)at * 2);
+    float v[8];
+    token8<XF>(t, v);
+    const bool cut = at + 8 > s.K;                         // K ends in these
 #pragma unroll
-      for (int i = 0; i < NR; ++i)
+    for (int u = 0; u < 8; ++u)
+      if (cut && at + u >= s.K) v[u] = 0.0f;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          f.a[i][u] = u32x4{0u, 0u, 0u, 0u};
-          if (whole || at + 8 * u < s.K) f.a[i][u] = ldg16(a[i] + (int64_t)(at + 8 * u) * 2);
-        }
-    };
-    auto multiply = [&](int st, TokenStep<XF, NR>& f) {
-      const int at = st * 128 + 32 * g;
-      if (st * 128 + 128 > s.K) {                          // K ends in this one
-        constexpr int per = 128 / elem_bits<XF>();
-#pragma unroll
-        for (int q = 0; q < row_pieces<XF>(); ++q) f.x[q] = keep_inputs<XF>(f.x[q], at + q * per, s.K);
-#pragma unroll
-        for (int i = 0; i < NR; ++i)
-#pragma unroll
-          for (int u = 0; u < 4; ++u) f.a[i][u] = keep_inputs<AR_BF16>(f.a[i][u], at + 8 * u, s.K);
-      }
+    for (int e = 0; e < 4; ++e) {
+      if (cut) w[e] = keep_inputs<AR_BF16>(w[e], at, s.K);
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const bf16x8 v = __builtin_bit_cast(bf16x8, token_operand<XF>(f.x, f.s, u));
-#pragma unroll
-        for (int i = 0; i < NR; ++i)
-          acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, f.a[i][u]), v, acc[i], 0, 0, 0);
-      }
-    };
-    const int steps = (s.K + 127) / 128;
-    if (wave < steps) {
-      TokenStep<XF, NR> cur;
-      int st = wave;
-      load(st, cur);
-      for (; st + kTokenWaves < steps; st += kTokenWaves) {
-        TokenStep<XF, NR> next;
-        load(st + kTokenWaves, next);
-        multiply(st, cur);
-        cur = next;
-      }
-      multiply(st, cur);
-    }
-#pragma unroll
-    for (int i = 0; i < NR; ++i) part[(wave * NR + i) * kWave + lane] = acc[i];
-    __syncthreads();
-    if (wave < NR && take) {
-      f32x4 v = part[wave * kWave + lane];
-#pragma unroll
-      for (int w = 1; w < kTokenWaves; ++w) v += part[(w * NR + wave) * kWave + lane];
-      if (s.scale) v *= s.scale[which];
-      if constexpr (XF == AR_E4M3_ROW) v *= *reinterpret_cast<const float*>(xs);
-      const int j = j0 + 16 * wave + 4 * g;
-      uint32_t p[4][P];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) bf16_parts<P>(j + e < s.rank ? v[e] : 0.0f, p[e]);
-      uint8_t* t = s.t + r * s.t_rank + m * s.t_stride + j / 8 * (16 * P) + j % 8 * 2;
-      if (j0 + 16 * wave < s.rank) {
-#pragma unroll
-        for (int q = 0; q < P; ++q)
-          *reinterpret_cast<u32x2*>(t + 16 * q) = u32x2{pack2(p[0][q], p[1][q]), pack2(p[2][q], p[3][q])};
+        sum[e] = __builtin_fmaf(v[2 * u], bf_lo(w[e][u]), sum[e]);
+        sum[e] = __builtin_fmaf(v[2 * u + 1], bf_hi(w[e][u]), sum[e]);
       }
     }
+  }
+#pragma unroll
+  for (int d = 32; d > 0; d /= 2)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum[e] += __shfl_xor(sum[e], d);
+  if constexpr (WK > 1) {
+    if (lane == 0) part[wave] = sum;
     __syncthreads();
+    if (wave > 0) return;
+    sum = part[0];
+#pragma unroll
+    for (int w = 1; w < WK; ++w) sum += part[w];
+  }
+  if (lane > 0 || j0 >= (s.rank + 15) / 16 * 16) return;
+  sum *= scale;
+  if constexpr (XF == AR_E4M3_ROW) sum *= *reinterpret_cast<const float*>(xs);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) sum[e] = j0 + e < s.rank ? sum[e] : 0.0f;
+  *reinterpret_cast<f32x4*>(s.t + r * s.t_rank + m * s.t_stride + j0 * 4) = sum;
+}
+
+constexpr int kTokenGroup = 256;
+
+// Parts of t for 16 * TT tokens of one adapter, in 16 * WR of its dimensions, over
+// a share of K.  Bound by the way of a and x to the CUs.  A group is 256 tokens:
+// its workgroups find the group's adapters, each with the list of its tokens, and
+// take turns with them, 16 * TT tokens at a time, so that tokens in any order read
+// an adapter's rows once for all of them.  `splits` workgroups share K for each.
+// (Groups go round the XCDs, so that each reads all of K: with a share of K each,
+// rows 8 and 16 KiB apart met a quarter of an L2's channels, 4096 x 8192, rank 64,
+// 62 us.)  In a workgroup WR waves have 16 dimensions each (they read the same tokens,
+// the later ones from the L1), WK share the steps, and join their sums in shared memory;
+// the workgroups' sums are joined by k_adapter_sum.
+template <int XF, int WR, int WK, int TT>
+__global__ __launch_bounds__(kWave * WR * WK, 2) void k_adapter_tokens(TokenArgs s) {
+  constexpr int W = WR * WK;
+  __shared__ f32x4 part[WK > 1 ? W * TT * kWave : 1];
+  __shared__ int list[kTokenGroup];
+  const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wr = wave % WR, wk = wave / WR;
+  int b = blockIdx.x;
+  const int m0 = b % s.m_groups * kTokenGroup;
+  b /= s.m_groups;
+  const int slot = b % s.slots;
+  b /= s.slots;
+  const int split = b % s.splits;
+  b /= s.splits;
+  const int j0 = (b % s.r_groups * WR + wr) * 16, r = b / s.r_groups;
+  const int steps = (s.K + 127) / 128, each = (steps + s.splits - 1) / s.splits;
+  const int st0 = split * each + wk, st1 = min(steps, split * each + each);
+  int mine[4];
+  uint64_t left[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int m = m0 + 64 * k + lane;
+    mine[k] = m < s.M ? s.index[m] : -1;
+    left[k] = __ballot((uint32_t)mine[k] < (uint32_t)s.count);
+  }
+  int turn = 0;
+  while ((left[0] | left[1] | left[2] | left[3]) != 0) {
+    int which = 0;
+    bool found = false;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (!found && left[k] != 0) {
+        which = __builtin_amdgcn_readlane(mine[k], __builtin_ctzll(left[k]));
+        found = true;
+      }
+    int tokens = 0, before = 0;
+    uint64_t has[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      has[k] = __ballot(mine[k] == which) & left[k];
+      left[k] &= ~has[k];
+      tokens += __builtin_popcountll(has[k]);
+    }
+    const int first = turn;
+    turn += (tokens + 16 * TT - 1) / (16 * TT);
+    // this workgroup's turns among them
+    if (first + (slot - first % s.slots + s.slots) % s.slots >= turn) continue;
+    __syncthreads();                                       // the list was read
+    if (wave == 0) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint64_t below = has[k] & ((uint64_t(1) << lane) - 1);
+        if (has[k] >> lane & 1) list[before + __builtin_popcountll(below)] = 64 * k + lane;
+        before += __builtin_popcountll(has[k]);
+      }
+    }
+    __syncthreads();
+    const float scale = s.scale ? s.scale[which] : 1.0f;
+    const uint8_t* a = s.a + r * s.a_rank + which * s.a_adapter + min(j0 + c, s.rank - 1) * s.a_stride;
+    for (int t0 = 0, it = first; t0 < tokens; t0 += 16 * TT, ++it) {
+      if (it % s.slots != slot) continue;
+      const int tiles = min(TT, (tokens - t0 + 15) / 16);
+      const uint8_t *x[TT], *xs[TT];
+      int m[TT];
+      f32x4 acc[TT];
+#pragma unroll
+      for (int j = 0; j < TT; ++j) {
+        m[j] = m0 + list[min(t0 + 16 * j + c, tokens - 1)];
+        x[j] = s.x + r * s.x_rank + m[j] * s.x_stride;
+        xs[j] = s.xs + r * s.xs_rank + m[j] * s.xs_stride;
+        acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      }
+      auto load = [&](int st, TokenStep<XF, TT>& f) {
+        const int at = st * 128 + 32 * g;
+        constexpr int per = 128 / elem_bits<XF>();
+        const bool whole = st * 128 + 128 <= s.K;
+#pragma unroll
+        for (int j = 0; j < TT; ++j) {
+          if (TT > 1 && j >= tiles) continue;
+#pragma unroll
+          for (int q = 0; q < row_pieces<XF>(); ++q) {
+            f.x[j][q] = u32x4{0u, 0u, 0u, 0u};
+            if (whole || at + q * per < s.K) f.x[j][q] = ldg16(x[j] + (int64_t)(at + q * per) * elem_bits<XF>() / 8);
+          }
+          f.s[j] = 127;
+          if constexpr (is_mx_format(XF)) {
+            if (whole || at < s.K) f.s[j] = xs[j][at / 32];
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          f.a[u] = u32x4{0u, 0u, 0u, 0u};
+          if (whole || at + 8 * u < s.K) f.a[u] = ldg16(a + (int64_t)(at + 8 * u) * 2);
+        }
+      };
+      // a step that K ends in has zeros behind it
+      auto keep = [&](int st, TokenStep<XF, TT>& f) {
+        const int at = st * 128 + 32 * g;
+        constexpr int per = 128 / elem_bits<XF>();
+        if (st * 128 + 128 <= s.K) return;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) f.a[u] = keep_inputs<AR_BF16>(f.a[u], at + 8 * u, s.K);
+#pragma unroll
+        for (int j = 0; j < TT; ++j)
+#pragma unroll
+          for (int q = 0; q < row_pieces<XF>(); ++q) f.x[j][q] = keep_inputs<XF>(f.x[j][q], at + q * per, s.K);
+      };
+      auto multiply = [&](const TokenStep<XF, TT>& f) {
+#pragma unroll
+        for (int j = 0; j < TT; ++j) {
+          if (TT > 1 && j >= tiles) continue;
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                __builtin_bit_cast(bf16x8, f.a[u]), __builtin_bit_cast(bf16x8, token_operand<XF>(f.x[j], f.s[j], u)),
+                acc[j], 0, 0, 0);
+        }
+      };
+      if (st0 < st1) {
+        TokenStep<XF, TT> cur;
+        int st = st0;
+        load(st, cur);
+        for (; st + WK < st1; st += WK) {                  // the next one is on its way
+          TokenStep<XF, TT> next;
+          load(st + WK, next);
+          multiply(cur);                                   // never the last step
+          cur = next;
+        }
+        keep(st, cur);
+        multiply(cur);
+      }
+      if constexpr (WK > 1) {
+#pragma unroll
+        for (int j = 0; j < TT; ++j) part[(wave * TT + j) * kWave + lane] = acc[j];
+        __syncthreads();
+      }
+#pragma unroll
+      for (int j = 0; j < TT; ++j) {
+        if (j % WK != wk || t0 + 16 * j + c >= tokens || j0 >= s.rank) continue;
+        f32x4 v = acc[j];
+        if constexpr (WK > 1) {
+          v = part[(wr * TT + j) * kWave + lane];
+#pragma unroll
+          for (int w = 1; w < WK; ++w) v += part[((w * WR + wr) * TT + j) * kWave + lane];
+        }
+        v *= scale;
+        if constexpr (XF == AR_E4M3_ROW) v *= *reinterpret_cast<const float*>(xs[j]);
+        const int d = j0 + 4 * g;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = d + e < s.rank ? v[e] : 0.0f;
+        *reinterpret_cast<f32x4*>(s.t + split * s.t_part + r * s.t_rank + m[j] * s.t_stride + d * 4) = v;
+      }
+      if constexpr (WK > 1) __syncthreads();
+    }
+  }
+}
+
+// The parts of t added up, in order, into the first.
+struct TokenSum {
+  uint8_t* t;
+  int64_t part, pieces;              // bytes of a part, 16-byte pieces of it
+  int32_t parts;
+};
+__global__ __launch_bounds__(kBlock) void k_adapter_sum(TokenSum s) {
+  const int64_t at = (int64_t)blockIdx.x * kBlock + threadIdx.x;
+  if (at >= s.pieces) return;
+  uint8_t* p = s.t + at * 16;
+  f32x4 v[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    v[k] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    if (k < s.parts) v[k] = *reinterpret_cast<const f32x4*>(p + k * s.part);
+  }
+#pragma unroll
+  for (int k = 1; k < 8; ++k)
+    if (k < s.parts) v[0] += v[k];
+  *reinterpret_cast<f32x4*>(p) = v[0];
+}
+
+// What the adapters add, ready in binary32, for tokens that are too few for the
+// layer's largest tiles: every thread has an output, and its row of b for one
+// adapter in registers, which it uses for all ranks that share b and for as many
+// of its tokens as have that adapter next to each other.  So rows of b are read
+// as they lie, once, where the layer's own waves would each gather them again
+// for 16 tokens (64 tokens with an adapter each, rank 64, 4 shards of 8192 x 2048: 173
+// us).  Bound by the stream of b.  t is the same for all threads: scalars.
+struct DeltaArgs {
+  const int32_t* index;
+  const float* t;                    // strides in floats
+  int64_t t_stride, t_rank;
+  const uint8_t* b;
+  int64_t b_stride, b_adapter, b_rank;
+  float* delta;
+  int64_t delta_stride, delta_rank;
+  int32_t M, N, count, rank;
+  int32_t ranks, n_blocks, m_blocks, tokens;   // ranks of one workgroup, its tokens
+};
+template <int R16>
+__global__ __launch_bounds__(kBlock) void k_adapter_delta(DeltaArgs s) {
+  int b = blockIdx.x;
+  const int n = b % s.n_blocks * kBlock + threadIdx.x;
+  b /= s.n_blocks;
+  const int m0 = b % s.m_blocks * s.tokens, r0 = b / s.m_blocks * s.ranks;
+  const uint8_t* row = s.b + r0 * s.b_rank + min(n, s.N - 1) * s.b_stride;
+  u32x4 w[2 * R16];
+  int have = -1;
+  for (int m = m0; m < min(s.M, m0 + s.tokens); ++m) {
+    const int which = ld_const(s.index, m);
+    if ((uint32_t)which >= (uint32_t)s.count) continue;
+    if (which != have) {
+      have = which;
+#pragma unroll
+      for (int k = 0; k < 2 * R16; ++k) w[k] = load_b8(row + which * s.b_adapter, 8 * k, s.rank);
+#pragma unroll
+      for (int k = 0; k < 2 * R16; ++k) w[k] = keep_b8(w[k], 8 * k, s.rank);
+    }
+    for (int r = r0; r < r0 + s.ranks; ++r) {
+      const float* t = s.t + r * s.t_rank + m * s.t_stride;
+      float sum = 0.0f;
+#pragma unroll
+      for (int k = 0; k < R16; ++k) {                      // (t's row ends with a multiple of 16)
+        if (16 * k >= s.rank) continue;
+        float part = 0.0f;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const uint32_t d = w[2 * k + u / 4][u % 4];
+          part = __builtin_fmaf(ld_const(t, 16 * k + 2 * u), bf_lo(d), part);
+          part = __builtin_fmaf(ld_const(t, 16 * k + 2 * u + 1), bf_hi(d), part);
+        }
+        sum += part;
+      }
+      if (n < s.N) s.delta[r * s.delta_rank + m * s.delta_stride + n] = sum;
+    }
   }
 }
 
@@ -210,6 +446,7 @@ static int check_adapter_rows(const ar_linear_params* p, const ar_adapter_params
   if (q->a_adapter_stride >= most || q->a_rank_stride >= most || q->b_adapter_stride >= most ||
       q->b_rank_stride >= most)
     return AR_ESIZE;
+  if (q->b_stride >= 1 << 23) return AR_ESIZE;             // 128 rows' offsets stay 32-bit
   if (q->a_adapter_stride % 8 || q->b_adapter_stride % 8) return AR_EALIGN;
   if (p->nranks > 1 && (q->a_rank_stride % 8 || q->b_rank_stride % 8)) return AR_EALIGN;
   return AR_OK;
@@ -222,52 +459,136 @@ static int t_ranks(const ar_linear_params* p, const ar_adapter_params* q) {
              : p->nranks;
 }
 
-static int64_t t_row_bytes(const ar_linear_params* p, const ar_adapter_params* q) {
-  return ceil_div64(q->rank, 16) * 16 * 2 * t_parts(p->y_format);
+static int64_t t_row_bytes(const ar_adapter_params* q) { return ceil_div64(q->rank, 16) * 16 * 4; }
+
+// Workgroups that share K, and those that share a group's adapters, for about
+// 1024 in all (of which many may have no turn).
+constexpr int kTokenBlocks = 1024;
+
+// Outputs of all ranks up to which up to 16 dimensions of 16 tokens' adapters are
+// left to the layer's own waves: 4 x 16 x 8192 18.4 us both ways with an adapter
+// for each token, 14.5 and 17.8 with one for all.
+constexpr int64_t kLaneOutputs = 1 << 19;
+
+struct TokenPlan {
+  int32_t wr, splits, slots;         // wr 0: few tokens
+};
+static TokenPlan plan_tokens(const ar_linear_params* p, const ar_adapter_params* q) {
+  TokenPlan t{0, 1, 1};
+  if (p->rows <= kFewTokens ||
+      (p->rows <= 1024 && p->rows * t_ranks(p, q) * p->inputs * q->rank <= kFewProducts))
+    return t;
+  t.wr = q->rank <= 16 ? 1 : (q->rank <= 32 ? 2 : 4);
+  const int64_t blocks = t_ranks(p, q) * ceil_div64(p->rows, kTokenGroup) * ceil_div64(q->rank, 16 * t.wr);
+  const int64_t steps = ceil_div64(p->inputs, 128 * (4 / t.wr));
+  while (t.splits < 8 && 2 * t.splits <= steps && blocks * t.splits < kTokenBlocks) t.splits *= 2;
+  const int64_t group = p->rows < kTokenGroup ? p->rows : kTokenGroup;
+  const int64_t turns = group < q->adapters + 4 ? group : q->adapters + 4;
+  while (t.slots < turns && blocks * t.splits * t.slots < kTokenBlocks) t.slots *= 2;
+  return t;
+}
+
+// Bytes of t, and of the sums that are made ready for the layer (0: none are).
+static int64_t t_bytes(const ar_linear_params* p, const ar_adapter_params* q) {
+  return (plan_tokens(p, q).splits * t_ranks(p, q) * p->rows * t_row_bytes(q) + 255) / 256 * 256;
+}
+static int64_t delta_row(const ar_linear_params* p) { return (p->outputs + 3) / 4 * 4; }
+static int64_t delta_bytes(const ar_linear_params* p, const ar_adapter_params* q) {
+  const MxLinArgs a = linear_args(p);
+  if (large_tiles(a, p->nranks)) return 0;
+  if (p->rows <= 16 && q->rank <= 16 && p->nranks * p->rows * p->outputs <= kLaneOutputs) return 0;
+  return (p->nranks * p->rows * delta_row(p) * 4 + 255) / 256 * 256;
 }
 
 static int64_t adapter_work(const ar_linear_params* p, const ar_adapter_params* q) {
-  if (!adapters_count(p, q)) return 0;
-  return (t_ranks(p, q) * p->rows * t_row_bytes(p, q) + 255) / 256 * 256;
+  return adapters_count(p, q) ? t_bytes(p, q) + delta_bytes(p, q) : 0;
 }
 
-template <int XF, int NR, int P>
-static hipError_t launch_tokens(const TokenArgs& a0, int ranks, hipStream_t s) {
-  TokenArgs a = a0;
-  a.r_groups = (a.rank + 16 * NR - 1) / (16 * NR);
-  // as many workgroups at once for the adapters of 16 tokens as fill the chip
-  const int64_t groups = ceil_div64(a0.M, 16) * ranks * a.r_groups;
-  a.slots = 1;
-  while (a.slots < 16 && a.slots < a.M && a.slots < a.count && groups * a.slots < 512) a.slots *= 2;
-  const int64_t most = most_blocks(kWave * kTokenWaves) / ((int64_t)ranks * a.r_groups * a.slots) * 16;
-  for (int64_t m = 0; m < a0.M; m += most) {
-    a.M = (int32_t)(a0.M - m < most ? a0.M - m : most);
-    a.m_tiles = (a.M + 15) / 16;
-    a.x = a0.x + m * a0.x_stride;
-    if (a0.xs) a.xs = a0.xs + m * a0.xs_stride;
-    a.index = a0.index + m;
-    a.t = a0.t + m * a0.t_stride;
-    const int64_t blocks = (int64_t)ranks * a.m_tiles * a.r_groups * a.slots;
-    const hipError_t e = launch(k_adapter_tokens<XF, NR, P>, dim3((unsigned)blocks), dim3(kWave * kTokenWaves), s, a);
+static hipError_t launch_delta(const Adapters& ad, const MxLinArgs& a, int nranks, hipStream_t s) {
+  DeltaArgs d{};
+  d.index = ad.index;
+  d.t = reinterpret_cast<const float*>(ad.t);
+  d.t_stride = ad.t_stride / 4;
+  d.t_rank = ad.t_rank / 4;
+  d.b = ad.b;
+  d.b_stride = ad.b_stride;
+  d.b_adapter = ad.b_adapter;
+  d.b_rank = ad.b_rank;
+  d.delta = const_cast<float*>(ad.delta);
+  d.delta_stride = ad.delta_stride;
+  d.delta_rank = ad.delta_rank;
+  d.N = a.N;
+  d.count = ad.count;
+  d.rank = ad.rank;
+  d.ranks = ad.b_rank == 0 ? nranks : 1;
+  d.n_blocks = (a.N + kBlock - 1) / kBlock;
+  // tokens of a workgroup: as many as leave 1024 workgroups, at most 16
+  const int64_t all = (int64_t)(nranks / d.ranks) * d.n_blocks;
+  int64_t tokens = all * a.M / 1024;
+  tokens = tokens < 1 ? 1 : (tokens > 16 ? 16 : tokens);
+  d.tokens = (int32_t)tokens;
+  const int64_t most = most_blocks(kBlock) / all * tokens;
+  for (int64_t m = 0; m < a.M; m += most) {
+    d.M = (int32_t)(a.M - m < most ? a.M - m : most);
+    d.m_blocks = (int32_t)ceil_div64(d.M, tokens);
+    d.index = ad.index + m;
+    d.t = reinterpret_cast<const float*>(ad.t + m * ad.t_stride);
+    d.delta = const_cast<float*>(ad.delta) + m * ad.delta_stride;
+    const dim3 grid((unsigned)(all * d.m_blocks)), block(kBlock);
+    const hipError_t e = ad.rank <= 16   ? launch(k_adapter_delta<1>, grid, block, s, d)
+                         : ad.rank <= 32 ? launch(k_adapter_delta<2>, grid, block, s, d)
+                         : ad.rank <= 64 ? launch(k_adapter_delta<4>, grid, block, s, d)
+                                         : launch(k_adapter_delta<8>, grid, block, s, d);
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
 }
 
-template <int XF, int P>
-static hipError_t launch_tokens_rank(const TokenArgs& a, int ranks, hipStream_t s) {
-  if (a.rank <= 16 || a.M <= 16) return launch_tokens<XF, 1, P>(a, ranks, s);
-  if (a.rank <= 32) return launch_tokens<XF, 2, P>(a, ranks, s);
-  return launch_tokens<XF, 4, P>(a, ranks, s);
+template <int XF, int WR, int WK, int TT>
+static hipError_t launch_tokens(const TokenArgs& a0, int ranks, hipStream_t s) {
+  TokenArgs a = a0;
+  constexpr int W = WR * WK;
+  a.r_groups = (a.rank + 16 * WR - 1) / (16 * WR);
+  const int64_t each = (int64_t)ranks * a.r_groups * a.slots * a.splits;
+  const int64_t most = most_blocks(kWave * W) / each * kTokenGroup;
+  for (int64_t m = 0; m < a0.M; m += most) {
+    a.M = (int32_t)(a0.M - m < most ? a0.M - m : most);
+    a.m_groups = (a.M + kTokenGroup - 1) / kTokenGroup;
+    a.x = a0.x + m * a0.x_stride;
+    if (a0.xs) a.xs = a0.xs + m * a0.xs_stride;
+    a.index = a0.index + m;
+    a.t = a0.t + m * a0.t_stride;
+    const hipError_t e = launch(k_adapter_tokens<XF, WR, WK, TT>, dim3((unsigned)(each * a.m_groups)),
+                                dim3(kWave * W), s, a);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
-template <int P>
-static hipError_t launch_tokens_x(const TokenArgs& a, int xf, int ranks, hipStream_t s) {
+template <int XF>
+static hipError_t launch_few_tokens(const TokenArgs& a0, int ranks, hipStream_t s) {
+  TokenArgs a = a0;
+  const bool share = a.K > 512;                            // K is long enough for 4 waves
+  a.r_groups = (a.rank + 15) / 16 * (share ? 4 : 1);
+  const dim3 grid((unsigned)(ranks * a.M * a.r_groups)), block(kBlock);
+  return share ? launch(k_adapter_few_tokens<XF, kWavesPerBlock>, grid, block, s, a)
+               : launch(k_adapter_few_tokens<XF, 1>, grid, block, s, a);
+}
+
+template <int XF>
+static hipError_t launch_tokens_x(const TokenArgs& a, const TokenPlan& t, int ranks, hipStream_t s) {
+  if (t.wr == 0) return launch_few_tokens<XF>(a, ranks, s);
+  if (t.wr == 1) return launch_tokens<XF, 1, 4, 4>(a, ranks, s);
+  if (t.wr == 2) return launch_tokens<XF, 2, 2, 4>(a, ranks, s);
+  return launch_tokens<XF, 4, 1, 4>(a, ranks, s);
+}
+
+static hipError_t launch_tokens_any(const TokenArgs& a, const TokenPlan& t, int xf, int ranks, hipStream_t s) {
   switch (xf) {
-    case AR_BF16: return launch_tokens_rank<AR_BF16, P>(a, ranks, s);
-    case AR_E4M3_ROW: return launch_tokens_rank<AR_E4M3_ROW, P>(a, ranks, s);
-    case AR_E4M3_MX: return launch_tokens_rank<AR_E4M3_MX, P>(a, ranks, s);
-    default: return launch_tokens_rank<AR_E2M1_MX, P>(a, ranks, s);
+    case AR_BF16: return launch_tokens_x<AR_BF16>(a, t, ranks, s);
+    case AR_E4M3_ROW: return launch_tokens_x<AR_E4M3_ROW>(a, t, ranks, s);
+    case AR_E4M3_MX: return launch_tokens_x<AR_E4M3_MX>(a, t, ranks, s);
+    default: return launch_tokens_x<AR_E2M1_MX>(a, t, ranks, s);
   }
 }
 
@@ -295,6 +616,7 @@ int ar_mx4_linear_adapters(const ar_linear_params* p, const ar_adapter_params* q
   if (work_bytes < adapter_work(p, q)) return AR_ESIZE;
   const MxLinArgs a = linear_args(p);
   const int ranks = t_ranks(p, q);
+  const TokenPlan plan = plan_tokens(p, q);
   TokenArgs t{};
   t.x = a.x;
   t.x_stride = a.x_stride;
@@ -309,11 +631,13 @@ int ar_mx4_linear_adapters(const ar_linear_params* p, const ar_adapter_params* q
   t.index = q->index;
   t.scale = q->scale;
   t.t = static_cast<uint8_t*>(work);
-  t.t_stride = t_row_bytes(p, q);
+  t.t_stride = t_row_bytes(q);
   t.t_rank = ranks > 1 ? p->rows * t.t_stride : 0;
+  t.t_part = ranks * p->rows * t.t_stride;
   t.M = a.M;
   t.K = a.K;
-  t.nb = a.nb;
+  t.splits = plan.splits;
+  t.slots = plan.slots;
   t.count = q->adapters;
   t.rank = q->rank;
   Adapters ad{};
@@ -328,8 +652,19 @@ int ar_mx4_linear_adapters(const ar_linear_params* p, const ar_adapter_params* q
   ad.count = q->adapters;
   ad.rank = q->rank;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  const hipError_t e = t_parts(p->y_format) == 2 ? launch_tokens_x<2>(t, p->x_format, ranks, s)
-                                                 : launch_tokens_x<3>(t, p->x_format, ranks, s);
+  hipError_t e = launch_tokens_any(t, plan, p->x_format, ranks, s);
+  if (e == hipSuccess && plan.splits > 1) {
+    const TokenSum sum{t.t, t.t_part, t.t_part / 16, plan.splits};
+    const int64_t blocks = ceil_div64(sum.pieces, kBlock);
+    if (blocks > most_blocks(kBlock)) return AR_ESIZE;
+    e = launch(k_adapter_sum, dim3((unsigned)blocks), dim3(kBlock), s, sum);
+  }
+  if (delta_bytes(p, q) > 0) {
+    ad.delta = reinterpret_cast<const float*>(t.t + t_bytes(p, q));
+    ad.delta_stride = delta_row(p);
+    ad.delta_rank = p->rows * ad.delta_stride;
+    if (e == hipSuccess) e = launch_delta(ad, a, p->nranks, s);
+  }
   if (e != hipSuccess) return map_hip(e);
   return map_hip(launch_pieces(a, ad, p->x_format, p->y_format, p->nranks, s));
 }

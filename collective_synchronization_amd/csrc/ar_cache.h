@@ -90,11 +90,4 @@ inline int check_cache_rows(const ar_kv_cache* c) {
   return aligned(c->k_scales, 4) && aligned(c->v_scales, 4) ? AR_OK : AR_EALIGN;
 }
 
-// An element that is the same for all lanes, through the scalar cache: page
-// tables and lengths, which no kernel of this library writes.
-__device__ __forceinline__ int ld_const(const int32_t* p, int64_t i) {
-  typedef const __attribute__((address_space(4))) int32_t const_t;
-  return ((const_t*)p)[__builtin_amdgcn_readfirstlane((int)i)];
-}
-
 }  // namespace ar

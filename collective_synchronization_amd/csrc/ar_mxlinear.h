@@ -51,21 +51,26 @@ struct MxLinArgs {
 // No adapters.
 struct NoAdapters {};
 
+template <class A, class B> constexpr bool is_same = false;
+template <class A> constexpr bool is_same<A, A> = true;
+
 // Low-rank adapters: token m's is index[m] (none outside 0 .. count - 1), its
-// products with the adapter's first matrix are in t, and what they add to output
-// n is sum over j of t[m][j] * b[n][j].  t is held as bf16 parts whose sum it is,
-// 8 values of each part after 8 of the one before: 2 parts (16 bits) for bf16
-// outputs, 3 (all 24) for binary32 ones.  Strides in bytes.
+// products with the adapter's first matrix are the binary32 row t[m], with zeros
+// from `rank` on up to a multiple of 16, and what they add to output n is sum
+// over j of t[m][j] * b[n][j].  Strides in bytes.
 struct Adapters {
   const int32_t* index;
   const uint8_t* t;
   int64_t t_stride, t_rank;
   const uint8_t* b;
   int64_t b_stride, b_adapter, b_rank;
+  // not null: these sums, ready in binary32, element [m][n] of rank r at delta +
+  // r * delta_rank + m * delta_stride + n, for tokens with an adapter (never
+  // where large_tiles holds)
+  const float* delta;
+  int64_t delta_stride, delta_rank;
   int32_t count, rank;
 };
-template <int YF> constexpr int t_parts() { return YF == AR_F32 ? 3 : 2; }
-inline int t_parts(int yf) { return yf == AR_F32 ? 3 : 2; }
 
 // Scales of blocks b .. b+15 of a row of `nb`; TAIL: the row's last dword in the
 // place of those past its end.
@@ -248,53 +253,158 @@ __device__ __forceinline__ void store_out4(void* y, int64_t at, int n, int N, bo
   }
 }
 
-template <class A, class B> constexpr bool is_same = false;
-template <class A> constexpr bool is_same<A, A> = true;
+// A binary32 value as P bf16 values whose sum it is, to 16 bits for 2 and to all
+// 24 for 3: the leading ones cut, so none of them overflows, the last rounded.
+// Infinities and NaNs are in the first alone.
+template <int P>
+__device__ __forceinline__ void bf16_parts(float v, uint32_t (&p)[P]) {
+  const uint32_t bits = __float_as_uint(v);
+  const bool fine = abs_bits(v) < kInfBits;
+  p[0] = abs_bits(v) > kInfBits ? 0x7FC0u : bits >> 16;
+  float rest = fine ? v - __uint_as_float(bits & 0xFFFF0000u) : 0.0f;
+  if constexpr (P == 3) {
+    const uint32_t next = __float_as_uint(rest) & 0xFFFF0000u;
+    p[1] = next >> 16;
+    rest -= __uint_as_float(next);
+  }
+  p[P - 1] = bf16_pair(rest, 0.0f) & 0xFFFFu;
+}
 
-// What the adapters of 16 tokens (token m in lane m % 16 of each group) add to TI
-// tiles of 16 outputs from n0 on, whose sums `acc` holds as the matrix
-// instruction leaves them.  One adapter after the other, each for the tokens
-// that have it: requests' tokens stand together, so most often there is one.
-template <int YF, int TI, class Acc>
-__device__ __forceinline__ void add_adapters(const Adapters& ad, const MxLinArgs& a, int r, int m, int n0, Acc acc) {
-  constexpr int P = t_parts<YF>();
-  const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
-  const int mine = m < a.M ? ad.index[m] : -1;
-  const uint8_t* t = ad.t + r * ad.t_rank + (int64_t)min(m, a.M - 1) * ad.t_stride;
-  uint32_t left = (uint32_t)__ballot((uint32_t)mine < (uint32_t)ad.count) & 0xFFFFu;
-  while (left != 0) {
-    const int which = __builtin_amdgcn_readlane(mine, __builtin_ctz(left));
-    const bool take = mine == which;
-    left &= ~(uint32_t)__ballot(take);
-    const uint8_t* b = ad.b + r * ad.b_rank + which * ad.b_adapter;
-    f32x4 d[TI];
+// Sums that are ready, for TI x TJ tiles of 16 outputs by 16 tokens.
+template <int TI, int TJ, class Acc>
+__device__ __forceinline__ void add_delta(const Adapters& ad, const MxLinArgs& a, int r, int m0, int n0, Acc acc) {
+  const int c = threadIdx.x & 15, g = threadIdx.x >> 4 & 3;
 #pragma unroll
-    for (int i = 0; i < TI; ++i) d[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int j = 8 * g; j - 8 * g < ad.rank; j += 32) {    // 32 of the adapter's dimensions
-      const bool in = j < ad.rank;
-      const int at = min(j, (ad.rank - 1) & ~7);
-      u32x4 p[P];
+  for (int j = 0; j < TJ; ++j) {
+    const int m = m0 + 16 * j + c;
+    const bool has = m < a.M && (uint32_t)ad.index[min(m, a.M - 1)] < (uint32_t)ad.count;
+    const float* row = ad.delta + r * ad.delta_rank + (int64_t)min(m, a.M - 1) * ad.delta_stride;
 #pragma unroll
-      for (int q = 0; q < P; ++q) {
-        p[q] = *reinterpret_cast<const u32x4*>(t + (at * P + 8 * q) * 2);
-        if (!in) p[q] = u32x4{0u, 0u, 0u, 0u};
-      }
-#pragma unroll
-      for (int i = 0; i < TI; ++i) {
-        const int n = min(n0 + 16 * i + c, a.N - 1);
-        const u32x4 w = keep_inputs<AR_BF16>(*reinterpret_cast<const u32x4*>(b + n * ad.b_stride + at * 2), in ? j : ad.rank, ad.rank);
-#pragma unroll
-        for (int q = 0; q < P; ++q)
-          d[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w), __builtin_bit_cast(bf16x8, p[q]),
-                                                         d[i], 0, 0, 0);
-      }
+    for (int i = 0; i < TI; ++i) {
+      const int n = n0 + 16 * i + 4 * g;
+      if (has && n < a.N) acc(i, j) += *reinterpret_cast<const f32x4*>(row + n);
     }
-#pragma unroll
-    for (int i = 0; i < TI; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc(i)[e] += take ? d[i][e] : 0.0f;
   }
 }
+
+// 8 values of an adapter's row of b from dimension `at` on, zeros from `rank` on.
+__device__ __forceinline__ u32x4 load_b8(const uint8_t* row, int at, int rank) {
+  u32x4 v = u32x4{0u, 0u, 0u, 0u};
+  if (at < rank) v = ldg16(row + at * 2);
+  return v;
+}
+__device__ __forceinline__ u32x4 keep_b8(u32x4 v, int at, int rank) {
+  return at + 8 > rank ? keep_inputs<AR_BF16>(v, at, rank) : v;
+}
+
+// What adapters add to TI x TJ tiles of 16 outputs by 16 tokens where there are
+// few: every lane by itself, for its token (lane % 16 of each group) and the 4
+// outputs of its group, in binary32 products and sums.  No two tokens need the
+// same adapter for it, there is nothing to find out, and the loads do not wait for
+// each other.  ROOM: registers for the first 16 dimensions' operands beside
+// the layer's own, so that they are loaded before its products.
+template <int TI, int TJ, bool ROOM>
+struct AdapterLanes {
+  int mine[TJ];                      // -1: none
+  const uint8_t* t[TJ];
+  const uint8_t* b[TJ];              // of the first output, this token's adapter
+  int n, last;                       // this lane's first output, and the last there is
+  f32x4 tv[ROOM ? TJ : 1][4];
+  u32x4 w[ROOM ? TI * TJ : 1][4][2];
+
+  // m0: the first token, n0: the first output.
+  __device__ __forceinline__ void find(const Adapters& ad, const MxLinArgs& a, int r, int m0, int n0) {
+    const int c = threadIdx.x & 15, g = threadIdx.x >> 4 & 3;
+    n = n0 + 4 * g;
+    last = a.N - 1;
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) {
+      const int m = m0 + 16 * j + c;
+      mine[j] = m < a.M ? ad.index[m] : -1;
+      t[j] = ad.t + r * ad.t_rank + (int64_t)min(m, a.M - 1) * ad.t_stride;
+    }
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) {
+      if ((uint32_t)mine[j] >= (uint32_t)ad.count) mine[j] = -1;
+      b[j] = ad.b + r * ad.b_rank + mine[j] * ad.b_adapter;
+    }
+  }
+  // Dimensions q .. q + 15.
+  __device__ __forceinline__ void load_t(int j, int q, f32x4 (&v)[4]) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      v[k] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      if (mine[j] >= 0) v[k] = *reinterpret_cast<const f32x4*>(t[j] + (q + 4 * k) * 4);
+    }
+  }
+  __device__ __forceinline__ void load_b(const Adapters& ad, int i, int j, int q, u32x4 (&v)[4][2]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint8_t* row = b[j] + min(n + 16 * i + e, last) * ad.b_stride;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        v[e][k] = u32x4{0u, 0u, 0u, 0u};
+        if (mine[j] >= 0) v[e][k] = load_b8(row, q + 8 * k, ad.rank);
+      }
+    }
+  }
+  static __device__ __forceinline__ void add(const Adapters& ad, int q, const f32x4 (&x)[4], const u32x4 (&v)[4][2],
+                                             f32x4& sum) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float s = 0.0f;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const u32x4 y = keep_b8(v[e][k], q + 8 * k, ad.rank);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          s = __builtin_fmaf(x[2 * k + u / 2][u % 2 * 2], bf_lo(y[u]), s);
+          s = __builtin_fmaf(x[2 * k + u / 2][u % 2 * 2 + 1], bf_hi(y[u]), s);
+        }
+      }
+      sum[e] += s;
+    }
+  }
+  // Where the layer's first loads are under way.
+  __device__ __forceinline__ void start(const Adapters& ad, const MxLinArgs& a, int r, int m0, int n0) {
+    find(ad, a, r, m0, n0);
+    if constexpr (ROOM) {
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) {
+        load_t(j, 0, tv[j]);
+#pragma unroll
+        for (int i = 0; i < TI; ++i) load_b(ad, i, j, 0, w[i * TJ + j]);
+      }
+    }
+  }
+  template <class Acc>
+  __device__ __forceinline__ void finish(const Adapters& ad, Acc acc) {
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) {
+      if (!__any(mine[j] >= 0)) continue;
+      f32x4 sum[TI];
+#pragma unroll
+      for (int i = 0; i < TI; ++i) sum[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      if constexpr (ROOM) {
+#pragma unroll
+        for (int i = 0; i < TI; ++i) add(ad, 0, tv[j], w[i * TJ + j], sum[i]);
+      }
+      for (int q = ROOM ? 16 : 0; q < ad.rank; q += 16) {
+        f32x4 x[4];
+        u32x4 v[TI][4][2];
+        load_t(j, q, x);
+#pragma unroll
+        for (int i = 0; i < TI; ++i) load_b(ad, i, j, q, v[i]);
+#pragma unroll
+        for (int i = 0; i < TI; ++i) add(ad, q, x, v[i], sum[i]);
+      }
+      if (mine[j] >= 0) {
+#pragma unroll
+        for (int i = 0; i < TI; ++i) acc(i, j) += sum[i];
+      }
+    }
+  }
+};
 
 // Up to 16 tokens: bound by the stream of weights.  A wave holds 16 * NT outputs
 // and the tokens; WK waves split K step by step and join their sums, in order,
@@ -324,6 +434,11 @@ __global__ __launch_bounds__(kWave * WN * WK) void k_mx_linear_rows(MxLinArgs a,
   }
   const uint8_t* xrow = a.x + r * a.x_rank + min(m, a.M - 1) * a.x_stride;
   const uint8_t* xsrow = a.xs + r * a.xs_rank + min(m, a.M - 1) * a.xs_stride;
+  // this wave's output tiles: all, or one of those that the group shares
+  constexpr int own = WK == 1 ? NT : 1;
+  AdapterLanes<own, 1, true> tiles;
+  if constexpr (!is_same<AD, NoAdapters>) {
+  }
   f32x4 acc[NT];
 #pragma unroll
   for (int i = 0; i < NT; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -366,10 +481,16 @@ __global__ __launch_bounds__(kWave * WN * WK) void k_mx_linear_rows(MxLinArgs a,
 #pragma unroll
     for (int i = 0; i < NT; ++i) acc[i] = multiply<XF, 3>(f.w[i], f.x, shift, acc[i]);
   };
+  auto start = [&]() {                                     // beside the layer's first loads
+    if constexpr (!is_same<AD, NoAdapters>) {
+      if (!ad.delta && wk < NT) tiles.start(ad, a, r, mg * 16, n0 + (WK == 1 ? 0 : 16 * wk));
+    }
+  };
   if (wk < steps) {
     Step cur;
     int st = wk;
     load(st, cur);
+    start();
     for (; st + WK < steps; st += WK) {
       Step next;
       load(st + WK, next);
@@ -378,12 +499,15 @@ __global__ __launch_bounds__(kWave * WN * WK) void k_mx_linear_rows(MxLinArgs a,
     }
     keep(st, cur);
     compute(cur);
+  } else {
+    start();
   }
   if constexpr (WK > 1) {
 #pragma unroll
     for (int i = 0; i < NT; ++i) part[((wk * WN + wn) * NT + i) * kWave + lane] = acc[i];
     __syncthreads();
   }
+  f32x4 sums[NT];
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
     if (i % WK != wk) continue;                            // the waves of a group share the tiles
@@ -393,18 +517,30 @@ __global__ __launch_bounds__(kWave * WN * WK) void k_mx_linear_rows(MxLinArgs a,
 #pragma unroll
       for (int k = 1; k < WK; ++k) v += part[((k * WN + wn) * NT + i) * kWave + lane];
     }
-    const int n = n0 + i * 16 + 4 * g;
-    if constexpr (!is_same<AD, NoAdapters>) {
-      if constexpr (XF == AR_E4M3_ROW) {
-        if (a.K > 0) v *= *reinterpret_cast<const float*>(xsrow);
-      }
-      add_adapters<YF, 1>(ad, a, r, m, n0 + i * 16, [&](int) -> f32x4& { return v; });
-    }
-    if (m >= a.M || n >= a.N) continue;
-    if constexpr (XF == AR_E4M3_ROW && is_same<AD, NoAdapters>) {
+    if constexpr (XF == AR_E4M3_ROW) {
       if (a.K > 0) v *= *reinterpret_cast<const float*>(xsrow);
     }
-    store_out4<YF>(a.y, r * a.y_rank + m * a.y_stride + n, n, a.N, a.vec != 0, v);
+    sums[i] = v;
+  }
+  if constexpr (!is_same<AD, NoAdapters>) {
+    if (ad.delta) {
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+        if (i % WK == wk) add_delta<1, 1>(ad, a, r, mg * 16, n0 + 16 * i, [&](int, int) -> f32x4& { return sums[i]; });
+    } else if constexpr (WK == 1) {
+      tiles.finish(ad, [&](int i, int) -> f32x4& { return sums[i]; });
+    } else {
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+        if (i == wk) tiles.finish(ad, [&](int, int) -> f32x4& { return sums[i]; });
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    if (i % WK != wk) continue;
+    const int n = n0 + i * 16 + 4 * g;
+    if (m >= a.M || n >= a.N) continue;
+    store_out4<YF>(a.y, r * a.y_rank + m * a.y_stride + n, n, a.N, a.vec != 0, sums[i]);
   }
 }
 
@@ -497,6 +633,126 @@ struct Tile {
   static_assert(KG == 1 || tile_waves * WM * WN * 4 * KG <= lds, "room to join the sums");
   static_assert((NS - 2) * (nx + nw) < 64, "loads on their way that a wait can name");
 };
+
+// What adapters add to a workgroup's BM tokens by BN outputs: one adapter after
+// the other, for the tokens that have it, so that one's infinities stay with its
+// own tokens (those of a request stand together, so most often there are one or
+// two).  The layer's operands are done with, so t and the adapter's rows of b
+// go through shared memory, 32 dimensions at a time, the next adapter's rows on
+// their way in registers.  t's values go as 2 bf16 parts for bf16 outputs, as 3,
+// which is all of them, for binary32 ones.  4096 x 8192 x 8192, 8-bit tokens, 195
+// us without adapters: 8 requests with one of rank 16 each 224, of rank 64 254 (of
+// them 40 for t), 16 adapters of rank 16 in any order 326.
+template <class G, class Acc>
+__device__ __forceinline__ void add_adapters(const Adapters& ad, const MxLinArgs& a, int r, int m0, int n0, int wm,
+                                             int wn, uint8_t* smem, Acc acc) {
+  constexpr int P = G::YF == AR_F32 ? 3 : 2, TI = G::WN / 16, TJ = G::WM / 16, threads = G::threads;
+  constexpr int TS = 64 * P + 16, BS = 64 + 16;            // 16 rows' reads meet different banks
+  constexpr int pieces = G::BN * 4 / threads, sets = G::BM / kWave;
+  static_assert(G::KG == 1 && G::BM % kWave == 0 && G::BN * 4 % threads == 0, "");
+  static_assert(G::BM * (4 + TS) + 2 * G::BN * BS <= G::lds, "room for t and b");
+  const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, g = lane >> 4;
+  int* ids = reinterpret_cast<int*>(smem);
+  uint8_t *ts = smem + G::BM * 4, *bs = ts + G::BM * TS;
+  __syncthreads();
+  for (int i = tid; i < G::BM; i += threads) {
+    const int which = m0 + i < a.M ? ad.index[m0 + i] : -1;
+    ids[i] = (uint32_t)which < (uint32_t)ad.count ? which : -1;
+  }
+  __syncthreads();
+  int mine[sets];
+  uint64_t all[sets], left[sets], any = 0;
+#pragma unroll
+  for (int k = 0; k < sets; ++k) {
+    mine[k] = ids[64 * k + lane];
+    all[k] = __ballot(mine[k] >= 0);
+    any |= all[k];
+  }
+  auto next = [&]() {
+    int which = -1;
+#pragma unroll
+    for (int k = 0; k < sets; ++k)
+      if (which < 0 && left[k] != 0) which = __builtin_amdgcn_readlane(mine[k], __builtin_ctzll(left[k]));
+#pragma unroll
+    for (int k = 0; k < sets; ++k) left[k] &= ~__ballot(mine[k] == which);
+    return which;
+  };
+  if (any == 0) return;
+  for (int q = 0; q < ad.rank; q += 32) {
+    u32x4 w[pieces];
+    auto load_rows = [&](int which) {
+      const uint8_t* b = ad.b + r * ad.b_rank + which * ad.b_adapter;
+#pragma unroll
+      for (int i = 0; i < pieces; ++i) {
+        const int s = i * threads + tid;
+        w[i] = load_b8(b + min(n0 + s / 4, a.N - 1) * ad.b_stride, q + 8 * (s % 4), ad.rank);
+      }
+    };
+#pragma unroll
+    for (int k = 0; k < sets; ++k) left[k] = all[k];
+    int which = next();
+    load_rows(which);
+    for (int s = tid; s < G::BM * 4; s += threads) {
+      const int row = s / 4, at = q + 8 * (s % 4);
+      f32x4 v[2] = {f32x4{0.0f, 0.0f, 0.0f, 0.0f}, f32x4{0.0f, 0.0f, 0.0f, 0.0f}};
+      if (ids[row] >= 0 && at < ad.rank) {
+        const uint8_t* t = ad.t + r * ad.t_rank + (m0 + row) * ad.t_stride + at * 4;
+        v[0] = *reinterpret_cast<const f32x4*>(t);
+        v[1] = *reinterpret_cast<const f32x4*>(t + 16);
+      }
+      u32x4 p[P];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        uint32_t lo[P], hi[P];
+        bf16_parts<P>(v[e / 2][e % 2 * 2], lo);
+        bf16_parts<P>(v[e / 2][e % 2 * 2 + 1], hi);
+#pragma unroll
+        for (int k = 0; k < P; ++k) p[k][e] = pack2(lo[k], hi[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < P; ++k) *reinterpret_cast<u32x4*>(ts + row * TS + s % 4 * (16 * P) + 16 * k) = p[k];
+    }
+    for (int buf = 0; which >= 0; buf ^= 1) {
+      uint8_t* rows = bs + buf * G::BN * BS;
+#pragma unroll
+      for (int i = 0; i < pieces; ++i) {
+        const int s = i * threads + tid;
+        *reinterpret_cast<u32x4*>(rows + s / 4 * BS + s % 4 * 16) = keep_b8(w[i], q + 8 * (s % 4), ad.rank);
+      }
+      __syncthreads();                                     // the other buffer's readers are through, too
+      const int after = next();
+      if (after >= 0) load_rows(after);
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) {
+        const bool take = ids[wm + 16 * j + c] == which;
+        if (!__any(take)) continue;
+        const bool each = __all(take);
+        u32x4 t[P];
+#pragma unroll
+        for (int k = 0; k < P; ++k)
+          t[k] = *reinterpret_cast<const u32x4*>(ts + (wm + 16 * j + c) * TS + g * (16 * P) + 16 * k);
+#pragma unroll
+        for (int i = 0; i < TI; ++i) {
+          const bf16x8 x =
+              __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(rows + (wn + 16 * i + c) * BS + g * 16));
+          f32x4 v = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int k = 0; k < P; ++k)
+            v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, __builtin_bit_cast(bf16x8, t[k]), v, 0, 0, 0);
+          if (each) {
+            acc(i, j) += v;
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc(i, j)[e] += take ? v[e] : 0.0f;
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);                 // one tile's operands at a time: the sums fill the registers
+      }
+      which = after;
+    }
+    __syncthreads();                                       // t may be written over
+  }
+}
 
 template <class G, class AD>
 __global__ __launch_bounds__(G::threads) void k_mx_linear_tiles(MxLinArgs a, AD ad) {
@@ -618,6 +874,9 @@ __global__ __launch_bounds__(G::threads) void k_mx_linear_tiles(MxLinArgs a, AD 
 #pragma unroll
     for (int j = 0; j < TJ; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
+  constexpr bool few = TI * TJ <= 4;
+  AdapterLanes<few ? TI : 1, few ? TJ : 1, (TI * TJ <= 2 && G::threads <= 256)> tiles;
+
   // Operands of one round (round h of a step) in registers.  8- and 4-bit
   // tokens: one matrix instruction a tile; bf16: two, group g with elements
   // 16g .. 16g + 15 of the 64.
@@ -713,6 +972,10 @@ __global__ __launch_bounds__(G::threads) void k_mx_linear_tiles(MxLinArgs a, AD 
     if (k < steps && k % T::steps_scales == 0) load_scales(k);
     if (k < steps) load_next(k);
   }
+  // (newer than those, so that a wait for those is at most longer for these)
+  if constexpr (!is_same<AD, NoAdapters> && few) {
+    if (!ad.delta) tiles.start(ad, a, r, m0 + wj * WM, n0 + wi * WN);
+  }
   constexpr int behind = (NS - 2) * (G::nx + G::nw);
   constexpr int wait_behind = 0x0F70 | (behind & 15) | (behind >> 4) << 14;      // vmcnt alone
   int buf = 0;
@@ -804,16 +1067,21 @@ __global__ __launch_bounds__(G::threads) void k_mx_linear_tiles(MxLinArgs a, AD 
         for (int j = 0; j < TJ; ++j) acc[i][j] += part[(q - 1) * group + (i * TJ + j) * kWave];
   }
   if constexpr (!is_same<AD, NoAdapters>) {
+    if constexpr (XF == AR_E4M3_ROW) {
 #pragma unroll
-    for (int j = 0; j < TJ; ++j) {
-      const int m = m0 + wj * WM + j * 16 + c;
-      if constexpr (XF == AR_E4M3_ROW) {
-        const float scale =
-            a.K > 0 ? *reinterpret_cast<const float*>(a.xs + r * a.xs_rank + min(m, a.M - 1) * a.xs_stride) : 1.0f;
+      for (int j = 0; j < TJ; ++j) {
+        const int m = min(m0 + wj * WM + j * 16 + c, a.M - 1);
+        const float scale = a.K > 0 ? *reinterpret_cast<const float*>(a.xs + r * a.xs_rank + m * a.xs_stride) : 1.0f;
 #pragma unroll
         for (int i = 0; i < TI; ++i) acc[i][j] *= scale;
       }
-      add_adapters<YF, TI>(ad, a, r, m, n0 + wi * WN, [&](int i) -> f32x4& { return acc[i][j]; });
+    }
+    const auto sums = [&](int i, int j) -> f32x4& { return acc[i][j]; };
+    if constexpr (few) {
+      if (ad.delta) add_delta<TI, TJ>(ad, a, r, m0 + wj * WM, n0 + wi * WN, sums);
+      else tiles.finish(ad, sums);
+    } else {
+      add_adapters<G>(ad, a, r, m0, n0, wj * WM, wi * WN, smem, sums);
     }
   }
 #pragma unroll
@@ -933,11 +1201,19 @@ static hipError_t launch_tiles(const MxLinArgs& a0, const AD& ad, int nranks, hi
 //   7.9, 4 x 32 x 8192 x 2048 9.9 and 10.5.
 // The tile kernels' offsets inside a tile are 31 bits: rows further apart take
 // the other kernel at any number of tokens.
+inline int64_t linear_tiles(const MxLinArgs& a, int nranks, int bm, int bn) {
+  return (int64_t)((a.N + bn - 1) / bn) * ((a.M + bm - 1) / bm) * nranks;
+}
+// Tiles of 128 x 128 or 256 x 256.
+inline bool large_tiles(const MxLinArgs& a, int nranks) {
+  return a.x_stride < (1 << 23) && a.w_stride < (1 << 23) &&
+         ((a.M > 128 && linear_tiles(a, nranks, 256, 256) >= 256) ||
+          (a.M > 64 && linear_tiles(a, nranks, 128, 128) >= 256));
+}
+
 template <int XF, int YF, class AD>
 static hipError_t launch_linear(const MxLinArgs& a, const AD& ad, int nranks, hipStream_t s) {
-  auto tiles = [&](int bm, int bn) -> int64_t {
-    return (int64_t)((a.N + bn - 1) / bn) * ((a.M + bm - 1) / bm) * nranks;
-  };
+  auto tiles = [&](int bm, int bn) { return linear_tiles(a, nranks, bm, bn); };
   const bool many = a.M > 16 || (XF != AR_BF16 && a.M > 8 && tiles(32, 64) > 256);
   if (many && a.x_stride < (1 << 23) && a.w_stride < (1 << 23)) {
     constexpr int K1 = XF == AR_BF16 ? 64 : 128;
@@ -995,6 +1271,7 @@ static hipError_t launch_pieces(const MxLinArgs& a, const AD& ad, int xf, int yf
     if constexpr (!is_same<AD, NoAdapters>) {
       b.index += m;
       b.t += r * ad.t_rank + m * ad.t_stride;
+      if (b.delta) b.delta += r * ad.delta_rank + m * ad.delta_stride + n;
       b.b += r * ad.b_rank + n * ad.b_stride;
     }
     return b;

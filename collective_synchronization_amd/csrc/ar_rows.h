@@ -21,6 +21,14 @@ __host__ __device__ constexpr bool is_mx_format(int f) { return f == AR_E4M3_MX 
 
 __device__ __forceinline__ u32x4 ldg16(const uint8_t* p) { return *reinterpret_cast<const u32x4*>(p); }
 
+// An element that is the same for all lanes, through the scalar cache: what no
+// kernel in flight writes.
+template <class T>
+__device__ __forceinline__ T ld_const(const T* p, int64_t i) {
+  typedef const __attribute__((address_space(4))) T const_t;
+  return ((const_t*)p)[__builtin_amdgcn_readfirstlane((int)i)];
+}
+
 // ------------------------------------------------------------- chunks ---
 // A chunk is 8 elements of one row, 16-byte aligned in a 16-bit row.  Rows
 // are written below `count` only; a chunk that ends past it goes element by

@@ -537,6 +537,7 @@ typedef struct {
  * with infinities in b may be NaN.  The order of every sum is fixed by the
  * sizes, so equal calls give equal bits, and a token's bits do not depend on the
  * other tokens' adapters.  adapters, rank or inputs 0: ar_mx4_linear alone.
+ * AR_ESIZE: b_stride of 2^23 and more, and as for ar_mx4_linear.
  */
 int ar_mx4_linear_adapters(const ar_linear_params* p, const ar_adapter_params* q, void* work,
                            int64_t work_bytes, void* stream);
