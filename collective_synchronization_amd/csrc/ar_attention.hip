@@ -158,6 +158,14 @@ struct Piece {
 
 // ---------------------------------------------------------------- forms ---
 
+// 16 bytes a lane straight into shared memory, at `lds` (the wave's own address)
+// + 16 * lane.
+__device__ __forceinline__ void load_to_lds(rsrc_t r, uint8_t* lds, uint32_t off) {
+  typedef __attribute__((address_space(3))) void lds_void;
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)lds, 16, off, 0, 0, 0);
+}
+constexpr uint32_t kNowhere = 0x80000000u;   // past every range: reads as zeros
+
 template <int QF, bool C8, int DT>
 struct Attn {
   static constexpr int VF = C8 ? AR_BF16 : QF;             // type of weights and values
@@ -169,56 +177,74 @@ struct Attn {
   static constexpr int CH = pow2_up(DT / CB);              // lanes to a row
   static constexpr int wave_keys = kWave / CH;             // rows that a wave loads at once: at most 16, on one page
   static constexpr int passes = KT * CH / kAttnThreads;
-  // Rows in shared memory: 16 rows' 16-byte reads, and 8 rows' 32-byte ones,
-  // fall into different banks.
-  static constexpr int KS = DT * 2 + 16, VS = DT * 2 + 32;
-  static constexpr int tile = KT * (KS + VS) + (C8 ? KT * 8 : 0);
-  static constexpr int few_wave = 32 * VS + (C8 ? 32 * 8 : 0);
+  // Rows in shared memory: C16 pieces of 8 elements.  16 rows' reads of one piece
+  // (keys), and 4 rows' of four (values), meet different banks, since pieces are
+  // permuted by the row; loads straight into shared memory have the permutation in
+  // their addresses.
+  static constexpr int C16 = pow2_up(DT / 8), RS = C16 * 16;
+  static constexpr int tile = 2 * KT * RS + (C8 ? KT * 8 : 0);
+  static constexpr int few_step = 32 * RS + (C8 ? 32 * 8 : 0);
+  static constexpr int few_wave = (C8 ? 1 : 2) * few_step; // (8-bit values wait in registers)
   static constexpr int few_join = kAttnWaves * (16 * DT * 4 + 16 * 8);
   static constexpr int few = kAttnWaves * few_wave > few_join ? kAttnWaves * few_wave : few_join;
   static constexpr int lds = 2 * tile > few ? 2 * tile : few;
   static_assert(wave_keys <= 16 && KT * CH % kAttnThreads == 0, "");
 
-  // 16 bytes of a token's row for every lane of a wave: lane / CH-th token
-  // after `key`, which is a multiple of 16 and less; zeros for what is not there.
-  static __device__ __forceinline__ u32x4 load(const AttnArgs& a, const Piece& p, const uint8_t* base, int key, int lane) {
-    u32x4 v = u32x4{0u, 0u, 0u, 0u};
-    if (key >= p.k1) return v;
-    const int page = ld_const(p.table, key >> a.kv.page_shift);
-    if ((uint32_t)page >= (uint32_t)a.kv.pages) return v;
-    const int t = lane / CH, c = lane % CH;
-    const uint8_t* at = base + page * a.kv.page_stride + ((key & (a.kv.page - 1)) + t) * a.kv.token_stride +
-                        p.kh * a.kv.head_stride + c * 16;
-    if (key + t < p.k1 && c * CB < a.kv.dim) v = ldg16(at);
-    return v;
+  static __device__ __forceinline__ int swap_k(int row) { return C16 == 8 ? row >> 1 & 7 : row & 15; }
+  static __device__ __forceinline__ int swap_v(int row) { return C16 == 8 ? (row >> 1 & 1) << 2 : (row & 3) << 2; }
+
+  // Pages of the N 16-key runs from `key` on; -1 for those that are none, or past the end.
+  template <int N>
+  struct Pages { int at[N]; };
+  template <int N>
+  static __device__ __forceinline__ Pages<N> find_pages(const AttnArgs& a, const Piece& p, int key) {
+    Pages<N> r;
+#pragma unroll
+    for (int i = 0; i < N; ++i) r.at[i] = ld_const(p.table, min(key + 16 * i, p.k1 - 1) >> a.kv.page_shift);
+    return r;
   }
-  // The scale of one token's row, for each lane's own key.
-  static __device__ __forceinline__ float load_scale(const AttnArgs& a, const Piece& p, const float* base, int key) {
-    if (key >= p.k1) return 0.0f;
-    const int page = p.table[key >> a.kv.page_shift];
-    if ((uint32_t)page >= (uint32_t)a.kv.pages) return 0.0f;
+  template <int N>
+  static __device__ __forceinline__ void check_pages(const AttnArgs& a, const Piece& p, int key, Pages<N>& r) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (key + 16 * i >= p.k1 || (uint32_t)r.at[i] >= (uint32_t)a.kv.pages) r.at[i] = -1;
+  }
+  // Of checked ones, those that are none (past the end they are, too).
+  template <int N>
+  static __device__ __forceinline__ uint32_t missing(const Pages<N>& r) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) m |= r.at[i] < 0 ? 1u << i : 0u;
+    return m;
+  }
+  // Rows of token `key` and the ones after it up to `n`, or to the end.
+  static __device__ __forceinline__ rsrc_t rows(const AttnArgs& a, const Piece& p, const uint8_t* base, int page, int key,
+                                                int n) {
+    const int count = min(n, p.k1 - key);
+    const int64_t at = page * a.kv.page_stride + (key & (a.kv.page - 1)) * a.kv.token_stride + p.kh * a.kv.head_stride;
+    const uint32_t range = (uint32_t)(count - 1) * (uint32_t)a.kv.token_stride + (uint32_t)(a.kv.dim * (C8 ? 1 : 2));
+    const bool none = page < 0 || count <= 0;
+    return make_rsrc(none ? base : base + at, none ? 0u : range);
+  }
+  // Scale of each lane's own key, `run` of the pages' runs.
+  template <int N>
+  static __device__ __forceinline__ float load_scale(const AttnArgs& a, const Piece& p, const float* base,
+                                                     const Pages<N>& r, int key, int run) {
+    int page = r.at[0];
+#pragma unroll
+    for (int i = 1; i < N; ++i)
+      if (run == i) page = r.at[i];
+    if (page < 0 || key >= p.k1) return 0.0f;
     return base[page * a.kv.scale_page_stride + (key & (a.kv.page - 1)) * a.kv.scale_token_stride +
                 p.kh * a.kv.scale_head_stride];
   }
-  // Which 16-key runs of `n` keys from `key` on are on no page.
-  static __device__ __forceinline__ uint32_t missing(const AttnArgs& a, const Piece& p, int key, int n) {
-    uint32_t m = 0;
-    for (int i = 0; i < n / 16; ++i) {
-      const int k = key + 16 * i;
-      if (k < p.k1 && (uint32_t)ld_const(p.table, k >> a.kv.page_shift) >= (uint32_t)a.kv.pages) m |= 1u << i;
-    }
-    return m;
-  }
-  // As 16-bit values in shared memory.
+  // 16 bytes of the cache as 16-bit values of row `row` in shared memory.
   template <int F>
-  static __device__ __forceinline__ void store(uint8_t* row, int c, u32x4 v) {
-    if (c * CB >= DT) return;
-    if constexpr (C8) {
-      *reinterpret_cast<u32x4*>(row + c * 32) = wide8<F>(v.x, v.y);
-      *reinterpret_cast<u32x4*>(row + c * 32 + 16) = wide8<F>(v.z, v.w);
-    } else {
-      *reinterpret_cast<u32x4*>(row + c * 16) = v;
-    }
+  static __device__ __forceinline__ void store8(uint8_t* rows, int row, int swap, int c, u32x4 v) {
+    static_assert(C8, "");
+    if (c * 16 >= DT) return;
+    *reinterpret_cast<u32x4*>(rows + row * RS + ((2 * c) ^ swap) * 16) = wide8<F>(v.x, v.y);
+    *reinterpret_cast<u32x4*>(rows + row * RS + ((2 * c + 1) ^ swap) * 16) = wide8<F>(v.z, v.w);
   }
 
   static __device__ __forceinline__ const uint8_t* query(const AttnArgs& a, const Piece& p, int row) {
@@ -236,13 +262,16 @@ struct Attn {
 
   // Many rows: bound by the matrix cores and the exponentials beside them.  Each
   // wave has 32 rows, and tiles of KT keys pass through shared memory, the next
-  // one on its way in registers while one is multiplied.
+  // one on its way while one is multiplied (8-bit ones in registers, since they
+  // are converted), and the pages of the one after that.
   static __device__ void many_rows(const AttnArgs& a, const Piece& p, uint8_t* smem) {
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int col = lane & 31, half = lane >> 5;
     const int first = p.row0 + wave * 32, row = first + col;
     const bool idle = first >= p.rows;
+    constexpr int runs = KT / 16, pass_keys = kAttnThreads / CH;
+    auto pages = find_pages<runs>(a, p, p.k0);
     u32x4 q[DT / 16];
     {
       const uint8_t* at = query(a, p, row);
@@ -258,57 +287,98 @@ struct Attn {
       for (int r = 0; r < 16; ++r) o[i][r] = 0.0f;
     float top = -__builtin_inff(), ref = 0.0f, l = 0.0f;
 
-    u32x4 kr[passes], vr[passes];
+    // this lane's piece of a row: as loaded, and straight into its place
+    uint32_t k_off[passes], v_off[passes];
+    const int piece = lane % CH, key_in = lane / CH;
+#pragma unroll
+    for (int i = 0; i < passes; ++i) {
+      const int k = i * pass_keys + wave * wave_keys + key_in;
+      const int kc = C8 ? piece : piece ^ swap_k(k), vc = C8 ? piece : piece ^ swap_v(k);
+      k_off[i] = kc * CB < a.kv.dim ? (uint32_t)key_in * (uint32_t)a.kv.token_stride + kc * 16 : kNowhere;
+      v_off[i] = vc * CB < a.kv.dim ? (uint32_t)key_in * (uint32_t)a.kv.token_stride + vc * 16 : kNowhere;
+    }
+    u32x4 kr[C8 ? passes : 1], vr[C8 ? passes : 1];
     float scale = 0.0f;
-    auto load_tile = [&](int key) {
+    auto load_tile = [&](int key, int buf) {
+      uint8_t* at = smem + buf * tile;
 #pragma unroll
       for (int i = 0; i < passes; ++i) {
-        const int k = key + i * (kAttnThreads / CH) + wave * wave_keys;
-        kr[i] = load(a, p, a.kv.k, k, lane);
-        vr[i] = load(a, p, a.kv.v, k, lane);
+        const int k = i * pass_keys + wave * wave_keys;    // of the tile; on one page with the wave's others
+        int page = pages.at[0];
+#pragma unroll
+        for (int u = 1; u < runs; ++u)
+          if (k >> 4 == u) page = pages.at[u];
+        const rsrc_t kp = rows(a, p, a.kv.k, page, key + k, wave_keys), vp = rows(a, p, a.kv.v, page, key + k, wave_keys);
+        if constexpr (C8) {
+          kr[i] = __builtin_amdgcn_raw_buffer_load_b128(kp, k_off[i], 0, 0);
+          vr[i] = __builtin_amdgcn_raw_buffer_load_b128(vp, v_off[i], 0, 0);
+        } else {
+          load_to_lds(kp, at + k * RS, k_off[i]);
+          load_to_lds(vp, at + KT * RS + k * RS, v_off[i]);
+        }
       }
       if constexpr (C8) {
-        if (tid < 2 * KT) scale = load_scale(a, p, tid < KT ? a.kv.k_scales : a.kv.v_scales, key + tid % KT);
+        if (tid < 2 * KT)
+          scale = load_scale<runs>(a, p, tid < KT ? a.kv.k_scales : a.kv.v_scales, pages, key + tid % KT, tid % KT / 16);
       }
     };
     auto store_tile = [&](int buf) {
       uint8_t* at = smem + buf * tile;
-#pragma unroll
-      for (int i = 0; i < passes; ++i) {
-        const int k = i * (kAttnThreads / CH) + tid / CH, c = tid % CH;
-        store<QF>(at + k * KS, c, kr[i]);
-        store<VF>(at + KT * KS + k * VS, c, vr[i]);
-      }
       if constexpr (C8) {
-        if (tid < 2 * KT) reinterpret_cast<float*>(at + KT * (KS + VS))[tid] = scale;
+#pragma unroll
+        for (int i = 0; i < passes; ++i) {
+          const int k = i * pass_keys + wave * wave_keys + key_in;
+          store8<QF>(at, k, swap_k(k), piece, kr[i]);
+          store8<VF>(at + KT * RS, k, swap_v(k), piece, vr[i]);
+        }
+        if (tid < 2 * KT) reinterpret_cast<float*>(at + 2 * KT * RS)[tid] = scale;
+      }
+    };
+    // every wave's pieces of the tile are there
+    auto arrived = [&]() {
+      if constexpr (C8) {
+        __syncthreads();
+      } else {
+        compiler_barrier();
+        __builtin_amdgcn_s_waitcnt(0x0070);                // vmcnt and lgkmcnt
+        __builtin_amdgcn_s_barrier();
+        compiler_barrier();
       }
     };
 
-    load_tile(p.k0);
-    uint32_t gone = missing(a, p, p.k0, KT);
+    check_pages(a, p, p.k0, pages);
+    load_tile(p.k0, 0);
+    uint32_t gone = missing(pages);
+    pages = find_pages<runs>(a, p, p.k0 + KT);
     store_tile(0);
-    __syncthreads();
+    arrived();
+    // group of 16 lanes: columns 16 * (group % 2) on, keys 4 * half on and 8 after them
+    const int vk = 4 * half + (lane & 15) / 4, vc = 2 * (lane >> 4 & 1) + (lane & 3) / 2;
+    const int k_base = col * RS, k_swap = half ^ swap_k(col);
+    const int v_base = KT * RS + vk * RS + (lane & 1) * 8, v_swap = vc ^ swap_v(vk);
     int buf = 0;
     for (int key = p.k0; key < p.k1; key += KT, buf ^= 1) {
       const bool more = key + KT < p.k1;
       uint32_t next_gone = 0;
       if (more) {
-        load_tile(key + KT);
-        next_gone = missing(a, p, key + KT, KT);
+        check_pages(a, p, key + KT, pages);
+        load_tile(key + KT, buf ^ 1);
+        next_gone = missing(pages);
+        pages = find_pages<runs>(a, p, key + 2 * KT);
       }
       if (!idle) {
         const uint8_t* ks = smem + buf * tile;
-        const uint8_t* vs = ks + KT * KS;
-        const float* sc = reinterpret_cast<const float*>(ks + KT * (KS + VS));
+        const float* sc = reinterpret_cast<const float*>(ks + 2 * KT * RS);
         f32x16 s[KT / 32];
 #pragma unroll
-        for (int t = 0; t < KT / 32; ++t) {
+        for (int t = 0; t < KT / 32; ++t)
 #pragma unroll
           for (int r = 0; r < 16; ++r) s[t][r] = 0.0f;
 #pragma unroll
-          for (int i = 0; i < DT / 16; ++i)
-            s[t] = mma32<QF>(*reinterpret_cast<const u32x4*>(ks + (32 * t + col) * KS + 32 * i + 16 * half), q[i], s[t]);
-        }
+        for (int i = 0; i < DT / 16; ++i)
+#pragma unroll
+          for (int t = 0; t < KT / 32; ++t)
+            s[t] = mma32<QF>(*reinterpret_cast<const u32x4*>(ks + k_base + 32 * t * RS + ((2 * i) ^ k_swap) * 16), q[i], s[t]);
         if constexpr (C8) {
 #pragma unroll
           for (int t = 0; t < KT / 32; ++t)
@@ -372,14 +442,12 @@ struct Attn {
               if constexpr (two) w2[2 * t + u][j] = rest16<VF>(a0, a1, w[2 * t + u][j]);
             }
         }
-        // group of 16 lanes: columns 16 * (group % 2) on, keys 4 * half on and 8 after them
-        const uint8_t* at = vs + (4 * half + (lane & 15) / 4) * VS + 32 * (lane >> 4 & 1) + (lane & 3) * 8;
 #pragma unroll
         for (int t = 0; t < KT / 16; ++t)
 #pragma unroll
           for (int i = 0; i < DT / 32; ++i) {
-            const u32x2 lo = read_transposed(at + 16 * t * VS + 64 * i);
-            const u32x2 hi = read_transposed(at + (16 * t + 8) * VS + 64 * i);
+            const uint8_t* at = ks + v_base + ((4 * i) ^ v_swap) * 16 + 16 * t * RS;
+            const u32x2 lo = read_transposed(at), hi = read_transposed(at + 8 * RS);
             o[i] = mma32<VF>(u32x4{lo.x, lo.y, hi.x, hi.y}, w[t], o[i]);
             if constexpr (two) o[i] = mma32<VF>(u32x4{lo.x, lo.y, hi.x, hi.y}, w2[t], o[i]);
           }
@@ -388,7 +456,7 @@ struct Attn {
         store_tile(buf ^ 1);
         gone = next_gone;
       }
-      __syncthreads();
+      arrived();
     }
     l = other_half_sum(l);
     if (row < p.rows) {
@@ -409,15 +477,20 @@ struct Attn {
   // Up to 16 rows: bound by the stream of the cache.  The waves take 32 keys in
   // turn, each on its own: keys straight into registers as the operand that they
   // are, values through the wave's own part of shared memory, to be transposed.
-  // The next 32 are on their way meanwhile.
+  // The next 32 are on their way meanwhile, and the pages of those after them.
   static __device__ void few_rows(const AttnArgs& a, const Piece& p, uint8_t* smem) {
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int col = lane & 15, g = lane >> 4;
+    constexpr int stride = 32 * kAttnWaves;
     constexpr int steps = DT / 32;                         // of 32 elements of a row
     constexpr int vloads = 32 / wave_keys;
     // which elements group g has in step i: 8 of each 32, of 8-bit rows 16 of each 64
-    auto elem = [&](int i) { return C8 && DT % 64 == 0 ? 64 * (i / 2) + 16 * g + 8 * (i & 1) : 32 * i + 8 * g; };
+    constexpr bool wide = C8 && DT % 64 == 0;
+    constexpr int kloads = wide ? steps / 2 : steps;
+    auto elem = [&](int i) { return wide ? 64 * (i / 2) + 16 * g + 8 * (i & 1) : 32 * i + 8 * g; };
+    int key = p.k0 + 32 * wave;
+    auto pages = find_pages<2>(a, p, key);
     u32x4 q[steps];
     {
       const uint8_t* at = query(a, p, col);
@@ -430,72 +503,105 @@ struct Attn {
 #pragma unroll
     for (int i = 0; i < DT / 16; ++i) o[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     float top = -__builtin_inff(), ref = 0.0f, l = 0.0f;
-    uint8_t* vs = smem + wave * few_wave;
-    float* sc = reinterpret_cast<float*>(vs + 32 * VS);
+    uint8_t* mine = smem + wave * few_wave;
 
+    const int piece = lane % CH, key_in = lane / CH;
+    uint32_t k_off[kloads], v_off[vloads];
+#pragma unroll
+    for (int i = 0; i < kloads; ++i) {
+      const int d = elem(wide ? 2 * i : i);
+      k_off[i] = d < a.kv.dim ? (uint32_t)col * (uint32_t)a.kv.token_stride + d * (C8 ? 1 : 2) : kNowhere;
+    }
+#pragma unroll
+    for (int i = 0; i < vloads; ++i) {
+      const int c = C8 ? piece : piece ^ swap_v(i * wave_keys + key_in);
+      v_off[i] = c * CB < a.kv.dim ? (uint32_t)key_in * (uint32_t)a.kv.token_stride + c * 16 : kNowhere;
+    }
     struct Keys {
-      u32x4 k[2][steps];
-      u32x4 v[vloads];
+      u32x4 k[2][kloads];
+      u32x4 v[C8 ? vloads : 1];
       float scale;
       uint32_t gone;
     };
-    auto load_keys = [&](int key, Keys& f) {
+    constexpr int loads = 2 * kloads + vloads;             // of a step, without scales
+    auto load_keys = [&](int at, int buf, Keys& f) {       // values first: keys that are there say that they are, too
+#pragma unroll
+      for (int i = 0; i < vloads; ++i) {
+        const rsrc_t r = rows(a, p, a.kv.v, pages.at[i * wave_keys / 16], at + i * wave_keys, wave_keys);
+        if constexpr (C8) f.v[i] = __builtin_amdgcn_raw_buffer_load_b128(r, v_off[i], 0, 0);
+        else load_to_lds(r, mine + buf * few_step + i * wave_keys * RS, v_off[i]);
+      }
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        const int k = key + 16 * t;
-        const int page = k < p.k1 ? ld_const(p.table, k >> a.kv.page_shift) : -1;
-        const bool there = (uint32_t)page < (uint32_t)a.kv.pages && k + col < p.k1;
-        const uint8_t* at = a.kv.k + page * a.kv.page_stride + ((k & (a.kv.page - 1)) + col) * a.kv.token_stride +
-                            p.kh * a.kv.head_stride;
+        const rsrc_t r = rows(a, p, a.kv.k, pages.at[t], at + 16 * t, 16);
 #pragma unroll
-        for (int i = 0; i < steps; ++i) {
-          f.k[t][i] = u32x4{0u, 0u, 0u, 0u};
-          if constexpr (C8 && DT % 64 == 0) {
-            if (i % 2 == 0 && there && elem(i) < a.kv.dim) f.k[t][i] = ldg16(at + elem(i));
-          } else if constexpr (C8) {
-            if (there && elem(i) < a.kv.dim) {
-              const u32x2 d = *reinterpret_cast<const u32x2*>(at + elem(i));
-              f.k[t][i].x = d.x;
-              f.k[t][i].y = d.y;
-            }
+        for (int i = 0; i < kloads; ++i) {
+          if constexpr (C8 && !wide) {
+            const u32x2 d = __builtin_amdgcn_raw_buffer_load_b64(r, k_off[i], 0, 0);
+            f.k[t][i] = u32x4{d.x, d.y, 0u, 0u};
           } else {
-            if (there && elem(i) < a.kv.dim) f.k[t][i] = ldg16(at + elem(i) * 2);
+            f.k[t][i] = __builtin_amdgcn_raw_buffer_load_b128(r, k_off[i], 0, 0);
           }
         }
       }
-#pragma unroll
-      for (int i = 0; i < vloads; ++i) f.v[i] = load(a, p, a.kv.v, key + i * wave_keys, lane);
-      if constexpr (C8) f.scale = load_scale(a, p, lane < 32 ? a.kv.k_scales : a.kv.v_scales, key + (lane & 31));
-      f.gone = missing(a, p, key, 32);
+      if constexpr (C8)
+        f.scale = load_scale<2>(a, p, lane < 32 ? a.kv.k_scales : a.kv.v_scales, pages, at + (lane & 31), lane >> 4 & 1);
+      f.gone = missing(pages);
     };
 
     Keys cur;
-    int key = p.k0 + 32 * wave;
-    if (key < p.k1) load_keys(key, cur);
-    for (; key < p.k1; key += 32 * kAttnWaves) {
+    if (key < p.k1) {
+      check_pages(a, p, key, pages);
+      load_keys(key, 0, cur);
+      pages = find_pages<2>(a, p, key + stride);
+    }
+    for (int buf = 0; key < p.k1; key += stride, buf ^= C8 ? 0 : 1) {
       const uint32_t gone = cur.gone;
-#pragma unroll
-      for (int i = 0; i < vloads; ++i) store<VF>(vs + (i * wave_keys + lane / CH) * VS, lane % CH, cur.v[i]);
-      if constexpr (C8) sc[lane] = cur.scale;
+      uint8_t* vs = mine + buf * few_step;
+      float* sc = reinterpret_cast<float*>(vs + 32 * RS);
       u32x4 k[2][steps];
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int i = 0; i < steps; ++i) {
-          if constexpr (C8 && DT % 64 == 0)
-            k[t][i] = i % 2 == 0 ? wide8<QF>(cur.k[t][i].x, cur.k[t][i].y) : wide8<QF>(cur.k[t][i - 1].z, cur.k[t][i - 1].w);
-          else if constexpr (C8) k[t][i] = wide8<QF>(cur.k[t][i].x, cur.k[t][i].y);
-          else k[t][i] = cur.k[t][i];
+          if constexpr (wide) {
+            const u32x4 d = cur.k[t][i / 2];
+            k[t][i] = i % 2 == 0 ? wide8<QF>(d.x, d.y) : wide8<QF>(d.z, d.w);
+          } else if constexpr (C8) {
+            k[t][i] = wide8<QF>(cur.k[t][i].x, cur.k[t][i].y);
+          } else {
+            k[t][i] = cur.k[t][i];
+          }
         }
-      if (key + 32 * kAttnWaves < p.k1) load_keys(key + 32 * kAttnWaves, cur);
+      if constexpr (C8) {
+#pragma unroll
+        for (int i = 0; i < vloads; ++i) {
+          const int r = i * wave_keys + key_in;
+          store8<VF>(vs, r, swap_v(r), piece, cur.v[i]);
+        }
+        sc[lane] = cur.scale;
+      }
+      const bool more = key + stride < p.k1;
+      if (more) {
+        check_pages(a, p, key + stride, pages);
+        load_keys(key + stride, buf ^ 1, cur);
+        pages = find_pages<2>(a, p, key + 2 * stride);
+      }
       f32x4 s[2];
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        s[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int t = 0; t < 2; ++t) s[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int i = 0; i < steps; ++i) s[t] = mma16<QF>(k[t][i], q[i], s[t]);
+      for (int i = 0; i < steps; ++i)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) s[t] = mma16<QF>(k[t][i], q[i], s[t]);
+      compiler_barrier();
+      if constexpr (!C8) {                                 // this step's values
+        constexpr int wait_next = 0x0F70 | (loads & 15) | (loads >> 4) << 14;
+        static_assert(loads < 64, "loads on their way that a wait can name");
+        if (more) __builtin_amdgcn_s_waitcnt(wait_next);
+        else __builtin_amdgcn_s_waitcnt(0x0F70);
+        compiler_barrier();
       }
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       if constexpr (C8) {
 #pragma unroll
         for (int t = 0; t < 2; ++t) s[t] *= *reinterpret_cast<const f32x4*>(sc + 16 * t + 4 * g);
@@ -536,14 +642,16 @@ struct Attn {
       if constexpr (two)
         w2 = u32x4{rest16<VF>(e[0][0], e[0][1], w.x), rest16<VF>(e[0][2], e[0][3], w.y),
                    rest16<VF>(e[1][0], e[1][1], w.z), rest16<VF>(e[1][2], e[1][3], w.w)};
-      const uint8_t* at = vs + (4 * g + col / 4) * VS + (col & 3) * 8;
+      // rows 4g on and 16 after them, columns 4 * (lane % 4) on of each 16
+      const int vk = 4 * g + col / 4, swap = ((lane & 3) / 2) ^ swap_v(vk);
+      const uint8_t* at = vs + vk * RS + (lane & 1) * 8;
 #pragma unroll
       for (int i = 0; i < DT / 16; ++i) {
-        const u32x2 lo = read_transposed(at + 32 * i), hi = read_transposed(at + 16 * VS + 32 * i);
+        const u32x2 lo = read_transposed(at + ((2 * i) ^ swap) * 16), hi = read_transposed(at + 16 * RS + ((2 * i) ^ swap) * 16);
         o[i] = mma16<VF>(u32x4{lo.x, lo.y, hi.x, hi.y}, w, o[i]);
         if constexpr (two) o[i] = mma16<VF>(u32x4{lo.x, lo.y, hi.x, hi.y}, w2, o[i]);
       }
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      compiler_barrier();                                  // before the buffer is filled again
     }
     l = other_half_sum(other_row_sum(l));
     // the waves' sums, joined in shared memory

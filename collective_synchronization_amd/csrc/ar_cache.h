@@ -77,6 +77,7 @@ inline int check_cache_rows(const ar_kv_cache* c) {
   if (c->page_stride < 0 || c->token_stride < 0 || c->head_stride < 0) return AR_EINVAL;
   const int64_t most = int64_t(1) << 30;       // a page's number times its stride stays within 2^62 bytes
   if (c->page_stride >= most || c->token_stride >= most || c->head_stride >= most) return AR_ESIZE;
+  if (c->token_stride >= 1 << 26) return AR_ESIZE;      // 16 tokens' offsets stay 32-bit
   if (!rows_apart(c, c->dim, c->page_stride, c->token_stride, c->head_stride)) return AR_EINVAL;
   const int unit = c->format == AR_E4M3_ROW ? 16 : 8;
   if (!aligned(c->k, 16) || !aligned(c->v, 16) || c->page_stride % unit || c->token_stride % unit ||
