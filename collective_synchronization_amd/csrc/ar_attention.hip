@@ -166,6 +166,15 @@ __device__ __forceinline__ void load_to_lds(rsrc_t r, uint8_t* lds, uint32_t off
 }
 constexpr uint32_t kNowhere = 0x80000000u;   // past every range: reads as zeros
 
+template <int I> struct Index { static constexpr int value = I; };
+template <int N, int I = 0, class F>
+__device__ __forceinline__ void for_each(F f) {
+  if constexpr (I < N) {
+    f(Index<I>{});
+    for_each<N, I + 1>(f);
+  }
+}
+
 template <int QF, bool C8, int DT>
 struct Attn {
   static constexpr int VF = C8 ? AR_BF16 : QF;             // type of weights and values
@@ -195,7 +204,18 @@ struct Attn {
 
   // Pages of the N 16-key runs from `key` on; -1 for those that are none, or past the end.
   template <int N>
-  struct Pages { int at[N]; };
+  struct Pages {
+    int at[N];
+    // Run B + sub, sub < S.
+    template <int B, int S>
+    __device__ __forceinline__ int of(int sub) const {
+      int page = at[B];
+      if constexpr (S > 1) page = sub == 1 ? at[B + 1] : page;
+      if constexpr (S > 2) page = sub == 2 ? at[B + 2] : page;
+      if constexpr (S > 3) page = sub == 3 ? at[B + 3] : page;
+      return page;
+    }
+  };
   template <int N>
   static __device__ __forceinline__ Pages<N> find_pages(const AttnArgs& a, const Piece& p, int key) {
     Pages<N> r;
@@ -217,23 +237,31 @@ struct Attn {
     for (int i = 0; i < N; ++i) m |= r.at[i] < 0 ? 1u << i : 0u;
     return m;
   }
-  // Rows of token `key` and the ones after it up to `n`, or to the end.
-  static __device__ __forceinline__ rsrc_t rows(const AttnArgs& a, const Piece& p, const uint8_t* base, int page, int key,
-                                                int n) {
-    const int count = min(n, p.k1 - key);
-    const int64_t at = page * a.kv.page_stride + (key & (a.kv.page - 1)) * a.kv.token_stride + p.kh * a.kv.head_stride;
-    const uint32_t range = (uint32_t)(count - 1) * (uint32_t)a.kv.token_stride + (uint32_t)(a.kv.dim * (C8 ? 1 : 2));
-    const bool none = page < 0 || count <= 0;
-    return make_rsrc(none ? base : base + at, none ? 0u : range);
+  // The rows of a run of 16 tokens from `key` on, as far as they go: where the first
+  // one's keys and values are, and bytes up to the last one's end.
+  struct Run {
+    int64_t at;
+    uint32_t range;
+  };
+  static __device__ __forceinline__ Run run_of(const AttnArgs& a, const Piece& p, int page, int key) {
+    const int count = min(16, p.k1 - key);
+    if (page < 0 || count <= 0) return Run{0, 0};
+    return Run{page * a.kv.page_stride + (key & (a.kv.page - 1)) * a.kv.token_stride + p.kh * a.kv.head_stride,
+               (uint32_t)(count - 1) * (uint32_t)a.kv.token_stride + (uint32_t)(a.kv.dim * (C8 ? 1 : 2))};
+  }
+  static __device__ __forceinline__ rsrc_t rows(const uint8_t* base, const Run& r) {
+    // (the same for all lanes, which the compiler does not always see)
+    const uint64_t from = (uint64_t)(base + r.at);
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)from);
+    const uint32_t hi = __builtin_amdgcn_readfirstlane((int)(uint32_t)(from >> 32));
+    return make_rsrc(reinterpret_cast<const void*>((uint64_t)hi << 32 | lo),
+                     __builtin_amdgcn_readfirstlane((int)r.range));
   }
   // Scale of each lane's own key, `run` of the pages' runs.
   template <int N>
   static __device__ __forceinline__ float load_scale(const AttnArgs& a, const Piece& p, const float* base,
                                                      const Pages<N>& r, int key, int run) {
-    int page = r.at[0];
-#pragma unroll
-    for (int i = 1; i < N; ++i)
-      if (run == i) page = r.at[i];
+    const int page = r.template of<0, N>(run);
     if (page < 0 || key >= p.k1) return 0.0f;
     return base[page * a.kv.scale_page_stride + (key & (a.kv.page - 1)) * a.kv.scale_token_stride +
                 p.kh * a.kv.scale_head_stride];
@@ -294,21 +322,20 @@ struct Attn {
     for (int i = 0; i < passes; ++i) {
       const int k = i * pass_keys + wave * wave_keys + key_in;
       const int kc = C8 ? piece : piece ^ swap_k(k), vc = C8 ? piece : piece ^ swap_v(k);
-      k_off[i] = kc * CB < a.kv.dim ? (uint32_t)key_in * (uint32_t)a.kv.token_stride + kc * 16 : kNowhere;
-      v_off[i] = vc * CB < a.kv.dim ? (uint32_t)key_in * (uint32_t)a.kv.token_stride + vc * 16 : kNowhere;
+      k_off[i] = kc * CB < a.kv.dim ? (uint32_t)(k & 15) * (uint32_t)a.kv.token_stride + kc * 16 : kNowhere;
+      v_off[i] = vc * CB < a.kv.dim ? (uint32_t)(k & 15) * (uint32_t)a.kv.token_stride + vc * 16 : kNowhere;
     }
     u32x4 kr[C8 ? passes : 1], vr[C8 ? passes : 1];
     float scale = 0.0f;
     auto load_tile = [&](int key, int buf) {
       uint8_t* at = smem + buf * tile;
-#pragma unroll
-      for (int i = 0; i < passes; ++i) {
+      for_each<passes>([&](auto pass) {
+        constexpr int i = pass.value;
         const int k = i * pass_keys + wave * wave_keys;    // of the tile; on one page with the wave's others
-        int page = pages.at[0];
-#pragma unroll
-        for (int u = 1; u < runs; ++u)
-          if (k >> 4 == u) page = pages.at[u];
-        const rsrc_t kp = rows(a, p, a.kv.k, page, key + k, wave_keys), vp = rows(a, p, a.kv.v, page, key + k, wave_keys);
+        constexpr int each = pass_keys > 16 ? pass_keys / 16 : 1;
+        const int page = pages.template of<i * pass_keys / 16, each>(wave * wave_keys / 16);
+        const Run run = run_of(a, p, page, key + (k & ~15));
+        const rsrc_t kp = rows(a.kv.k, run), vp = rows(a.kv.v, run);
         if constexpr (C8) {
           kr[i] = __builtin_amdgcn_raw_buffer_load_b128(kp, k_off[i], 0, 0);
           vr[i] = __builtin_amdgcn_raw_buffer_load_b128(vp, v_off[i], 0, 0);
@@ -316,7 +343,7 @@ struct Attn {
           load_to_lds(kp, at + k * RS, k_off[i]);
           load_to_lds(vp, at + KT * RS + k * RS, v_off[i]);
         }
-      }
+      });
       if constexpr (C8) {
         if (tid < 2 * KT)
           scale = load_scale<runs>(a, p, tid < KT ? a.kv.k_scales : a.kv.v_scales, pages, key + tid % KT, tid % KT / 16);
@@ -515,7 +542,8 @@ struct Attn {
 #pragma unroll
     for (int i = 0; i < vloads; ++i) {
       const int c = C8 ? piece : piece ^ swap_v(i * wave_keys + key_in);
-      v_off[i] = c * CB < a.kv.dim ? (uint32_t)key_in * (uint32_t)a.kv.token_stride + c * 16 : kNowhere;
+      v_off[i] = c * CB < a.kv.dim
+                     ? (uint32_t)((i * wave_keys + key_in) & 15) * (uint32_t)a.kv.token_stride + c * 16 : kNowhere;
     }
     struct Keys {
       u32x4 k[2][kloads];
@@ -525,15 +553,16 @@ struct Attn {
     };
     constexpr int loads = 2 * kloads + vloads;             // of a step, without scales
     auto load_keys = [&](int at, int buf, Keys& f) {       // values first: keys that are there say that they are, too
+      const Run run[2] = {run_of(a, p, pages.at[0], at), run_of(a, p, pages.at[1], at + 16)};
 #pragma unroll
       for (int i = 0; i < vloads; ++i) {
-        const rsrc_t r = rows(a, p, a.kv.v, pages.at[i * wave_keys / 16], at + i * wave_keys, wave_keys);
+        const rsrc_t r = rows(a.kv.v, run[i * wave_keys / 16]);
         if constexpr (C8) f.v[i] = __builtin_amdgcn_raw_buffer_load_b128(r, v_off[i], 0, 0);
         else load_to_lds(r, mine + buf * few_step + i * wave_keys * RS, v_off[i]);
       }
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        const rsrc_t r = rows(a, p, a.kv.k, pages.at[t], at + 16 * t, 16);
+        const rsrc_t r = rows(a.kv.k, run[t]);
 #pragma unroll
         for (int i = 0; i < kloads; ++i) {
           if constexpr (C8 && !wide) {
