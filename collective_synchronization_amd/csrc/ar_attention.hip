@@ -257,12 +257,13 @@ struct Attn {
     return make_rsrc(reinterpret_cast<const void*>((uint64_t)hi << 32 | lo),
                      __builtin_amdgcn_readfirstlane((int)r.range));
   }
-  // Scale of each lane's own key, `run` of the pages' runs.
-  template <int N>
-  static __device__ __forceinline__ float load_scale(const AttnArgs& a, const Piece& p, const float* base,
-                                                     const Pages<N>& r, int key, int run) {
-    const int page = r.template of<0, N>(run);
-    if (page < 0 || key >= p.k1) return 0.0f;
+  // Scales: each lane has its own key, whose page it has read before.
+  static __device__ __forceinline__ int scale_page(const AttnArgs& a, const Piece& p, int key) {
+    return C8 ? p.table[min(key, p.k1 - 1) >> a.kv.page_shift] : -1;
+  }
+  static __device__ __forceinline__ float load_scale(const AttnArgs& a, const Piece& p, const float* base, int page,
+                                                     int key) {
+    if ((uint32_t)page >= (uint32_t)a.kv.pages || key >= p.k1) return 0.0f;
     return base[page * a.kv.scale_page_stride + (key & (a.kv.page - 1)) * a.kv.scale_token_stride +
                 p.kh * a.kv.scale_head_stride];
   }
@@ -300,6 +301,7 @@ struct Attn {
     const bool idle = first >= p.rows;
     constexpr int runs = KT / 16, pass_keys = kAttnThreads / CH;
     auto pages = find_pages<runs>(a, p, p.k0);
+    int of_scale = scale_page(a, p, p.k0 + tid % KT);
     u32x4 q[DT / 16];
     {
       const uint8_t* at = query(a, p, row);
@@ -346,7 +348,7 @@ struct Attn {
       });
       if constexpr (C8) {
         if (tid < 2 * KT)
-          scale = load_scale<runs>(a, p, tid < KT ? a.kv.k_scales : a.kv.v_scales, pages, key + tid % KT, tid % KT / 16);
+          scale = load_scale(a, p, tid < KT ? a.kv.k_scales : a.kv.v_scales, of_scale, key + tid % KT);
       }
     };
     auto store_tile = [&](int buf) {
@@ -377,6 +379,7 @@ struct Attn {
     load_tile(p.k0, 0);
     uint32_t gone = missing(pages);
     pages = find_pages<runs>(a, p, p.k0 + KT);
+    of_scale = scale_page(a, p, p.k0 + KT + tid % KT);
     store_tile(0);
     arrived();
     // group of 16 lanes: columns 16 * (group % 2) on, keys 4 * half on and 8 after them
@@ -392,6 +395,7 @@ struct Attn {
         load_tile(key + KT, buf ^ 1);
         next_gone = missing(pages);
         pages = find_pages<runs>(a, p, key + 2 * KT);
+        of_scale = scale_page(a, p, key + 2 * KT + tid % KT);
       }
       if (!idle) {
         const uint8_t* ks = smem + buf * tile;
@@ -518,6 +522,7 @@ struct Attn {
     auto elem = [&](int i) { return wide ? 64 * (i / 2) + 16 * g + 8 * (i & 1) : 32 * i + 8 * g; };
     int key = p.k0 + 32 * wave;
     auto pages = find_pages<2>(a, p, key);
+    int of_scale = scale_page(a, p, key + (lane & 31));
     u32x4 q[steps];
     {
       const uint8_t* at = query(a, p, col);
@@ -574,7 +579,7 @@ struct Attn {
         }
       }
       if constexpr (C8)
-        f.scale = load_scale<2>(a, p, lane < 32 ? a.kv.k_scales : a.kv.v_scales, pages, at + (lane & 31), lane >> 4 & 1);
+        f.scale = load_scale(a, p, lane < 32 ? a.kv.k_scales : a.kv.v_scales, of_scale, at + (lane & 31));
       f.gone = missing(pages);
     };
 
@@ -583,6 +588,7 @@ struct Attn {
       check_pages(a, p, key, pages);
       load_keys(key, 0, cur);
       pages = find_pages<2>(a, p, key + stride);
+      of_scale = scale_page(a, p, key + stride + (lane & 31));
     }
     for (int buf = 0; key < p.k1; key += stride, buf ^= C8 ? 0 : 1) {
       const uint32_t gone = cur.gone;
@@ -615,6 +621,7 @@ struct Attn {
         check_pages(a, p, key + stride, pages);
         load_keys(key + stride, buf ^ 1, cur);
         pages = find_pages<2>(a, p, key + 2 * stride);
+        of_scale = scale_page(a, p, key + 2 * stride + (lane & 31));
       }
       f32x4 s[2];
 #pragma unroll
