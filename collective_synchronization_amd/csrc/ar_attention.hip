@@ -907,8 +907,12 @@ struct AttnPlan {
 
 // Pieces of keys.  A piece costs a step for each 64 keys of a tile of many rows,
 // or for each 128 that the waves of few rows take together; all are made as
-// long as fills the chip's 512 places for workgroups (two to a CU) once, or
-// twice where pieces are long, so that they end together.
+// long as fills the chip's places for workgroups once: four to a CU where heads are of
+// up to 64, two up to 128, else one, by registers and shared memory.  Short pieces
+// are made twice as long: their rows' way through memory to the join counts more.
+// 128 x 64 heads over 32768, bf16: 192 us with 512 pieces, 204 with 1024; heads of 64
+// 112 and 105; of 256 277 and, with 256 pieces, 254; 16 x 64 heads over 8192 27 with
+// 512, 23 with 256.
 static AttnPlan plan_attention(const ar_attention_params* p) {
   AttnPlan s{};
   const int64_t kv = p->cache.kv_heads, group = p->heads / kv;
@@ -920,8 +924,9 @@ static AttnPlan plan_attention(const ar_attention_params* p) {
   s.own_tiles = (int32_t)tiles(own_rows);
   const int64_t shared = kv * s.prefix_tiles * ceil_div64(p->prefix, step(rows));
   const int64_t own = p->sequences * kv * s.own_tiles * ceil_div64(capacity, step(own_rows));
-  int64_t steps = ceil_div64(shared + own, 512);
-  if (steps >= 32) steps = ceil_div64(steps, 2);
+  const int64_t places = p->cache.dim <= 64 ? 1024 : (p->cache.dim <= 128 ? 512 : 256);
+  int64_t steps = ceil_div64(shared + own, places);
+  if (steps < 6) steps = ceil_div64(shared + own, 256);
   if (p->prefix > 0) {
     const int64_t n = ceil_div64(p->prefix, steps * step(rows));
     s.prefix_chunk = (int32_t)(ceil_div64(ceil_div64(p->prefix, n), 64) * 64);
