@@ -446,6 +446,8 @@ static int check_adapter_rows(const ar_linear_params* p, const ar_adapter_params
   if (q->a_adapter_stride >= most || q->a_rank_stride >= most || q->b_adapter_stride >= most ||
       q->b_rank_stride >= most)
     return AR_ESIZE;
+  const int64_t each = (int64_t(1) << 60) / q->adapters;
+  if (q->a_adapter_stride > each || q->b_adapter_stride > each) return AR_ESIZE;
   if (q->b_stride >= 1 << 23) return AR_ESIZE;             // 128 rows' offsets stay 32-bit
   if (q->a_adapter_stride % 8 || q->b_adapter_stride % 8) return AR_EALIGN;
   if (p->nranks > 1 && (q->a_rank_stride % 8 || q->b_rank_stride % 8)) return AR_EALIGN;

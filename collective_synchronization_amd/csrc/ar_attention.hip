@@ -874,7 +874,7 @@ static int check_attention(const ar_attention_params* p) {
 }
 
 static int check_attention_rows(const ar_attention_params* p) {
-  const int64_t most = int64_t(1) << 40;
+  const int64_t most = int64_t(1) << 36;                   // times 2^26 rows within 2^62
   const int64_t tokens = p->sequences * p->queries;
   if (!p->q || !p->out || !p->lengths) return AR_EINVAL;
   if (p->max_pages > 0 && (!p->pages || (p->sequences > 1 && p->pages_stride < p->max_pages))) return AR_EINVAL;
@@ -882,7 +882,7 @@ static int check_attention_rows(const ar_attention_params* p) {
   if (p->q_stride < 0 || p->q_head_stride < 0 || p->out_stride < 0 || p->out_head_stride < 0 || p->lse_stride < 0)
     return AR_EINVAL;
   if (p->q_stride >= most || p->q_head_stride >= most || p->out_stride >= most || p->out_head_stride >= most ||
-      p->lse_stride >= most || p->pages_stride >= most)
+      p->lse_stride >= most || p->pages_stride >= (int64_t(1) << 30))
     return AR_ESIZE;
   // outputs may not overlap each other
   const int64_t dim = p->cache.dim, heads = p->heads;

@@ -537,7 +537,8 @@ typedef struct {
  * with infinities in b may be NaN.  The order of every sum is fixed by the
  * sizes, so equal calls give equal bits, and a token's bits do not depend on the
  * other tokens' adapters.  adapters, rank or inputs 0: ar_mx4_linear alone.
- * AR_ESIZE: b_stride of 2^23 and more, and as for ar_mx4_linear.
+ * AR_ESIZE: b_stride of 2^23 and more, adapters whose offsets pass 2^60, and as
+ * for ar_mx4_linear.
  */
 int ar_mx4_linear_adapters(const ar_linear_params* p, const ar_adapter_params* q, void* work,
                            int64_t work_bytes, void* stream);
@@ -552,7 +553,8 @@ int64_t ar_adapter_work_bytes(const ar_linear_params* p, const ar_adapter_params
  * same place of v.  Rows are of AR_BF16, AR_F16 or AR_E4M3_ROW (strides in
  * elements or bytes), 16-byte aligned, strides multiples of 8 elements or 16
  * bytes; AR_E4M3_ROW has a binary32 scale for each row, with strides of its
- * own in floats.  Rows may lie in any order but not overlap.
+ * own in floats.  Rows may lie in any order but not overlap.  AR_ESIZE: 2^31
+ * and more pages, strides of 2^30 (token_stride 2^26) and more.
  */
 #define AR_CACHE_MAX_DIM 256
 typedef struct {
@@ -643,7 +645,7 @@ typedef struct {
  * of every sum is fixed by the sizes and lengths, so equal calls give equal
  * bits.  out may not overlap the inputs.  sequences 0: nothing is written.
  * AR_ESIZE: sequences, prefix or max_pages * page above 2^30, 2^26 or more
- * rows of all heads, strides of 2^40 and more.
+ * rows of all heads, strides of 2^36 (pages_stride 2^30) and more.
  */
 int ar_prefix_attention(const ar_attention_params* p, void* work, int64_t work_bytes, void* stream);
 
