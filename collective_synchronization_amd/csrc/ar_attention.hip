@@ -166,6 +166,14 @@ __device__ __forceinline__ void load_to_lds(rsrc_t r, uint8_t* lds, uint32_t off
 }
 constexpr uint32_t kNowhere = 0x80000000u;   // past every range: reads as zeros
 
+// Which halves of a pair of 16-bit values are infinities or NaNs: all ones there.
+template <int F>
+__device__ __forceinline__ uint32_t odd_halves(uint32_t v) {
+  constexpr uint32_t top = F == AR_BF16 ? 0x7F80u : 0x7C00u;
+  return ((v & top) == top ? 0xFFFFu : 0u) | ((v >> 16 & top) == top ? 0xFFFF0000u : 0u);
+}
+template <int F> constexpr uint32_t ones16() { return F == AR_BF16 ? 0x3F803F80u : 0x3C003C00u; }
+
 template <int I> struct Index { static constexpr int value = I; };
 template <int N, int I = 0, class F>
 __device__ __forceinline__ void for_each(F f) {
@@ -175,7 +183,9 @@ __device__ __forceinline__ void for_each(F f) {
   }
 }
 
-template <int QF, bool C8, int DT>
+// LATER: there may be tokens that other tokens of their step do not see (two and
+// more queries of a sequence).
+template <int QF, bool C8, int DT, bool LATER>
 struct Attn {
   static constexpr int VF = C8 ? AR_BF16 : QF;             // type of weights and values
   // Weights times the scales of 8-bit values can have any exponent, so they are
@@ -284,6 +294,57 @@ struct Attn {
   static __device__ __forceinline__ u32x4 query8(const AttnArgs& a, const uint8_t* row, int d) {
     return d < a.kv.dim ? ldg16(row + d * 2) : u32x4{0u, 0u, 0u, 0u};
   }
+  // What a token of the step does not see may not touch it, be it an infinity or a
+  // NaN, which its weight 0 would make NaN.  So where keys that some of the rows do
+  // not see have such values, or scales (values_odd), these are taken out, and
+  // counted for each output by a product of their places with those of the keys
+  // that are seen: an output with any is NaN.
+  static __device__ __forceinline__ bool values_odd(const uint8_t* values, const float* scales, int n, int lane) {
+    uint32_t odd = 0;
+    for (int i = lane; i < n * C16; i += kWave) {
+      const u32x4 v = *reinterpret_cast<const u32x4*>(values + i * 16);
+      odd |= odd_halves<VF>(v.x) | odd_halves<VF>(v.y) | odd_halves<VF>(v.z) | odd_halves<VF>(v.w);
+    }
+    if constexpr (C8) {
+      if (lane < n && abs_bits(scales[lane]) >= kInfBits) odd = 1;
+    }
+    return __any(odd != 0);
+  }
+  // 8 keys' weights of a row, 1 for those that are seen, and a column's values and the
+  // places of odd ones.
+  struct Apart {
+    u32x4 w, w2, seen, v, odd;
+    float sum;
+  };
+  static __device__ __forceinline__ Apart apart(const float (&score)[8], float c, float ref, const float (&scale)[8],
+                                                u32x4 v) {
+    Apart x;
+    x.sum = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float e[2], s[2];
+      uint32_t odd = odd_halves<VF>(v[j]);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const float t = score[2 * j + u];
+        s[u] = t == -__builtin_inff() ? 0.0f : 1.0f;
+        e[u] = t == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(__builtin_fmaf(t, c, -ref));
+        x.sum += e[u];
+        if constexpr (C8) {
+          const bool bad = abs_bits(scale[2 * j + u]) >= kInfBits;
+          e[u] = bad ? 0.0f : e[u] * scale[2 * j + u];
+          if (bad) odd |= u ? 0xFFFF0000u : 0xFFFFu;
+        }
+      }
+      x.w[j] = pair16<VF>(e[0], e[1]);
+      x.w2[j] = 0;
+      if constexpr (two) x.w2[j] = rest16<VF>(e[0], e[1], x.w[j]);
+      x.seen[j] = pair16<VF>(s[0], s[1]);
+      x.v[j] = v[j] & ~odd;
+      x.odd[j] = ones16<VF>() & odd;
+    }
+    return x;
+  }
   // Row of the parts' arrays.
   static __device__ __forceinline__ int64_t out_row(const AttnArgs& a, const Piece& p, int row) {
     return (int64_t)p.part * a.rows + (int64_t)(p.token0 + row / a.group) * a.heads + p.kh * a.group + row % a.group;
@@ -387,7 +448,7 @@ struct Attn {
     const int k_base = col * RS, k_swap = half ^ swap_k(col);
     const int v_base = KT * RS + vk * RS + (lane & 1) * 8, v_swap = vc ^ swap_v(vk);
     int buf = 0;
-    for (int key = p.k0; key < p.k1; key += KT, buf ^= 1) {
+    auto step = [&](auto all_see, int key) {
       const bool more = key + KT < p.k1;
       uint32_t next_gone = 0;
       if (more) {
@@ -420,7 +481,7 @@ struct Attn {
               for (int j = 0; j < 4; ++j) s[t][r + j] *= m[j];
             }
         }
-        if (gone != 0 || key + KT > least) {
+        if (gone != 0 || !all_see.value) {
 #pragma unroll
           for (int t = 0; t < KT / 32; ++t)
 #pragma unroll
@@ -447,6 +508,36 @@ struct Attn {
 #pragma unroll
             for (int r = 0; r < 16; ++r) o[i][r] *= f;
         }
+        if (LATER && !all_see.value && values_odd(ks + KT * RS, sc + KT, KT, lane)) {
+          for_each<DT / 32>([&](auto index) {
+            constexpr int i = index.value;
+            f32x16 count;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) count[r] = 0.0f;
+            for_each<KT / 16>([&](auto index) {
+              constexpr int t = index.value;
+              __builtin_amdgcn_sched_barrier(0);           // one piece at a time, and its weights formed anew for
+              int first = 4 * half;                        // each i: registers are short
+              __asm__ volatile("" : "+v"(first));
+              float score[8], scale[8];
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                score[j] = s[t / 2][8 * (t % 2) + j];
+                __asm__ volatile("" : "+v"(score[j]));
+                scale[j] = C8 ? sc[KT + 16 * t + (j < 4 ? 0 : 4) + first + j] : 1.0f;
+              }
+              const uint8_t* at = ks + v_base + ((4 * i) ^ v_swap) * 16 + 16 * t * RS;
+              const u32x2 lo = read_transposed(at), hi = read_transposed(at + 8 * RS);
+              const Apart x = apart(score, a.c, ref, scale, u32x4{lo.x, lo.y, hi.x, hi.y});
+              if constexpr (i == 0) l += x.sum;
+              o[i] = mma32<VF>(x.v, x.w, o[i]);
+              if constexpr (two) o[i] = mma32<VF>(x.v, x.w2, o[i]);
+              count = mma32<VF>(x.odd, x.seen, count);
+            });
+#pragma unroll
+            for (int r = 0; r < 16; ++r) o[i][r] = count[r] > 0.0f ? __builtin_nanf("") : o[i][r];
+          });
+        } else {
         u32x4 w[KT / 16], w2[two ? KT / 16 : 1];
 #pragma unroll
         for (int t = 0; t < KT / 32; ++t) {
@@ -482,13 +573,19 @@ struct Attn {
             o[i] = mma32<VF>(u32x4{lo.x, lo.y, hi.x, hi.y}, w[t], o[i]);
             if constexpr (two) o[i] = mma32<VF>(u32x4{lo.x, lo.y, hi.x, hi.y}, w2[t], o[i]);
           }
+        }
       }
       if (more) {
         store_tile(buf ^ 1);
         gone = next_gone;
       }
       arrived();
-    }
+      buf ^= 1;
+    };
+    // tiles that all tokens see whole, and those in which some stop, or all
+    int key = p.k0;
+    for (; key + KT <= least; key += KT) step(Index<1>{}, key);
+    for (; key < p.k1; key += KT) step(Index<0>{}, key);
     l = other_half_sum(l);
     if (row < p.rows) {
       const int64_t at = out_row(a, p, row);
@@ -662,6 +759,31 @@ struct Attn {
 #pragma unroll
         for (int i = 0; i < DT / 16; ++i) o[i] *= f;
       }
+      // rows 4g on and 16 after them, columns 4 * (lane % 4) on of each 16
+      const int vk = 4 * g + col / 4, swap = ((lane & 3) / 2) ^ swap_v(vk);
+      const uint8_t* at = vs + vk * RS + (lane & 1) * 8;
+      if (LATER && p.causal && key + 32 > least && values_odd(vs, sc + 32, 32, lane)) {
+        float score[8], scale[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          score[j] = s[j / 4][j % 4];
+          scale[j] = C8 ? sc[32 + 16 * (j / 4) + 4 * g + j % 4] : 1.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < DT / 16; ++i) {
+          __builtin_amdgcn_sched_barrier(0);
+          float again = ref;
+          __asm__ volatile("" : "+v"(again));
+          const u32x2 lo = read_transposed(at + ((2 * i) ^ swap) * 16), hi = read_transposed(at + 16 * RS + ((2 * i) ^ swap) * 16);
+          const Apart x = apart(score, a.c, again, scale, u32x4{lo.x, lo.y, hi.x, hi.y});
+          if (i == 0) l += x.sum;
+          o[i] = mma16<VF>(x.v, x.w, o[i]);
+          if constexpr (two) o[i] = mma16<VF>(x.v, x.w2, o[i]);
+          const f32x4 count = mma16<VF>(x.odd, x.seen, f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+#pragma unroll
+          for (int r = 0; r < 4; ++r) o[i][r] = count[r] > 0.0f ? __builtin_nanf("") : o[i][r];
+        }
+      } else {
       f32x4 e[2];
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
@@ -678,14 +800,12 @@ struct Attn {
       if constexpr (two)
         w2 = u32x4{rest16<VF>(e[0][0], e[0][1], w.x), rest16<VF>(e[0][2], e[0][3], w.y),
                    rest16<VF>(e[1][0], e[1][1], w.z), rest16<VF>(e[1][2], e[1][3], w.w)};
-      // rows 4g on and 16 after them, columns 4 * (lane % 4) on of each 16
-      const int vk = 4 * g + col / 4, swap = ((lane & 3) / 2) ^ swap_v(vk);
-      const uint8_t* at = vs + vk * RS + (lane & 1) * 8;
 #pragma unroll
       for (int i = 0; i < DT / 16; ++i) {
         const u32x2 lo = read_transposed(at + ((2 * i) ^ swap) * 16), hi = read_transposed(at + 16 * RS + ((2 * i) ^ swap) * 16);
         o[i] = mma16<VF>(u32x4{lo.x, lo.y, hi.x, hi.y}, w, o[i]);
         if constexpr (two) o[i] = mma16<VF>(u32x4{lo.x, lo.y, hi.x, hi.y}, w2, o[i]);
+      }
       }
       compiler_barrier();                                  // before the buffer is filled again
     }
@@ -728,9 +848,9 @@ struct Attn {
 // sequences' rows, or of one sequence's own tokens.  Workgroups go round the 8
 // XCDs one by one; each XCD takes a run of pieces, those with the same keys
 // next to each other, in its own L2.
-template <int QF, bool C8, int DT>
+template <int QF, bool C8, int DT, bool LATER>
 __global__ __launch_bounds__(kAttnThreads, DT > 128 ? 1 : 2) void k_attention(AttnArgs a) {
-  using G = Attn<QF, C8, DT>;
+  using G = Attn<QF, C8, DT, LATER>;
   __shared__ __align__(256) uint8_t smem[G::lds];
   Piece p;
   int b = blockIdx.x;
@@ -944,7 +1064,9 @@ static int64_t attention_bytes(const ar_attention_params* p, const AttnPlan& s) 
 
 template <int QF, bool C8, int DT>
 static hipError_t launch_parts(const AttnArgs& a, hipStream_t s) {
-  return launch(k_attention<QF, C8, DT>, dim3((unsigned)(a.prefix_blocks + a.own_blocks)), dim3(kAttnThreads), s, a);
+  const dim3 grid((unsigned)(a.prefix_blocks + a.own_blocks)), block(kAttnThreads);
+  return a.queries > 1 ? launch(k_attention<QF, C8, DT, true>, grid, block, s, a)
+                       : launch(k_attention<QF, C8, DT, false>, grid, block, s, a);
 }
 template <int QF, bool C8>
 static hipError_t launch_parts_dim(const AttnArgs& a, hipStream_t s) {

@@ -240,6 +240,52 @@ def test_infinite_and_nan_keys(queries):
     assert (np.abs(out - want[0])[:queries] <= 2.0 ** -6 * want[2][:queries]).all()
 
 
+@pytest.mark.parametrize("what", ["nan", "inf", "scale"])
+@pytest.mark.parametrize("fmt,cache", [("bf16", "same"), ("f16", "same"), ("bf16", "row8"), ("f16", "row8")])
+@pytest.mark.parametrize("queries,heads", [(3, 4), (9, 4), (40, 2), (5, 32)])
+def test_odd_values_of_later_tokens_are_not_seen(queries, heads, fmt, cache, what):
+    """Infinities and NaNs in the keys and values of the step's last token leave the tokens before it as they are."""
+    if cache == "same" and what == "scale":
+        pytest.skip("no scales")
+    b = Batch(12, (70, 64 + queries), queries, heads, 2, 64, 16, 20, fmt, cache, poison=False)
+    for i in range(2):
+        at = b.lengths[i] - 1
+        p, s = int(b.pages[i, at // 16]), at % 16
+        if what == "scale":
+            for sc in b.cache.tensors[2:]:
+                sc[p, s] = float("inf") if i else float("nan")
+        elif cache == "row8":
+            b.kd[p, s] = b.vd[p, s] = 0x7F
+        else:
+            b.kd[p, s] = b.vd[p, s] = float("nan") if what == "nan" else float("inf")
+    prm = b.params()
+    abi.ar_prefix_attention(prm, b.work(prm))
+    torch.cuda.synchronize()
+    last = np.arange(2 * queries) % queries == queries - 1
+    got = b.out[:2 * queries, :, :64].double().cpu().numpy()
+    if what != "scale":                        # (a key's infinite scale can give it the score -inf)
+        assert not np.isfinite(got[last]).any(-1).any()
+    # the others: as from tokens that are there
+    want, _, size, top, mass = oc.attention(b.q, b.k, b.v, b.scale, b.prefix, b.prefix_pages, b.lengths, b.pages, queries)
+    e = 64 * 2.0 ** -23 * mass + 2 * 2.0 ** -24 * top * 1.4427 + 2.0 ** -22
+    u = U[fmt]
+    tol = size * (u + 2 * e[..., None] + 200 * 2.0 ** -23) + u * np.abs(want) + 200 * 2.0 ** -31 * np.abs(b.v).max() + 2.0 ** -25
+    assert (np.abs(got - want)[~last] <= tol[~last]).all()
+
+
+def test_nothing_to_see():
+    """No prefix and no pages at all: zeros, and no work buffer."""
+    q = torch.ones((3, 4, 32), dtype=torch.bfloat16, device="cuda")
+    out, lse = torch.full_like(q, -77.0), torch.full((3, 4), -77.0, device="cuda")
+    c = abi.cache_params("bf16", 0, 16, 2, 32, None, None, 1024, 64, 32)
+    lengths = torch.tensor([0, 5, -1], dtype=torch.int32, device="cuda")
+    p = abi.attention_params(c, 3, 1, 4, 1.0, "bf16", q, 128, 32, out, 128, 32, lse, 4, 0, None, lengths, None, 0, 0)
+    assert abi.ar_prefix_attention_work_bytes(p) == 0
+    abi.ar_prefix_attention(p, None)
+    torch.cuda.synchronize()
+    assert (out[:2] == 0).all() and (lse[:2] == float("-inf")).all() and (out[2] == -77.0).all() and (lse[2] == -77.0).all()
+
+
 def test_far_offsets():
     """A cache of more than 2^32 bytes, its last pages in use."""
     page, kv, dim = 128, 8, 128
