@@ -99,6 +99,8 @@ class PagedCache:
         (int32 [sequences, pages of each])."""
         fmt = {torch.bfloat16: abi.AR_BF16, torch.float16: abi.AR_F16}.get(k.dtype)
         sequences = pages.shape[0]
+        if sequences == 0 and k.shape[0] == 0:
+            return
         if fmt is None or v.dtype != k.dtype or k.shape != v.shape or sequences == 0 or \
                 k.shape[0] % sequences or k.shape[1:] != (self.kv_heads, self.dim) or \
                 lengths.dtype != torch.int32 or pages.dtype != torch.int32 or \

@@ -649,7 +649,7 @@ __device__ __forceinline__ void add_adapters(const Adapters& ad, const MxLinArgs
   constexpr int P = G::YF == AR_F32 ? 3 : 2, TI = G::WN / 16, TJ = G::WM / 16, threads = G::threads;
   constexpr int TS = 64 * P + 16, BS = 64 + 16;            // 16 rows' reads meet different banks
   constexpr int pieces = G::BN * 4 / threads, sets = G::BM / kWave;
-  static_assert(G::KG == 1 && G::BM % kWave == 0 && G::BN * 4 % threads == 0, "");
+  static_assert(G::KG == 1 && TI % 4 == 0 && G::BM % kWave == 0 && G::BN * 4 % threads == 0, "");
   static_assert(G::BM * (4 + TS) + 2 * G::BN * BS <= G::lds, "room for t and b");
   const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, g = lane >> 4;
   int* ids = reinterpret_cast<int*>(smem);
@@ -722,31 +722,37 @@ __device__ __forceinline__ void add_adapters(const Adapters& ad, const MxLinArgs
       __syncthreads();                                     // the other buffer's readers are through, too
       const int after = next();
       if (after >= 0) load_rows(after);
+      // this wave's rows of b, 4 tiles of outputs at a time
 #pragma unroll
-      for (int j = 0; j < TJ; ++j) {
-        const bool take = ids[wm + 16 * j + c] == which;
-        if (!__any(take)) continue;
-        const bool each = __all(take);
-        u32x4 t[P];
+      for (int i0 = 0; i0 < TI; i0 += 4) {
+        bf16x8 x[4];
 #pragma unroll
-        for (int k = 0; k < P; ++k)
-          t[k] = *reinterpret_cast<const u32x4*>(ts + (wm + 16 * j + c) * TS + g * (16 * P) + 16 * k);
+        for (int i = 0; i < 4; ++i)
+          x[i] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(rows + (wn + 16 * (i0 + i) + c) * BS + g * 16));
 #pragma unroll
-        for (int i = 0; i < TI; ++i) {
-          const bf16x8 x =
-              __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(rows + (wn + 16 * i + c) * BS + g * 16));
-          f32x4 v = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int j = 0; j < TJ; ++j) {
+          const bool take = ids[wm + 16 * j + c] == which;
+          if (!__any(take)) continue;
+          const bool each = __all(take);
+          u32x4 t[P];
 #pragma unroll
           for (int k = 0; k < P; ++k)
-            v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, __builtin_bit_cast(bf16x8, t[k]), v, 0, 0, 0);
-          if (each) {
-            acc(i, j) += v;
-          } else {
+            t[k] = *reinterpret_cast<const u32x4*>(ts + (wm + 16 * j + c) * TS + g * (16 * P) + 16 * k);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc(i, j)[e] += take ? v[e] : 0.0f;
+          for (int i = 0; i < 4; ++i) {
+            f32x4 v = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int k = 0; k < P; ++k)
+              v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[i], __builtin_bit_cast(bf16x8, t[k]), v, 0, 0, 0);
+            if (each) {
+              acc(i0 + i, j) += v;
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) acc(i0 + i, j)[e] += take ? v[e] : 0.0f;
+            }
           }
+          __builtin_amdgcn_sched_barrier(0);               // one tile's operands at a time: the sums fill the registers
         }
-        __builtin_amdgcn_sched_barrier(0);                 // one tile's operands at a time: the sums fill the registers
       }
       which = after;
     }
