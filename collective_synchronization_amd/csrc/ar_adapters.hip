@@ -22,22 +22,16 @@ struct TokenArgs {
   const float* scale;
   uint8_t* t;
   int64_t t_stride, t_part, t_rank;  // part p of rank r's row m: t + p * t_part + r * t_rank + m * t_stride
-  int32_t M, K;
+  int32_t M, K, nb;
   int32_t count, rank;
   int32_t splits, slots, r_groups, m_groups;
 };
 
-// A lane's operands of 128 elements of K: group g has 32 of them, from 32g on,
-// 8 in each of 4 matrix instructions, so that x's and a's rows are read 16 bytes
-// at a time in every format.
+// A lane's part of 128 elements of K: group g has 32 of them, from 32g on, 8 in
+// each of 4 matrix instructions, so that rows of x are read 16 bytes at a time in
+// every format.
 template <int XF>
 constexpr int row_pieces() { return elem_bits<XF>() / 4; }
-template <int XF, int TT>
-struct TokenStep {
-  u32x4 x[TT][row_pieces<XF>()];
-  uint32_t s[TT];
-  u32x4 a[4];
-};
 
 template <int XF>
 __device__ __forceinline__ u32x4 token_operand(const u32x4 (&x)[row_pieces<XF>()], uint32_t scale, int u) {
@@ -171,25 +165,37 @@ __global__ __launch_bounds__(kBlock) void k_adapter_few_tokens(TokenArgs s) {
 }
 
 constexpr int kTokenGroup = 256;
+constexpr int kTurn = 64;                                  // tokens of a workgroup's turn
 
-// Parts of t for 16 * TT tokens of one adapter, in 16 * WR of its dimensions, over
+// Parts of t for up to 64 tokens of one adapter, in 16 * NR of its dimensions, over
 // a share of K.  Bound by the way of a and x to the CUs.  A group is 256 tokens:
 // its workgroups find the group's adapters, each with the list of its tokens, and
-// take turns with them, 16 * TT tokens at a time, so that tokens in any order read
-// an adapter's rows once for all of them.  `splits` workgroups share K for each.
-// (Groups go round the XCDs, so that each reads all of K: with a share of K each,
-// rows 8 and 16 KiB apart met a quarter of an L2's channels, 4096 x 8192, rank 64,
-// 62 us.)  In a workgroup WR waves have 16 dimensions each (they read the same tokens,
-// the later ones from the L1), WK share the steps, and join their sums in shared memory;
-// the workgroups' sums are joined by k_adapter_sum.
-template <int XF, int WR, int WK, int TT>
-__global__ __launch_bounds__(kWave * WR * WK, 2) void k_adapter_tokens(TokenArgs s) {
-  constexpr int W = WR * WK;
-  __shared__ f32x4 part[WK > 1 ? W * TT * kWave : 1];
+// take turns with them, so that tokens in any order read an adapter's rows once
+// for all of them.  `splits` workgroups share K for each; their sums are joined by
+// k_adapter_sum.  A wave has 16 of the tokens.  Steps of 128 elements pass
+// through shared memory, loaded straight into it, the ones after a step on their
+// way while it is multiplied; rows lie there with their 16-byte pieces permuted
+// so that lanes which read at once meet different banks.  (Groups go round the
+// XCDs, so that each reads all of K: with a share of K each, rows 8 and 16 KiB
+// apart meet a quarter of an L2's channels.)
+template <int XF, int NR>
+struct TokenTile {
+  static constexpr int XB = 16 * elem_bits<XF>(), XC = XB / 16, AC = 16;   // bytes and pieces of a row's step
+  static constexpr int nx = kTurn * XC / kBlock, na = NR * 16 * AC / kBlock;
+  static constexpr int scales = is_mx_format(XF) ? kWavesPerBlock * 256 : 0;
+  static constexpr int stage = kTurn * XB + NR * 16 * AC * 16 + scales;
+  static constexpr int NS = 3 * stage <= 80 * 1024 ? 3 : 2;
+  static constexpr int loads = nx + na + (is_mx_format(XF) ? 1 : 0);
+  static_assert(kWavesPerBlock * 16 == kTurn, "a wave has 16 tokens");
+};
+template <int XF, int NR>
+__global__ __launch_bounds__(kBlock) void k_adapter_tokens(TokenArgs s) {
+  using T = TokenTile<XF, NR>;
+  constexpr int NS = T::NS;
+  __shared__ __align__(256) uint8_t smem[NS * T::stage];
   __shared__ int list[kTokenGroup];
-  const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wr = wave % WR, wk = wave / WR;
+  const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   int b = blockIdx.x;
   const int m0 = b % s.m_groups * kTokenGroup;
   b /= s.m_groups;
@@ -197,17 +203,18 @@ __global__ __launch_bounds__(kWave * WR * WK, 2) void k_adapter_tokens(TokenArgs
   b /= s.slots;
   const int split = b % s.splits;
   b /= s.splits;
-  const int j0 = (b % s.r_groups * WR + wr) * 16, r = b / s.r_groups;
+  const int j0 = b % s.r_groups * 16 * NR, r = b / s.r_groups;
   const int steps = (s.K + 127) / 128, each = (steps + s.splits - 1) / s.splits;
-  const int st0 = split * each + wk, st1 = min(steps, split * each + each);
+  const int st0 = split * each, n = max(min(steps, st0 + each) - st0, 0);
   int mine[4];
   uint64_t left[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const int m = m0 + 64 * k + lane;
     mine[k] = m < s.M ? s.index[m] : -1;
-    left[k] = __ballot((uint32_t)mine[k] < (uint32_t)s.count);
   }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) left[k] = __ballot((uint32_t)mine[k] < (uint32_t)s.count);
   int turn = 0;
   while ((left[0] | left[1] | left[2] | left[3]) != 0) {
     int which = 0;
@@ -227,7 +234,7 @@ __global__ __launch_bounds__(kWave * WR * WK, 2) void k_adapter_tokens(TokenArgs
       tokens += __builtin_popcountll(has[k]);
     }
     const int first = turn;
-    turn += (tokens + 16 * TT - 1) / (16 * TT);
+    turn += (tokens + kTurn - 1) / kTurn;
     // this workgroup's turns among them
     if (first + (slot - first % s.slots + s.slots) % s.slots >= turn) continue;
     __syncthreads();                                       // the list was read
@@ -241,101 +248,101 @@ __global__ __launch_bounds__(kWave * WR * WK, 2) void k_adapter_tokens(TokenArgs
     }
     __syncthreads();
     const float scale = s.scale ? s.scale[which] : 1.0f;
-    const uint8_t* a = s.a + r * s.a_rank + which * s.a_adapter + min(j0 + c, s.rank - 1) * s.a_stride;
-    for (int t0 = 0, it = first; t0 < tokens; t0 += 16 * TT, ++it) {
+    for (int t0 = 0, it = first; t0 < tokens; t0 += kTurn, ++it) {
       if (it % s.slots != slot) continue;
-      const int tiles = min(TT, (tokens - t0 + 15) / 16);
-      const uint8_t *x[TT], *xs[TT];
-      int m[TT];
-      f32x4 acc[TT];
+      // this thread's pieces: rows, and bytes in a step
+      const uint8_t *xp[T::nx], *ap[T::na];
+      int xo[T::nx], ao[T::na];
 #pragma unroll
-      for (int j = 0; j < TT; ++j) {
-        m[j] = m0 + list[min(t0 + 16 * j + c, tokens - 1)];
-        x[j] = s.x + r * s.x_rank + m[j] * s.x_stride;
-        xs[j] = s.xs + r * s.xs_rank + m[j] * s.xs_stride;
-        acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int i = 0; i < T::nx; ++i) {
+        const int at = i * kBlock + tid, row = at / T::XC;
+        xp[i] = s.x + r * s.x_rank + (m0 + list[min(t0 + row, tokens - 1)]) * s.x_stride;
+        xo[i] = place<T::XC>(row, at % T::XC) * 16;
       }
-      auto load = [&](int st, TokenStep<XF, TT>& f) {
-        const int at = st * 128 + 32 * g;
-        constexpr int per = 128 / elem_bits<XF>();
-        const bool whole = st * 128 + 128 <= s.K;
 #pragma unroll
-        for (int j = 0; j < TT; ++j) {
-          if (TT > 1 && j >= tiles) continue;
+      for (int i = 0; i < T::na; ++i) {
+        const int at = i * kBlock + tid, row = at / T::AC;
+        ap[i] = s.a + r * s.a_rank + which * s.a_adapter + min(j0 + row, s.rank - 1) * s.a_stride;
+        ao[i] = place<T::AC>(row, at % T::AC) * 16;
+      }
+      const int m = m0 + list[min(t0 + 16 * wave + c, tokens - 1)];
+      const uint8_t* xs = s.xs + r * s.xs_rank + m * s.xs_stride;
+      // rows' last pieces, which are read again in the place of those past them
+      const int x_last = (s.K * elem_bits<XF>() + 127) / 128 * 16 - 16, a_last = (s.K + 7) / 8 * 16 - 16;
+      auto load = [&](int k, int buf) {
+        uint8_t* at = smem + buf * T::stage;
+        const int st = st0 + k;
 #pragma unroll
-          for (int q = 0; q < row_pieces<XF>(); ++q) {
-            f.x[j][q] = u32x4{0u, 0u, 0u, 0u};
-            if (whole || at + q * per < s.K) f.x[j][q] = ldg16(x[j] + (int64_t)(at + q * per) * elem_bits<XF>() / 8);
-          }
-          f.s[j] = 127;
-          if constexpr (is_mx_format(XF)) {
-            if (whole || at < s.K) f.s[j] = xs[j][at / 32];
-          }
+        for (int i = 0; i < T::nx; ++i)
+          load_to_lds(xp[i] + min(st * T::XB + xo[i], x_last), at + (i * kBlock + wave * kWave) * 16);
+#pragma unroll
+        for (int i = 0; i < T::na; ++i)
+          load_to_lds(ap[i] + min(st * 256 + ao[i], a_last), at + kTurn * T::XB + (i * kBlock + wave * kWave) * 16);
+        if constexpr (is_mx_format(XF)) {                  // 4 scales of each of the wave's tokens
+          typedef __attribute__((address_space(3))) void lds_void;
+          typedef const __attribute__((address_space(1))) void global_void;
+          uint8_t* to = at + kTurn * T::XB + NR * 16 * T::AC * 16 + wave * 256;
+          __builtin_amdgcn_global_load_lds((global_void*)(xs + min(4 * st, (s.nb - 1) / 4 * 4)), (lds_void*)to, 4, 0, 0);
+        }
+      };
+      f32x4 acc[NR];
+#pragma unroll
+      for (int i = 0; i < NR; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      const bool idle = t0 + 16 * wave >= tokens;
+      auto compute = [&](int k, int buf) {
+        const uint8_t* at = smem + buf * T::stage;
+        const int st = st0 + k, first = st * 128 + 32 * g, row = 16 * wave + c;
+        const bool cut = st * 128 + 128 > s.K;             // K ends in this step: zeros behind it
+        u32x4 x[row_pieces<XF>()];
+#pragma unroll
+        for (int q = 0; q < row_pieces<XF>(); ++q) {
+          x[q] = *reinterpret_cast<const u32x4*>(at + row * T::XB + place<T::XC>(row, row_pieces<XF>() * g + q) * 16);
+          if (cut) x[q] = keep_inputs<XF>(x[q], first + q * (128 / elem_bits<XF>()), s.K);
+        }
+        uint32_t sc = 127;
+        if constexpr (is_mx_format(XF)) {
+          sc = at[kTurn * T::XB + NR * 16 * T::AC * 16 + wave * 256 + c * 4 + g];
+          if (cut && first >= s.K) sc = 127;
         }
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          f.a[u] = u32x4{0u, 0u, 0u, 0u};
-          if (whole || at + 8 * u < s.K) f.a[u] = ldg16(a + (int64_t)(at + 8 * u) * 2);
+          const bf16x8 v = __builtin_bit_cast(bf16x8, token_operand<XF>(x, sc, u));
+#pragma unroll
+          for (int i = 0; i < NR; ++i) {
+            u32x4 w = *reinterpret_cast<const u32x4*>(at + kTurn * T::XB + (16 * i + c) * 256 +
+                                                      place<T::AC>(16 * i + c, 4 * g + u) * 16);
+            if (cut) w = keep_inputs<AR_BF16>(w, first + 8 * u, s.K);
+            acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w), v, acc[i], 0, 0, 0);
+          }
         }
       };
-      // a step that K ends in has zeros behind it
-      auto keep = [&](int st, TokenStep<XF, TT>& f) {
-        const int at = st * 128 + 32 * g;
-        constexpr int per = 128 / elem_bits<XF>();
-        if (st * 128 + 128 <= s.K) return;
+      constexpr int behind = (NS - 2) * T::loads;
+      constexpr int wait_behind = 0x0070 | (behind & 15) | (behind >> 4) << 14;
+      static_assert(behind < 64, "loads on their way that a wait can name");
 #pragma unroll
-        for (int u = 0; u < 4; ++u) f.a[u] = keep_inputs<AR_BF16>(f.a[u], at + 8 * u, s.K);
-#pragma unroll
-        for (int j = 0; j < TT; ++j)
-#pragma unroll
-          for (int q = 0; q < row_pieces<XF>(); ++q) f.x[j][q] = keep_inputs<XF>(f.x[j][q], at + q * per, s.K);
-      };
-      auto multiply = [&](const TokenStep<XF, TT>& f) {
-#pragma unroll
-        for (int j = 0; j < TT; ++j) {
-          if (TT > 1 && j >= tiles) continue;
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-            acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                __builtin_bit_cast(bf16x8, f.a[u]), __builtin_bit_cast(bf16x8, token_operand<XF>(f.x[j], f.s[j], u)),
-                acc[j], 0, 0, 0);
-        }
-      };
-      if (st0 < st1) {
-        TokenStep<XF, TT> cur;
-        int st = st0;
-        load(st, cur);
-        for (; st + WK < st1; st += WK) {                  // the next one is on its way
-          TokenStep<XF, TT> next;
-          load(st + WK, next);
-          multiply(cur);                                   // never the last step
-          cur = next;
-        }
-        keep(st, cur);
-        multiply(cur);
+      for (int k = 0; k < NS - 1; ++k)
+        if (k < n) load(k, k);
+      for (int k = 0, buf = 0; k < n; ++k) {
+        // step k has arrived when at most the steps after it are on their way
+        if (NS > 2 && k + NS - 2 < n) __builtin_amdgcn_s_waitcnt(wait_behind);
+        else __builtin_amdgcn_s_waitcnt(0x0070);
+        barrier_only();                                    // and the buffer of step k - 1 is left
+        if (k + NS - 1 < n) load(k + NS - 1, buf == 0 ? NS - 1 : buf - 1);
+        if (!idle) compute(k, buf);
+        if (++buf == NS) buf = 0;
       }
-      if constexpr (WK > 1) {
+      const int token = t0 + 16 * wave + c;
 #pragma unroll
-        for (int j = 0; j < TT; ++j) part[(wave * TT + j) * kWave + lane] = acc[j];
-        __syncthreads();
-      }
-#pragma unroll
-      for (int j = 0; j < TT; ++j) {
-        if (j % WK != wk || t0 + 16 * j + c >= tokens || j0 >= s.rank) continue;
-        f32x4 v = acc[j];
-        if constexpr (WK > 1) {
-          v = part[(wr * TT + j) * kWave + lane];
-#pragma unroll
-          for (int w = 1; w < WK; ++w) v += part[((w * WR + wr) * TT + j) * kWave + lane];
-        }
-        v *= scale;
-        if constexpr (XF == AR_E4M3_ROW) v *= *reinterpret_cast<const float*>(xs[j]);
-        const int d = j0 + 4 * g;
+      for (int i = 0; i < NR; ++i) {
+        if (token >= tokens || j0 + 16 * i >= s.rank) continue;
+        f32x4 v = acc[i] * scale;
+        if constexpr (XF == AR_E4M3_ROW) v *= *reinterpret_cast<const float*>(xs);
+        const int d = j0 + 16 * i + 4 * g;
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = d + e < s.rank ? v[e] : 0.0f;
-        *reinterpret_cast<f32x4*>(s.t + split * s.t_part + r * s.t_rank + m[j] * s.t_stride + d * 4) = v;
+        *reinterpret_cast<f32x4*>(s.t + split * s.t_part + r * s.t_rank + m * s.t_stride + d * 4) = v;
       }
-      if constexpr (WK > 1) __syncthreads();
+      __syncthreads();                                     // the next turn's first loads
     }
   }
 }
@@ -473,16 +480,16 @@ constexpr int kTokenBlocks = 1024;
 constexpr int64_t kLaneOutputs = 1 << 19;
 
 struct TokenPlan {
-  int32_t wr, splits, slots;         // wr 0: few tokens
+  int32_t nr, splits, slots;         // nr 0: few tokens
 };
 static TokenPlan plan_tokens(const ar_linear_params* p, const ar_adapter_params* q) {
   TokenPlan t{0, 1, 1};
   if (p->rows <= kFewTokens ||
       (p->rows <= 1024 && p->rows * t_ranks(p, q) * p->inputs * q->rank <= kFewProducts))
     return t;
-  t.wr = q->rank <= 16 ? 1 : (q->rank <= 32 ? 2 : 4);
-  const int64_t blocks = t_ranks(p, q) * ceil_div64(p->rows, kTokenGroup) * ceil_div64(q->rank, 16 * t.wr);
-  const int64_t steps = ceil_div64(p->inputs, 128 * (4 / t.wr));
+  t.nr = q->rank <= 16 ? 1 : (q->rank <= 32 ? 2 : 4);
+  const int64_t blocks = t_ranks(p, q) * ceil_div64(p->rows, kTokenGroup) * ceil_div64(q->rank, 16 * t.nr);
+  const int64_t steps = ceil_div64(p->inputs, 256);        // two steps each at least
   while (t.splits < 8 && 2 * t.splits <= steps && blocks * t.splits < kTokenBlocks) t.splits *= 2;
   const int64_t group = p->rows < kTokenGroup ? p->rows : kTokenGroup;
   const int64_t turns = group < q->adapters + 4 ? group : q->adapters + 4;
@@ -546,13 +553,12 @@ static hipError_t launch_delta(const Adapters& ad, const MxLinArgs& a, int nrank
   return hipSuccess;
 }
 
-template <int XF, int WR, int WK, int TT>
+template <int XF, int NR>
 static hipError_t launch_tokens(const TokenArgs& a0, int ranks, hipStream_t s) {
   TokenArgs a = a0;
-  constexpr int W = WR * WK;
-  a.r_groups = (a.rank + 16 * WR - 1) / (16 * WR);
+  a.r_groups = (a.rank + 16 * NR - 1) / (16 * NR);
   const int64_t each = (int64_t)ranks * a.r_groups * a.slots * a.splits;
-  const int64_t most = most_blocks(kWave * W) / each * kTokenGroup;
+  const int64_t most = most_blocks(kBlock) / each * kTokenGroup;
   for (int64_t m = 0; m < a0.M; m += most) {
     a.M = (int32_t)(a0.M - m < most ? a0.M - m : most);
     a.m_groups = (a.M + kTokenGroup - 1) / kTokenGroup;
@@ -560,8 +566,8 @@ static hipError_t launch_tokens(const TokenArgs& a0, int ranks, hipStream_t s) {
     if (a0.xs) a.xs = a0.xs + m * a0.xs_stride;
     a.index = a0.index + m;
     a.t = a0.t + m * a0.t_stride;
-    const hipError_t e = launch(k_adapter_tokens<XF, WR, WK, TT>, dim3((unsigned)(each * a.m_groups)),
-                                dim3(kWave * W), s, a);
+    const hipError_t e = launch(k_adapter_tokens<XF, NR>, dim3((unsigned)(each * a.m_groups)),
+                                dim3(kBlock), s, a);
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
@@ -579,10 +585,10 @@ static hipError_t launch_few_tokens(const TokenArgs& a0, int ranks, hipStream_t 
 
 template <int XF>
 static hipError_t launch_tokens_x(const TokenArgs& a, const TokenPlan& t, int ranks, hipStream_t s) {
-  if (t.wr == 0) return launch_few_tokens<XF>(a, ranks, s);
-  if (t.wr == 1) return launch_tokens<XF, 1, 4, 4>(a, ranks, s);
-  if (t.wr == 2) return launch_tokens<XF, 2, 2, 4>(a, ranks, s);
-  return launch_tokens<XF, 4, 1, 4>(a, ranks, s);
+  if (t.nr == 0) return launch_few_tokens<XF>(a, ranks, s);
+  if (t.nr == 1) return launch_tokens<XF, 1>(a, ranks, s);
+  if (t.nr == 2) return launch_tokens<XF, 2>(a, ranks, s);
+  return launch_tokens<XF, 4>(a, ranks, s);
 }
 
 static hipError_t launch_tokens_any(const TokenArgs& a, const TokenPlan& t, int xf, int ranks, hipStream_t s) {
@@ -638,6 +644,7 @@ int ar_mx4_linear_adapters(const ar_linear_params* p, const ar_adapter_params* q
   t.t_part = ranks * p->rows * t.t_stride;
   t.M = a.M;
   t.K = a.K;
+  t.nb = a.nb;
   t.splits = plan.splits;
   t.slots = plan.slots;
   t.count = q->adapters;
