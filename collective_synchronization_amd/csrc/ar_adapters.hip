@@ -165,6 +165,7 @@ __global__ __launch_bounds__(kBlock) void k_adapter_few_tokens(TokenArgs s) {
 }
 
 constexpr int kTokenGroup = 256;
+constexpr int kTokenParts = 16;                            // most workgroups that share K
 constexpr int kTurn = 64;                                  // tokens of a workgroup's turn
 
 // Parts of t for up to 64 tokens of one adapter, in 16 * NR of its dimensions, over
@@ -184,7 +185,7 @@ struct TokenTile {
   static constexpr int nx = kTurn * XC / kBlock, na = NR * 16 * AC / kBlock;
   static constexpr int scales = is_mx_format(XF) ? kWavesPerBlock * 256 : 0;
   static constexpr int stage = kTurn * XB + NR * 16 * AC * 16 + scales;
-  static constexpr int NS = 3 * stage <= 80 * 1024 ? 3 : 2;
+  static constexpr int NS = 3 * stage <= 80 * 1024 ? 3 : 2;   // two workgroups to a CU, or more
   static constexpr int loads = nx + na + (is_mx_format(XF) ? 1 : 0);
   static_assert(kWavesPerBlock * 16 == kTurn, "a wave has 16 tokens");
 };
@@ -357,14 +358,14 @@ __global__ __launch_bounds__(kBlock) void k_adapter_sum(TokenSum s) {
   const int64_t at = (int64_t)blockIdx.x * kBlock + threadIdx.x;
   if (at >= s.pieces) return;
   uint8_t* p = s.t + at * 16;
-  f32x4 v[8];
+  f32x4 v[kTokenParts];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
+  for (int k = 0; k < kTokenParts; ++k) {
     v[k] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     if (k < s.parts) v[k] = *reinterpret_cast<const f32x4*>(p + k * s.part);
   }
 #pragma unroll
-  for (int k = 1; k < 8; ++k)
+  for (int k = 1; k < kTokenParts; ++k)
     if (k < s.parts) v[0] += v[k];
   *reinterpret_cast<f32x4*>(p) = v[0];
 }
@@ -470,8 +471,10 @@ static int t_ranks(const ar_linear_params* p, const ar_adapter_params* q) {
 
 static int64_t t_row_bytes(const ar_adapter_params* q) { return ceil_div64(q->rank, 16) * 16 * 4; }
 
-// Workgroups that share K, and those that share a group's adapters, for about
-// 1024 in all (of which many may have no turn).
+// Workgroups that share K (up to 128 in all), and those that share a group's
+// adapters, for about 1024 in all, of which many may have no turn: 4096 x 8192,
+// rank 64, one adapter for 512 tokens 21 us, rank 16 with 16 adapters in any order 23;
+// 512 tokens 4, 6.5 with half as many shares of K.
 constexpr int kTokenBlocks = 1024;
 
 // Outputs of all ranks up to which up to 16 dimensions of 16 tokens' adapters are
@@ -490,7 +493,7 @@ static TokenPlan plan_tokens(const ar_linear_params* p, const ar_adapter_params*
   t.nr = q->rank <= 16 ? 1 : (q->rank <= 32 ? 2 : 4);
   const int64_t blocks = t_ranks(p, q) * ceil_div64(p->rows, kTokenGroup) * ceil_div64(q->rank, 16 * t.nr);
   const int64_t steps = ceil_div64(p->inputs, 256);        // two steps each at least
-  while (t.splits < 8 && 2 * t.splits <= steps && blocks * t.splits < kTokenBlocks) t.splits *= 2;
+  while (t.splits < kTokenParts && 2 * t.splits <= steps && blocks * t.splits < 128) t.splits *= 2;
   const int64_t group = p->rows < kTokenGroup ? p->rows : kTokenGroup;
   const int64_t turns = group < q->adapters + 4 ? group : q->adapters + 4;
   while (t.slots < turns && blocks * t.splits * t.slots < kTokenBlocks) t.slots *= 2;
