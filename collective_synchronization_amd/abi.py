@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -200,8 +201,7 @@ _SIGS = {
                                 _vp, _i64, _vp], ctypes.c_int),
     "ar_adapter_work_bytes": ([ctypes.POINTER(ar_linear_params), ctypes.POINTER(ar_adapter_params)],
                               _i64),
-    "ar_cache_append": ([ctypes.POINTER(ar_kv_cache), _i64, _i32, _i32, _vp, _i64, _i64, _vp, _i64,
-                         _i64, _vp, _vp, _i64, _i64, _vp], ctypes.c_int),
+    "ar_cache_append": ([ctypes.POINTER(ar_kv_cache), ctypes.c_char_p, _vp], ctypes.c_int),
     "ar_prefix_attention": ([ctypes.POINTER(ar_attention_params), _vp, _i64, _vp], ctypes.c_int),
     "ar_prefix_attention_work_bytes": ([ctypes.POINTER(ar_attention_params)], _i64),
     "ar_sim_run": ([ctypes.POINTER(ar_sim_params), _vp], ctypes.c_int),
@@ -540,13 +540,18 @@ def cache_params(fmt, pages, page, kv_heads, dim, k, v, page_stride, token_strid
     return c
 
 
+# ar_append_params, packed for each call: without a kernel 2.3 us, against 3.6
+# with its 13 members as arguments of a ctypes function
+_append_params = struct.Struct("@qiiPqqPqqPPqq").pack
+
+
 def ar_cache_append(cache: ar_kv_cache, sequences, queries, fmt, k, k_stride, k_head_stride, v,
                     v_stride, v_head_stride, lengths, pages, pages_stride, max_pages,
                     stream=None) -> None:
     k, v, lengths, pages = _gpu_ptrs("ar_cache_append", k, v, lengths, pages)
-    _check(_lib.ar_cache_append(ctypes.byref(cache), sequences, queries, format_id(fmt), k, k_stride,
-                                k_head_stride, v, v_stride, v_head_stride, lengths, pages,
-                                pages_stride, max_pages, _stream(stream)), "ar_cache_append")
+    p = _append_params(sequences, queries, format_id(fmt), k or 0, k_stride, k_head_stride, v or 0,
+                       v_stride, v_head_stride, lengths or 0, pages or 0, pages_stride, max_pages)
+    _check(_lib.ar_cache_append(ctypes.byref(cache), p, _stream(stream)), "ar_cache_append")
 
 
 def attention_params(cache: ar_kv_cache, sequences, queries, heads, scale, fmt, q, q_stride,

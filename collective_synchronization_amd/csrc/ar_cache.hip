@@ -80,52 +80,49 @@ using namespace ar;
 
 extern "C" {
 
-int ar_cache_append(const ar_kv_cache* cache, int64_t sequences, int32_t queries, int32_t format, const void* k,
-                    int64_t k_stride, int64_t k_head_stride, const void* v, int64_t v_stride, int64_t v_head_stride,
-                    const int32_t* lengths, const int32_t* pages, int64_t pages_stride, int64_t max_pages,
-                    void* stream) {
-  if (!cache || sequences < 0 || queries < 0 || max_pages < 0) return AR_EINVAL;
+int ar_cache_append(const ar_kv_cache* cache, const ar_append_params* p, void* stream) {
+  if (!cache || !p || p->sequences < 0 || p->queries < 0 || p->max_pages < 0) return AR_EINVAL;
   int rc = check_cache(cache);
   if (rc) return rc;
-  if (format != AR_BF16 && format != AR_F16) return AR_EINVAL;
-  if (cache->format != AR_E4M3_ROW && cache->format != format) return AR_EINVAL;
-  if (sequences == 0 || queries == 0 || max_pages == 0 || cache->pages == 0) return AR_OK;
+  if (p->format != AR_BF16 && p->format != AR_F16) return AR_EINVAL;
+  if (cache->format != AR_E4M3_ROW && cache->format != p->format) return AR_EINVAL;
+  if (p->sequences == 0 || p->queries == 0 || p->max_pages == 0 || cache->pages == 0) return AR_OK;
   rc = check_cache_rows(cache);
   if (rc) return rc;
   const int64_t most = int64_t(1) << 30;
-  if (!k || !v || !lengths || !pages) return AR_EINVAL;
-  if (sequences > 1 && pages_stride < max_pages) return AR_EINVAL;
-  if (k_stride < 0 || k_head_stride < 0 || v_stride < 0 || v_head_stride < 0) return AR_EINVAL;
-  if (sequences >= most || max_pages >= most || pages_stride >= most || k_stride >= most || k_head_stride >= most ||
-      v_stride >= most || v_head_stride >= most)
+  if (!p->k || !p->v || !p->lengths || !p->pages) return AR_EINVAL;
+  if (p->sequences > 1 && p->pages_stride < p->max_pages) return AR_EINVAL;
+  if (p->k_stride < 0 || p->k_head_stride < 0 || p->v_stride < 0 || p->v_head_stride < 0) return AR_EINVAL;
+  if (p->sequences >= most || p->max_pages >= most || p->pages_stride >= most || p->k_stride >= most ||
+      p->k_head_stride >= most || p->v_stride >= most || p->v_head_stride >= most)
     return AR_ESIZE;
-  if (sequences * queries >= most || sequences * queries * cache->kv_heads >= most) return AR_ESIZE;
-  if (!aligned(k, 16) || !aligned(v, 16) || k_stride % 8 || k_head_stride % 8 || v_stride % 8 || v_head_stride % 8 ||
-      !aligned(lengths, 4) || !aligned(pages, 4))
+  if (p->sequences * p->queries >= most || p->sequences * p->queries * cache->kv_heads >= most) return AR_ESIZE;
+  if (!aligned(p->k, 16) || !aligned(p->v, 16) || p->k_stride % 8 || p->k_head_stride % 8 || p->v_stride % 8 ||
+      p->v_head_stride % 8 || !aligned(p->lengths, 4) || !aligned(p->pages, 4))
     return AR_EALIGN;
   AppendArgs a{};
   a.kv = cache_view(cache);
-  a.k = static_cast<const uint16_t*>(k);
-  a.v = static_cast<const uint16_t*>(v);
-  a.k_stride = k_stride;
-  a.k_head = k_head_stride;
-  a.v_stride = v_stride;
-  a.v_head = v_head_stride;
-  a.lengths = lengths;
-  a.tables = pages;
-  a.table_stride = pages_stride;
-  a.max_pages = (int32_t)max_pages;
-  a.queries = queries;
-  a.rows = sequences * queries * cache->kv_heads;
+  a.k = static_cast<const uint16_t*>(p->k);
+  a.v = static_cast<const uint16_t*>(p->v);
+  a.k_stride = p->k_stride;
+  a.k_head = p->k_head_stride;
+  a.v_stride = p->v_stride;
+  a.v_head = p->v_head_stride;
+  a.lengths = p->lengths;
+  a.tables = p->pages;
+  a.table_stride = p->pages_stride;
+  a.max_pages = (int32_t)p->max_pages;
+  a.queries = p->queries;
+  a.rows = p->sequences * p->queries * cache->kv_heads;
   a.heads = fast_div((uint32_t)cache->kv_heads);
-  a.steps = fast_div((uint32_t)queries);
+  a.steps = fast_div((uint32_t)p->queries);
   while ((8 << a.lanes_shift) < cache->dim) ++a.lanes_shift;
   const int64_t blocks = ceil_div64((2 * a.rows) << a.lanes_shift, kBlock);
   if (blocks > most_blocks(kBlock)) return AR_ESIZE;
   const dim3 grid((unsigned)blocks), block(kBlock);
   hipStream_t s = static_cast<hipStream_t>(stream);
   const bool c8 = cache->format == AR_E4M3_ROW;
-  if (format == AR_BF16)
+  if (p->format == AR_BF16)
     return map_hip(c8 ? launch(k_cache_append<AR_BF16, true>, grid, block, s, a)
                       : launch(k_cache_append<AR_BF16, false>, grid, block, s, a));
   return map_hip(c8 ? launch(k_cache_append<AR_F16, true>, grid, block, s, a)

@@ -571,6 +571,19 @@ typedef struct {
     int64_t scale_page_stride, scale_token_stride, scale_head_stride;
 } ar_kv_cache;
 
+typedef struct {
+    int64_t sequences;          /* >= 0 */
+    int32_t queries;            /* new tokens of each, >= 0 */
+    int32_t format;             /* of k and v */
+    const void* k;              /* row b*queries + i, head h: k + row*k_stride + h*k_head_stride */
+    int64_t k_stride, k_head_stride;
+    const void* v;
+    int64_t v_stride, v_head_stride;
+    const int32_t* lengths;     /* device int32[sequences] */
+    const int32_t* pages;       /* device: max_pages for each sequence */
+    int64_t pages_stride, max_pages;
+} ar_append_params;
+
 /*
  * ar_cache_append -- a step's keys and values into the cache: each of
  * `sequences` sequences has `queries` new tokens, and lengths[b] tokens with
@@ -580,21 +593,15 @@ typedef struct {
  *   format: of k and v: the cache's, or with an AR_E4M3_ROW cache AR_BF16 or
  *      AR_F16: s as above, every code the nearest to 448 v / max|v| (to v / s
  *      where s is 2^-126), which is v over s before its rounding.
- *   k, v: device, token rows at k + row*k_stride, head h's at h*k_head_stride
- *      after it, alignment as for rows of their format.
- *   lengths: device int32[sequences]; pages: device int32, max_pages for each
- *      sequence.  A token whose number is negative (a sequence shorter than
+ *   k, v: alignment as for rows of their format.
+ *   lengths, pages: a token whose number is negative (a sequence shorter than
  *      `queries`, or of negative length: one that is not there), or past the
  *      table's last page, or whose page is none of 0 .. cache->pages - 1, is
  *      not written.
  * No two tokens may have the same place.  AR_ESIZE: sizes or strides of 2^30
  * and more.
  */
-int ar_cache_append(const ar_kv_cache* cache, int64_t sequences, int32_t queries, int32_t format,
-                    const void* k, int64_t k_stride, int64_t k_head_stride,
-                    const void* v, int64_t v_stride, int64_t v_head_stride,
-                    const int32_t* lengths, const int32_t* pages, int64_t pages_stride,
-                    int64_t max_pages, void* stream);
+int ar_cache_append(const ar_kv_cache* cache, const ar_append_params* p, void* stream);
 
 typedef struct {
     ar_kv_cache cache;

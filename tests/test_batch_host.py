@@ -163,7 +163,9 @@ def test_append_refusals(kw, want):
 def test_append_of_nothing():
     for kw in (dict(sequences=0), dict(queries=0), dict(max_pages=0, pages=None), dict(cache=_cache(pages=0, k=None))):
         assert _append(**dict(dict(k=None), **kw)) == 0
-    assert abi.raw().ar_cache_append(None, 1, 1, 0, A, 8, 8, A, 8, 8, A, A, 1, 1, None) == -1
+    import ctypes
+    assert abi.raw().ar_cache_append(None, bytes(96), None) == -1
+    assert abi.raw().ar_cache_append(ctypes.byref(_cache()), None, None) == -1
 
 
 @pytest.mark.parametrize("kw,want", [
