@@ -2,10 +2,13 @@
 // low-rank adapters of many requests beside them (gfx950):
 //     y_r[m][n] = sum over k of x_r[m][k] w_r[n][k] + sum over j of t_r[m][j] b[n][j],
 //     t_r[m][j] = scale * sum over k of x_r[m][k] a[j][k],
-// a, b and scale those of token m's adapter.  Two launches: one for t, which is
-// small, and the linear layer's own, which adds the second product to its sums
-// before their one rounding, so that neither y nor what is added to it makes a
-// way through memory.
+// a, b and scale those of token m's adapter.  t is small and has a launch of its
+// own: k_adapter_few_tokens reads every token's rows of a for it alone, and
+// k_adapter_tokens (with k_adapter_sum) those of an adapter for all its tokens.  The
+// second product joins the layer's sums before their one rounding, so that y does
+// not make a way through memory for it: in the largest tiles through shared memory
+// (add_adapters), for 16 tokens and dimensions in the layer's waves (AdapterLanes),
+// else made ready in binary32 first (k_adapter_delta).
 #include "ar_mxlinear.h"
 
 namespace ar {
@@ -94,10 +97,13 @@ __device__ __forceinline__ void token8(const Token8<XF>& t, float (&v)[8]) {
   }
 }
 
-// t of one token, 4 dimensions a wave, for up to kFewTokens tokens: each has rows
-// of a to itself, so they are read as they are multiplied, in binary32, 512
-// elements of K at a time.  WK waves share K; without, a workgroup has 16
-// dimensions.  Bound by the loads' latency: index, then x and a, then the join.
+// t of one token, 4 dimensions a wave, for few tokens: each has rows of a to
+// itself, so they are read as they are multiplied, in binary32, 512 elements of K
+// at a time.  WK waves share K; without, a workgroup has 16 dimensions.  Bound by the
+// loads' latency: index, then x and a, then the join (1 to 2 us beside the launch for
+// 4 ranks of 16 tokens of 2048; in matrix instructions for 16 tokens at a time, with
+// 15 of them empty where each has its own adapter, 6).  Up to kFewTokens, and as
+// long as a is read no more than 64 MB in all.
 constexpr int kFewTokens = 32;
 constexpr int64_t kFewProducts = int64_t(1) << 25;
 template <int XF, int WK>
@@ -534,24 +540,32 @@ static hipError_t launch_delta(const Adapters& ad, const MxLinArgs& a, int nrank
   d.rank = ad.rank;
   d.ranks = ad.b_rank == 0 ? nranks : 1;
   d.n_blocks = (a.N + kBlock - 1) / kBlock;
+  // (at most 2^22 of them, so a launch takes 4 ranks' at least)
+  const int groups = nranks / d.ranks;
+  const int64_t at_once = most_blocks(kBlock) / d.n_blocks;
+  const int each = (int)(at_once < groups ? at_once : groups);
   // tokens of a workgroup: as many as leave 1024 workgroups, at most 16
-  const int64_t all = (int64_t)(nranks / d.ranks) * d.n_blocks;
+  const int64_t all = (int64_t)each * d.n_blocks;
   int64_t tokens = all * a.M / 1024;
   tokens = tokens < 1 ? 1 : (tokens > 16 ? 16 : tokens);
   d.tokens = (int32_t)tokens;
   const int64_t most = most_blocks(kBlock) / all * tokens;
-  for (int64_t m = 0; m < a.M; m += most) {
-    d.M = (int32_t)(a.M - m < most ? a.M - m : most);
-    d.m_blocks = (int32_t)ceil_div64(d.M, tokens);
-    d.index = ad.index + m;
-    d.t = reinterpret_cast<const float*>(ad.t + m * ad.t_stride);
-    d.delta = const_cast<float*>(ad.delta) + m * ad.delta_stride;
-    const dim3 grid((unsigned)(all * d.m_blocks)), block(kBlock);
-    const hipError_t e = ad.rank <= 16   ? launch(k_adapter_delta<1>, grid, block, s, d)
-                         : ad.rank <= 32 ? launch(k_adapter_delta<2>, grid, block, s, d)
-                         : ad.rank <= 64 ? launch(k_adapter_delta<4>, grid, block, s, d)
-                                         : launch(k_adapter_delta<8>, grid, block, s, d);
-    if (e != hipSuccess) return e;
+  for (int r = 0; r < groups; r += each) {
+    const int ranks = groups - r < each ? groups - r : each;
+    for (int64_t m = 0; m < a.M; m += most) {
+      d.M = (int32_t)(a.M - m < most ? a.M - m : most);
+      d.m_blocks = (int32_t)ceil_div64(d.M, tokens);
+      d.index = ad.index + m;
+      d.t = reinterpret_cast<const float*>(ad.t + r * ad.t_rank + m * ad.t_stride);
+      d.b = ad.b + r * ad.b_rank;
+      d.delta = const_cast<float*>(ad.delta) + r * ad.delta_rank + m * ad.delta_stride;
+      const dim3 grid((unsigned)((int64_t)ranks * d.n_blocks * d.m_blocks)), block(kBlock);
+      const hipError_t e = ad.rank <= 16   ? launch(k_adapter_delta<1>, grid, block, s, d)
+                           : ad.rank <= 32 ? launch(k_adapter_delta<2>, grid, block, s, d)
+                           : ad.rank <= 64 ? launch(k_adapter_delta<4>, grid, block, s, d)
+                                           : launch(k_adapter_delta<8>, grid, block, s, d);
+      if (e != hipSuccess) return e;
+    }
   }
   return hipSuccess;
 }
@@ -667,9 +681,8 @@ int ar_mx4_linear_adapters(const ar_linear_params* p, const ar_adapter_params* q
   hipError_t e = launch_tokens_any(t, plan, p->x_format, ranks, s);
   if (e == hipSuccess && plan.splits > 1) {
     const TokenSum sum{t.t, t.t_part, t.t_part / 16, plan.splits};
-    const int64_t blocks = ceil_div64(sum.pieces, kBlock);
-    if (blocks > most_blocks(kBlock)) return AR_ESIZE;
-    e = launch(k_adapter_sum, dim3((unsigned)blocks), dim3(kBlock), s, sum);
+    // (shares of K are for 2^15 tokens at most)
+    e = launch(k_adapter_sum, dim3((unsigned)ceil_div64(sum.pieces, kBlock)), dim3(kBlock), s, sum);
   }
   if (delta_bytes(p, q) > 0) {
     ad.delta = reinterpret_cast<const float*>(t.t + t_bytes(p, q));
