@@ -44,11 +44,7 @@ __device__ __forceinline__ u32x4 token_operand(const u32x4 (&x)[row_pieces<XF>()
     return __builtin_bit_cast(u32x4, weights_bf16(x[0][u], __uint_as_float(scale << 23)));
   } else {
     const float s = XF == AR_E4M3_MX ? __uint_as_float(scale << 23) : 1.0f;
-    const uint32_t lo = x[u >> 1][2 * (u & 1)], hi = x[u >> 1][2 * (u & 1) + 1];
-    return u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, s, false)),
-                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, s, true)),
-                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, s, false)),
-                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, s, true))};
+    return __builtin_bit_cast(u32x4, tokens_bf16(x[u >> 1][2 * (u & 1)], x[u >> 1][2 * (u & 1) + 1], s));
   }
 }
 

@@ -122,6 +122,22 @@ __device__ __forceinline__ u32x4 keep_weights(u32x4 v, int64_t at, int64_t K) {
   return keep_bits(v, (K - at) * 4);
 }
 
+// 8 e4m3 codes times a scale as bf16, without loss in its range.
+__device__ __forceinline__ bf16x8 tokens_bf16(uint32_t lo, uint32_t hi, float scale) {
+  const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false);
+  const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, true);
+  const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, false);
+  const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true);
+  return bf16x8{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
+}
+
+// Whether 8-bit tokens go through the bf16 instruction (as bf16, converted in
+// registers), which loses nothing: for binary32 outputs with adapters.
+template <int XF, int YF, class AD>
+constexpr bool exact8() {
+  return !is_same<AD, NoAdapters> && YF == AR_F32 && (XF == AR_E4M3_ROW || XF == AR_E4M3_MX);
+}
+
 // One lane's operands of a 512-element step: 4 blocks of K, one in each of 4
 // matrix instructions, and the row's 16 scales.
 template <int XF>
@@ -158,9 +174,10 @@ __device__ __forceinline__ void load_w(const uint8_t* row, const uint8_t* srow, 
 }
 
 // First element of piece q of instruction s in group g's operand of a step.
-template <int XF>
+template <int XF, bool EX = false>
 __device__ __forceinline__ int64_t input_at(int step, int s, int g, int q) {
-  if constexpr (XF == AR_E2M1_MX) return (int64_t)(16 * step + 4 * s + g) * 32;
+  if constexpr (EX) return (int64_t)(16 * step + 4 * s + g) * 32 + 16 * q;
+  else if constexpr (XF == AR_E2M1_MX) return (int64_t)(16 * step + 4 * s + g) * 32;
   else if constexpr (XF == AR_BF16) return (int64_t)(16 * step + 4 * s + g) * 32 + 8 * q;
   else return (int64_t)(16 * step + 4 * s) * 32 + 64 * q + 16 * g;
 }
@@ -172,7 +189,7 @@ __device__ __forceinline__ u32x4& input_piece(XFrag<XF>& f, int s, int q) {
   else return f.d[s][q];
 }
 
-template <int XF, bool TAIL>
+template <int XF, bool TAIL, bool EX>
 __device__ __forceinline__ void load_x(const uint8_t* row, const uint8_t* srow, int step, int g, int nb,
                                        int K, XFrag<XF>& f) {
   constexpr int per = 128 / elem_bits<XF>();               // elements of 16 bytes
@@ -180,20 +197,20 @@ __device__ __forceinline__ void load_x(const uint8_t* row, const uint8_t* srow, 
   for (int s = 0; s < 4; ++s)
 #pragma unroll
     for (int q = 0; q < input_pieces<XF>(); ++q) {
-      int64_t at = input_at<XF>(step, s, g, q);
+      int64_t at = input_at<XF, EX>(step, s, g, q);
       if (TAIL) at = min(at, (int64_t)((K - 1) / per) * per);
       input_piece<XF>(f, s, q) = ldg16(row + at * elem_bits<XF>() / 8);
     }
   if constexpr (is_mx_format(XF)) f.s = load_scales16<TAIL>(srow, 16 * step, nb);
 }
 
-template <int XF>
+template <int XF, bool EX>
 __device__ __forceinline__ void keep_step(int step, int g, int nb, int K, XFrag<XF>& f) {
 #pragma unroll
   for (int s = 0; s < 4; ++s)
 #pragma unroll
     for (int q = 0; q < input_pieces<XF>(); ++q)
-      input_piece<XF>(f, s, q) = keep_inputs<XF>(input_piece<XF>(f, s, q), input_at<XF>(step, s, g, q), K);
+      input_piece<XF>(f, s, q) = keep_inputs<XF>(input_piece<XF>(f, s, q), input_at<XF, EX>(step, s, g, q), K);
   if constexpr (is_mx_format(XF)) f.s = keep_scales(f.s, 16 * step, nb);
 }
 
@@ -213,11 +230,23 @@ __device__ __forceinline__ bf16x8 weights_bf16(uint32_t codes, float scale) {
 
 // Instruction S of a step; `shift` brings block 4S + g's scale to the lowest
 // byte, the one the instruction reads.
-template <int XF, int S>
+template <int XF, int S, bool EX>
 __device__ __forceinline__ f32x4 multiply(const WFrag& w, const XFrag<XF>& x, int shift, f32x4 acc) {
   constexpr u32x4 none = u32x4{0u, 0u, 0u, 0u};
   const uint32_t ws = w.s[S] >> shift;
-  if constexpr (XF == AR_BF16) {
+  if constexpr (EX) {
+    const float scale = __uint_as_float((ws & 0xFFu) << 23);
+    float xscale = 1.0f;
+    if constexpr (is_mx_format(XF)) xscale = __uint_as_float((x.s[S] >> shift & 0xFFu) << 23);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const u32x4 d = x.d[S][j / 2];
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+          weights_bf16(w.d[S][j], scale),
+          j % 2 ? tokens_bf16(d.z, d.w, xscale) : tokens_bf16(d.x, d.y, xscale), acc, 0, 0, 0);
+    }
+    return acc;
+  } else if constexpr (XF == AR_BF16) {
     const float scale = __uint_as_float((ws & 0xFFu) << 23);
 #pragma unroll
     for (int j = 0; j < 4; ++j)
@@ -419,6 +448,7 @@ __global__ __launch_bounds__(kWave * WN * WK) void k_mx_linear_rows(MxLinArgs a,
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wk = wave % WK, wn = wave / WK;
   const int c = lane & 15, g = lane >> 4, shift = 8 * g;
+  constexpr bool EX = exact8<XF, YF, AD>();
   int b = blockIdx.x;
   const int mg = b % a.m_groups;
   b /= a.m_groups;
@@ -451,11 +481,11 @@ __global__ __launch_bounds__(kWave * WN * WK) void k_mx_linear_rows(MxLinArgs a,
     if (st < full) {
 #pragma unroll
       for (int i = 0; i < NT; ++i) load_w<false>(wrow[i], wsrow[i], st, g, a.nb, f.w[i]);
-      load_x<XF, false>(xrow, xsrow, st, g, a.nb, a.K, f.x);
+      load_x<XF, false, EX>(xrow, xsrow, st, g, a.nb, a.K, f.x);
     } else {
 #pragma unroll
       for (int i = 0; i < NT; ++i) load_w<true>(wrow[i], wsrow[i], st, g, a.nb, f.w[i]);
-      load_x<XF, true>(xrow, xsrow, st, g, a.nb, a.K, f.x);
+      load_x<XF, true, EX>(xrow, xsrow, st, g, a.nb, a.K, f.x);
     }
   };
   auto keep = [&](int st, Step& f) {
@@ -463,23 +493,23 @@ __global__ __launch_bounds__(kWave * WN * WK) void k_mx_linear_rows(MxLinArgs a,
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       f.w[i].s = keep_scales(f.w[i].s, 16 * st, a.nb);
-      if constexpr (XF == AR_BF16) {
+      if constexpr (XF == AR_BF16 || EX) {
 #pragma unroll
         for (int q = 0; q < 4; ++q)
           f.w[i].d[q] = keep_weights(f.w[i].d[q], (int64_t)(16 * st + 4 * q + g) * 32, a.K);
       }
     }
-    keep_step<XF>(st, g, a.nb, a.K, f.x);
+    keep_step<XF, EX>(st, g, a.nb, a.K, f.x);
   };
   auto compute = [&](const Step& f) {
 #pragma unroll
-    for (int i = 0; i < NT; ++i) acc[i] = multiply<XF, 0>(f.w[i], f.x, shift, acc[i]);
+    for (int i = 0; i < NT; ++i) acc[i] = multiply<XF, 0, EX>(f.w[i], f.x, shift, acc[i]);
 #pragma unroll
-    for (int i = 0; i < NT; ++i) acc[i] = multiply<XF, 1>(f.w[i], f.x, shift, acc[i]);
+    for (int i = 0; i < NT; ++i) acc[i] = multiply<XF, 1, EX>(f.w[i], f.x, shift, acc[i]);
 #pragma unroll
-    for (int i = 0; i < NT; ++i) acc[i] = multiply<XF, 2>(f.w[i], f.x, shift, acc[i]);
+    for (int i = 0; i < NT; ++i) acc[i] = multiply<XF, 2, EX>(f.w[i], f.x, shift, acc[i]);
 #pragma unroll
-    for (int i = 0; i < NT; ++i) acc[i] = multiply<XF, 3>(f.w[i], f.x, shift, acc[i]);
+    for (int i = 0; i < NT; ++i) acc[i] = multiply<XF, 3, EX>(f.w[i], f.x, shift, acc[i]);
   };
   auto start = [&]() {                                     // beside the layer's first loads
     if constexpr (!is_same<AD, NoAdapters>) {
@@ -574,10 +604,10 @@ __device__ __forceinline__ void load_to_lds(const uint8_t* p, uint8_t* lds) {
   __builtin_amdgcn_global_load_lds((global_void*)p, (lds_void*)lds, 16, 0, 0);
 }
 
-template <int XF, int BK_>
+template <int XF, int BK_, bool EX>
 struct TileShape {
   static constexpr int BK = BK_;                           // elements of K a step
-  static constexpr int BI = XF == AR_BF16 ? 64 : 128;      // and of one round of instructions
+  static constexpr int BI = XF == AR_BF16 || EX ? 64 : 128; // and of one round of instructions
   static constexpr int rounds = BK / BI;
   static constexpr int XB = XF == AR_BF16 ? 2 * BK : (XF == AR_E2M1_MX ? BK / 2 : BK);  // bytes of an x row
   static constexpr int WB = BK / 2;                        // bytes of a weight row
@@ -603,11 +633,12 @@ __device__ __forceinline__ void barrier_only() {
 // KG groups of waves share a step's rounds among them and join their sums at
 // the end: more waves, and fewer steps one after the other, where there are few
 // tiles.
-template <int XF_, int YF_, int BK_, int BM_, int BN_, int WM_, int WN_, int NS_, int KG_ = 1>
+template <int XF_, int YF_, bool EX_, int BK_, int BM_, int BN_, int WM_, int WN_, int NS_, int KG_ = 1>
 struct Tile {
   static constexpr int XF = XF_, YF = YF_, BM = BM_, BN = BN_, WM = WM_, WN = WN_, NS = NS_,
                        KG = KG_;
-  using T = TileShape<XF, BK_>;
+  static constexpr bool EX = EX_;
+  using T = TileShape<XF, BK_, EX>;
   static constexpr int tile_waves = (BM / WM) * (BN / WN), waves = tile_waves * KG;
   static constexpr int threads = waves * kWave;
   static constexpr int xbytes = BM * T::XB, wbytes = BN * T::WB;
@@ -764,6 +795,7 @@ template <class G, class AD>
 __global__ __launch_bounds__(G::threads) void k_mx_linear_tiles(MxLinArgs a, AD ad) {
   using T = typename G::T;
   constexpr int XF = G::XF, YF = G::YF, BM = G::BM, BN = G::BN, WM = G::WM, WN = G::WN, NS = G::NS;
+  constexpr bool EX = G::EX;
   constexpr int TI = WN / 16, TJ = WM / 16;                // matrix tiles of a wave
   __shared__ __align__(256) uint8_t smem[G::lds];
   const int tid = threadIdx.x, lane = tid & 63;
@@ -839,7 +871,7 @@ __global__ __launch_bounds__(G::threads) void k_mx_linear_tiles(MxLinArgs a, AD 
       u32x4* p = reinterpret_cast<u32x4*>(at + slot * 16);
       *p = keep_inputs<XF>(*p, first * 8 / elem_bits<XF>(), a.K);
     }
-    if constexpr (XF == AR_BF16) {
+    if constexpr (XF == AR_BF16 || EX) {
 #pragma unroll
       for (int i = 0; i < (G::pw + G::threads - 1) / G::threads; ++i) {
         const int slot = i * G::threads + tid;
@@ -906,11 +938,11 @@ __global__ __launch_bounds__(G::threads) void k_mx_linear_tiles(MxLinArgs a, AD 
       const int row = wj * WM + j * 16 + c;
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
-        if (XF == AR_E2M1_MX && q == 1) continue;
+        if ((XF == AR_E2M1_MX || EX) && q == 1) continue;
         const int piece = h * (T::XC / T::rounds) + (XF == AR_BF16 ? 2 * g + q : 4 * q + g);
         f.d[j][q] = *reinterpret_cast<const u32x4*>(xs + row * T::XB + place<T::XC>(row, piece) * 16);
       }
-      if constexpr (is_mx_format(XF)) f.s[j] = (int)sc[(BN + row) * 16 + g];
+      if constexpr (is_mx_format(XF)) f.s[j] = (int)sc[(BN + row) * 16 + (EX ? g >> 1 : g)];
     }
   };
   auto read_weights = [&](int k, int h, int buf, int i, Weights& f) {
@@ -918,7 +950,7 @@ __global__ __launch_bounds__(G::threads) void k_mx_linear_tiles(MxLinArgs a, AD 
     const uint8_t* sc = scales_at(k, h);
     const int first = h * (T::WC / T::rounds);
     const int row = wi * WN + i * 16 + c;
-    if constexpr (XF == AR_BF16) {
+    if constexpr (XF == AR_BF16 || EX) {
       const u32x2 d = *reinterpret_cast<const u32x2*>(ws + row * T::WB +
                                                       place<T::WC>(row, first + (g >> 1)) * 16 + (g & 1) * 8);
       f.d.x = d.x;
@@ -930,7 +962,18 @@ __global__ __launch_bounds__(G::threads) void k_mx_linear_tiles(MxLinArgs a, AD 
     }
   };
   auto multiply_row = [&](int i, const Weights& w, const Tokens& x) {
-    if constexpr (XF == AR_BF16) {
+    if constexpr (EX) {
+      const float scale = __uint_as_float((uint32_t)w.s << 23);
+      const bf16x8 w0 = weights_bf16(w.d.x, scale), w1 = weights_bf16(w.d.y, scale);
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) {
+        float xscale = 1.0f;
+        if constexpr (is_mx_format(XF)) xscale = __uint_as_float((uint32_t)x.s[j] << 23);
+        const u32x4 d = x.d[j][0];
+        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w0, tokens_bf16(d.x, d.y, xscale), acc[i][j], 0, 0, 0);
+        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w1, tokens_bf16(d.z, d.w, xscale), acc[i][j], 0, 0, 0);
+      }
+    } else if constexpr (XF == AR_BF16) {
       const float scale = __uint_as_float((uint32_t)w.s << 23);
       const bf16x8 w0 = weights_bf16(w.d.x, scale), w1 = weights_bf16(w.d.y, scale);
 #pragma unroll
@@ -1222,15 +1265,18 @@ static hipError_t launch_linear(const MxLinArgs& a, const AD& ad, int nranks, hi
   auto tiles = [&](int bm, int bn) { return linear_tiles(a, nranks, bm, bn); };
   const bool many = a.M > 16 || (XF != AR_BF16 && a.M > 8 && tiles(32, 64) > 256);
   if (many && a.x_stride < (1 << 23) && a.w_stride < (1 << 23)) {
-    constexpr int K1 = XF == AR_BF16 ? 64 : 128;
+    constexpr bool EX = exact8<XF, YF, AD>();
+    constexpr int K1 = XF == AR_BF16 ? 64 : 128;           // of a step with all its waves
+    constexpr int KI = EX ? 64 : K1;                       // of a round for a group of them
     constexpr bool x4 = XF == AR_E2M1_MX;                  // small enough for steps of 256
-    if (a.M > 128 && tiles(256, 256) >= 256)
-      return launch_tiles<Tile<XF, YF, K1, 256, 256, 64, 128, 3>>(a, ad, nranks, s);
+    if constexpr (!EX)                                     // whose steps are two rounds
+      if (a.M > 128 && tiles(256, 256) >= 256)
+        return launch_tiles<Tile<XF, YF, EX, K1, 256, 256, 64, 128, 3>>(a, ad, nranks, s);
     if (a.M > 64 && tiles(128, 128) >= 256)
-      return launch_tiles<Tile<XF, YF, x4 ? 256 : K1, 128, 128, 64, 64, x4 ? 2 : 3>>(a, ad, nranks, s);
-    if (tiles(32, 64) <= 256) return launch_tiles<Tile<XF, YF, 4 * K1, 32, 64, 32, 16, 3, 4>>(a, ad, nranks, s);
-    if (a.M <= 32) return launch_tiles<Tile<XF, YF, K1, 32, 64, 32, 16, 5>>(a, ad, nranks, s);
-    return launch_tiles<Tile<XF, YF, 2 * K1, 64, 64, 32, 32, 3, 2>>(a, ad, nranks, s);
+      return launch_tiles<Tile<XF, YF, EX, x4 ? 256 : K1, 128, 128, 64, 64, x4 ? 2 : 3>>(a, ad, nranks, s);
+    if (tiles(32, 64) <= 256) return launch_tiles<Tile<XF, YF, EX, 4 * KI, 32, 64, 32, 16, 3, 4>>(a, ad, nranks, s);
+    if (a.M <= 32) return launch_tiles<Tile<XF, YF, EX, K1, 32, 64, 32, 16, 5>>(a, ad, nranks, s);
+    return launch_tiles<Tile<XF, YF, EX, 2 * KI, 64, 64, 32, 32, 3, 2>>(a, ad, nranks, s);
   }
   const int64_t steps = (a.nb + 15) / 16, wide = (int64_t)((a.N + 31) / 32) * nranks;
   if (wide * (steps < 8 ? steps : 8) >= kRowsWaves) return launch_rows<XF, YF, 2>(a, ad, nranks, s);

@@ -532,7 +532,9 @@ typedef struct {
  *      (AR_ESIZE); used for the time of the call, so calls that may overlap
  *      need each their own.
  * The values of x go as bf16 (8- and 4-bit ones without loss within its range)
- * times a into binary32 sums; t enters its second product as bf16 parts, off
+ * times a into binary32 sums, and so do 8-bit ones times the weights for AR_F32 y:
+ * nothing is lost between products there as ar_mx4_linear loses it, and y is not
+ * its y to the bit, for tokens without an adapter either; t enters its second product as bf16 parts, off
  * by at most 2^-15 of itself for AR_BF16 y and 2^-23 for AR_F32; so its products
  * with infinities in b may be NaN.  The order of every sum is fixed by the
  * sizes, so equal calls give equal bits, and a token's bits do not depend on the
