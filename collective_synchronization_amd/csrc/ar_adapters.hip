@@ -271,16 +271,18 @@ __global__ __launch_bounds__(kBlock) void k_adapter_tokens(TokenArgs s) {
       const int m = m0 + list[min(t0 + 16 * wave + c, tokens - 1)];
       const uint8_t* xs = s.xs + r * s.xs_rank + m * s.xs_stride;
       // rows' last pieces, which are read again in the place of those past them
-      const int x_last = (s.K * elem_bits<XF>() + 127) / 128 * 16 - 16, a_last = (s.K + 7) / 8 * 16 - 16;
+      // (offsets in a row pass 31 bits)
+      const uint32_t x_last = (uint32_t)(((int64_t)s.K * elem_bits<XF>() + 127) / 128 * 16 - 16);
+      const uint32_t a_last = (uint32_t)(((int64_t)s.K + 7) / 8 * 16 - 16);
       auto load = [&](int k, int buf) {
         uint8_t* at = smem + buf * T::stage;
         const int st = st0 + k;
 #pragma unroll
         for (int i = 0; i < T::nx; ++i)
-          load_to_lds(xp[i] + min(st * T::XB + xo[i], x_last), at + (i * kBlock + wave * kWave) * 16);
+          load_to_lds(xp[i] + min((uint32_t)st * T::XB + xo[i], x_last), at + (i * kBlock + wave * kWave) * 16);
 #pragma unroll
         for (int i = 0; i < T::na; ++i)
-          load_to_lds(ap[i] + min(st * 256 + ao[i], a_last), at + kTurn * T::XB + (i * kBlock + wave * kWave) * 16);
+          load_to_lds(ap[i] + min((uint32_t)st * 256 + ao[i], a_last), at + kTurn * T::XB + (i * kBlock + wave * kWave) * 16);
         if constexpr (is_mx_format(XF)) {                  // 4 scales of each of the wave's tokens
           typedef __attribute__((address_space(3))) void lds_void;
           typedef const __attribute__((address_space(1))) void global_void;

@@ -239,6 +239,36 @@ def test_far_adapters():
     c.check()
 
 
+def test_rows_of_more_than_2_31_bits():
+    """Inputs whose number times 16 passes 31 bits: of zeros but for a few places
+    near both ends and around 2^26 and 2^27 (the sums are exact)."""
+    m, n, k, rank = 33, 16, (1 << 27) + 40, 16
+    rng = np.random.default_rng(10)
+    at = np.array([0, 1, 511, (1 << 26) - 1, (1 << 26), (1 << 27) - 1, (1 << 27), k - 1])
+    x = torch.zeros((m, k), dtype=torch.bfloat16, device="cuda")
+    a = torch.zeros((rank, k), dtype=torch.bfloat16, device="cuda")
+    xv, av, bv = (rng.integers(-2, 3, s) / 2.0 for s in ((m, len(at)), (rank, len(at)), (n, rank)))
+    cols = torch.from_numpy(at).cuda()
+    x[:, cols] = torch.from_numpy(xv).to(torch.bfloat16).cuda()
+    a[:, cols] = torch.from_numpy(av).to(torch.bfloat16).cuda()
+    b = torch.from_numpy(bv).to(torch.bfloat16).cuda()
+    nb = -(-k // 32)
+    w = torch.zeros((n, 16 * nb), dtype=torch.uint8, device="cuda")
+    ws = torch.full((n, (nb + 15) // 16 * 16), 127, dtype=torch.uint8, device="cuda")
+    y = torch.full((m, n), -77.0, device="cuda")
+    index = torch.zeros(m, dtype=torch.int32, device="cuda")
+    index[5] = -1
+    lin = abi.linear_params(1, m, n, k, "bf16", x, x.stride(0), 0, None, 0, 0, w, w.stride(0), 0, ws, ws.stride(0), 0,
+                            "f32", y, y.stride(0), 0)
+    ad = abi.adapter_params(1, rank, index, None, a, a.stride(0), 0, 0, b, b.stride(0), 0, 0)
+    work = torch.full((abi.ar_adapter_work_bytes(lin, ad) // 4,), float("nan"), device="cuda")
+    abi.ar_mx4_linear_adapters(lin, ad, work)
+    torch.cuda.synchronize()
+    want = xv @ av.T @ bv.T
+    want[5] = 0.0
+    assert np.array_equal(y.double().cpu().numpy(), want)
+
+
 def test_two_streams_and_a_replayed_graph():
     one, two = Case(8, 4, 16, 500, 640, "mx8", "bf16", 6, 16, _index("each", 16, 6)), Case(9, 1, 90, 200, 300, "mx4", "f32", 3, 40, _index("mixed", 90, 3))
     p1, p2 = one.params(), two.params()
