@@ -816,6 +816,7 @@ struct Attn {
       }
       }
       compiler_barrier();                                  // before the buffer is filled again
+      if constexpr (!C8) __builtin_amdgcn_s_waitcnt(0xC07F);   // (lgkmcnt: loads to it keep no order with reads)
     }
     l = other_half_sum(other_row_sum(l));
     // the waves' sums, joined in shared memory
@@ -988,7 +989,7 @@ static int check_attention(const ar_attention_params* p) {
   if (p->reserved != 0 || p->sequences < 0 || p->queries < 1 || p->heads < 1 || p->prefix < 0 || p->max_pages < 0)
     return AR_EINVAL;
   if (p->format != AR_BF16 && p->format != AR_F16) return AR_EINVAL;
-  if (!(p->scale > 0.0f) || p->scale > 3.0e38f) return AR_EINVAL;
+  if (!(p->scale > 0.0f) || p->scale > 0x1p127f) return AR_EINVAL;   // times log2(e), finite
   int rc = check_cache(&p->cache);
   if (rc) return rc;
   if (p->heads % p->cache.kv_heads != 0) return AR_EINVAL;

@@ -536,7 +536,9 @@ typedef struct {
  * nothing is lost between products there as ar_mx4_linear loses it, and y is not
  * its y to the bit, for tokens without an adapter either; t enters its second product as bf16 parts, off
  * by at most 2^-15 of itself for AR_BF16 y and 2^-23 for AR_F32; so its products
- * with infinities in b may be NaN.  The order of every sum is fixed by the
+ * with infinities in b may be NaN.  Many tokens' t is added up from shares of K,
+ * scaled before that: an infinite scale, or one that takes a share past
+ * binary32, may give NaN.  The order of every sum is fixed by the
  * sizes, so equal calls give equal bits, and a token's bits do not depend on the
  * other tokens' adapters.  adapters, rank or inputs 0: ar_mx4_linear alone.
  * AR_ESIZE: b_stride of 2^23 and more, adapters whose offsets pass 2^60, and as
@@ -545,7 +547,7 @@ typedef struct {
 int ar_mx4_linear_adapters(const ar_linear_params* p, const ar_adapter_params* q, void* work,
                            int64_t work_bytes, void* stream);
 
-/* Bytes of its work buffer, by sizes, strides and y_format; < 0 on bad parameters. */
+/* Bytes of its work buffer, by sizes, strides and formats; < 0 on bad parameters. */
 int64_t ar_adapter_work_bytes(const ar_linear_params* p, const ar_adapter_params* q);
 
 /*
@@ -601,7 +603,7 @@ typedef struct {
  *      table's last page, or whose page is none of 0 .. cache->pages - 1, is
  *      not written.
  * No two tokens may have the same place.  AR_ESIZE: sizes or strides of 2^30
- * and more.
+ * and more, and 2^34 and more values of k, its rows taken up to a power of two.
  */
 int ar_cache_append(const ar_kv_cache* cache, const ar_append_params* p, void* stream);
 
@@ -610,7 +612,7 @@ typedef struct {
     int64_t sequences;          /* >= 0 */
     int32_t queries;            /* tokens of each, its last ones; >= 1 */
     int32_t heads;              /* a multiple of cache.kv_heads */
-    float scale;                /* of the scores; > 0, finite */
+    float scale;                /* of the scores; > 0, at most 2^127 */
     int32_t format;             /* of q and out: AR_BF16 or AR_F16 */
     const void* q;              /* row b*queries + i, head h: q + row*q_stride + h*q_head_stride */
     int64_t q_stride, q_head_stride;

@@ -185,6 +185,11 @@ def test_attention_refusals(kw, want):
     assert _attend(**kw) == want
 
 
+def test_attention_scale_is_finite_in_units_of_log2():
+    assert _attend(scale=2.0 ** 127, sequences=0) == 0
+    assert _attend(scale=2.4e38, sequences=0) == -1
+
+
 def test_attention_refuses_null_and_reserved():
     raw = abi.raw()
     assert raw.ar_prefix_attention(None, A, 1 << 30, None) == -1
