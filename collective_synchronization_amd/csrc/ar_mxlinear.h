@@ -467,8 +467,6 @@ __global__ __launch_bounds__(kWave * WN * WK) void k_mx_linear_rows(MxLinArgs a,
   // this wave's output tiles: all, or one of those that the group shares
   constexpr int own = WK == 1 ? NT : 1;
   AdapterLanes<own, 1, true> tiles;
-  if constexpr (!is_same<AD, NoAdapters>) {
-  }
   f32x4 acc[NT];
 #pragma unroll
   for (int i = 0; i < NT; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
