@@ -663,34 +663,46 @@ struct Tile {
   static_assert((NS - 2) * (nx + nw) < 64, "loads on their way that a wait can name");
 };
 
-// What adapters add to a workgroup's BM tokens by BN outputs: one adapter after
-// the other, for the tokens that have it, so that one's infinities stay with its
-// own tokens (those of a request stand together, so most often there are one or
-// two).  The layer's operands are done with, so t and the adapter's rows of b
-// go through shared memory, 32 dimensions at a time, the next adapter's rows on
-// their way in registers.  t's values go as 2 bf16 parts for bf16 outputs, as 3,
-// which is all of them, for binary32 ones.  4096 x 8192 x 8192, 8-bit tokens, 195
-// us without adapters: 8 requests with one of rank 16 each 224, of rank 64 254 (of
-// them 40 for t), 16 adapters of rank 16 in any order 326.
+// Whether one of two bf16 values is an infinity or a NaN.
+__device__ __forceinline__ bool bf16_odd(uint32_t v) {
+  return (v & 0x7F80u) == 0x7F80u || (v & 0x7F800000u) == 0x7F800000u;
+}
+
+// What adapters add to a workgroup's BM tokens by BN outputs, 64 outputs of a wave
+// at a time: one adapter after the other, for the tokens that have it (those of a
+// request stand together, so most often there are one or two), and two at a time
+// where their dimensions fit into one matrix instruction.  The layer's operands are
+// done with, so t and the adapter's rows of b go through shared memory, 32 dimensions
+// at a time, the next adapter's rows on their way in registers.  Tokens with other
+// adapters have zeros for t there, so their sums stay as they are (but for a zero's
+// sign); where rows of b have infinities or NaNs, which zeros would make NaN, the sums
+// are taken for their own tokens alone.
+// t's values go as 2 bf16 parts for bf16 outputs, as 3, which is all of them, for
+// binary32 ones.
 template <class G, class Acc>
 __device__ __forceinline__ void add_adapters(const Adapters& ad, const MxLinArgs& a, int r, int m0, int n0, int wm,
                                              int wn, uint8_t* smem, Acc acc) {
   constexpr int P = G::YF == AR_F32 ? 3 : 2, TI = G::WN / 16, TJ = G::WM / 16, threads = G::threads;
   constexpr int TS = 64 * P + 16, BS = 64 + 16;            // 16 rows' reads meet different banks
-  constexpr int pieces = G::BN * 4 / threads, sets = G::BM / kWave;
-  static_assert(G::KG == 1 && TI % 4 == 0 && G::BM % kWave == 0 && G::BN * 4 % threads == 0, "");
-  static_assert(G::BM * (4 + TS) + 2 * G::BN * BS <= G::lds, "room for t and b");
+  constexpr int HB = G::BN / (TI / 4);                     // rows of b at a time: 64 of every wave's
+  constexpr int pieces = HB * 4 / threads, sets = G::BM / kWave;
+  static_assert(G::KG == 1 && TI % 4 == 0 && G::BM % kWave == 0 && HB * 4 % threads == 0, "");
+  static_assert(G::BM * (4 + TS) + 2 * HB * BS + 8 <= G::lds, "room for t and b");
   const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, g = lane >> 4;
   int* ids = reinterpret_cast<int*>(smem);
   uint8_t *ts = smem + G::BM * 4, *bs = ts + G::BM * TS;
+  int* odd = reinterpret_cast<int*>(bs + 2 * HB * BS);   // the last turn whose rows were odd, of each buffer
   __syncthreads();
   for (int i = tid; i < G::BM; i += threads) {
     const int which = m0 + i < a.M ? ad.index[m0 + i] : -1;
     ids[i] = (uint32_t)which < (uint32_t)ad.count ? which : -1;
   }
+  if (tid < 2) odd[tid] = -1;
   __syncthreads();
-  int mine[sets];
+  int mine[sets], of[TJ];            // adapters of the workgroup's tokens, and of this lane's
   uint64_t all[sets], left[sets], any = 0;
+#pragma unroll
+  for (int j = 0; j < TJ; ++j) of[j] = ids[wm + 16 * j + c];
 #pragma unroll
   for (int k = 0; k < sets; ++k) {
     mine[k] = ids[64 * k + lane];
@@ -707,22 +719,11 @@ __device__ __forceinline__ void add_adapters(const Adapters& ad, const MxLinArgs
     return which;
   };
   if (any == 0) return;
+  const bool two = ad.rank <= 16;                          // adapters at a time: dimensions 16 on are the second one's
+  int turn = 0;
   for (int q = 0; q < ad.rank; q += 32) {
-    u32x4 w[pieces];
-    auto load_rows = [&](int which) {
-      const uint8_t* b = ad.b + r * ad.b_rank + which * ad.b_adapter;
-#pragma unroll
-      for (int i = 0; i < pieces; ++i) {
-        const int s = i * threads + tid;
-        w[i] = load_b8(b + min(n0 + s / 4, a.N - 1) * ad.b_stride, q + 8 * (s % 4), ad.rank);
-      }
-    };
-#pragma unroll
-    for (int k = 0; k < sets; ++k) left[k] = all[k];
-    int which = next();
-    load_rows(which);
     for (int s = tid; s < G::BM * 4; s += threads) {
-      const int row = s / 4, at = q + 8 * (s % 4);
+      const int row = s / 4, at = two ? 8 * (s % 2) : q + 8 * (s % 4);
       f32x4 v[2] = {f32x4{0.0f, 0.0f, 0.0f, 0.0f}, f32x4{0.0f, 0.0f, 0.0f, 0.0f}};
       if (ids[row] >= 0 && at < ad.rank) {
         const uint8_t* t = ad.t + r * ad.t_rank + (m0 + row) * ad.t_stride + at * 4;
@@ -741,49 +742,83 @@ __device__ __forceinline__ void add_adapters(const Adapters& ad, const MxLinArgs
 #pragma unroll
       for (int k = 0; k < P; ++k) *reinterpret_cast<u32x4*>(ts + row * TS + s % 4 * (16 * P) + 16 * k) = p[k];
     }
-    for (int buf = 0; which >= 0; buf ^= 1) {
-      uint8_t* rows = bs + buf * G::BN * BS;
 #pragma unroll
-      for (int i = 0; i < pieces; ++i) {
-        const int s = i * threads + tid;
-        *reinterpret_cast<u32x4*>(rows + s / 4 * BS + s % 4 * 16) = keep_b8(w[i], q + 8 * (s % 4), ad.rank);
-      }
-      __syncthreads();                                     // the other buffer's readers are through, too
-      const int after = next();
-      if (after >= 0) load_rows(after);
-      // this wave's rows of b, 4 tiles of outputs at a time
+    for (int i0 = 0; i0 < TI; i0 += 4) {
+      int which[2];
+      u32x4 w[pieces];
+      auto load_rows = [&]() {
+        which[0] = next();
+        which[1] = two ? next() : which[0];
+        if (which[0] < 0) return;
 #pragma unroll
-      for (int i0 = 0; i0 < TI; i0 += 4) {
-        bf16x8 x[4];
+        for (int i = 0; i < pieces; ++i) {
+          const int s = i * threads + tid, row = s / 4, at = two ? 8 * (s % 2) : q + 8 * (s % 4);
+          const int n = n0 + row / 64 * G::WN + 16 * i0 + row % 64;
+          const uint8_t* b = ad.b + r * ad.b_rank + (s % 4 < 2 || which[1] < 0 ? which[0] : which[1]) * ad.b_adapter;
+          w[i] = load_b8(b + min(n, a.N - 1) * ad.b_stride, at, ad.rank);
+        }
+      };
+#pragma unroll
+      for (int k = 0; k < sets; ++k) left[k] = all[k];
+      load_rows();
+      while (which[0] >= 0) {
+        const int buf = turn & 1, now[2] = {which[0], which[1]};
+        uint8_t* rows = bs + buf * HB * BS;
+        bool some = false;
+#pragma unroll
+        for (int i = 0; i < pieces; ++i) {
+          const int s = i * threads + tid;
+          const u32x4 v = keep_b8(w[i], two ? 8 * (s % 2) : q + 8 * (s % 4), ad.rank);
+          some |= bf16_odd(v.x) || bf16_odd(v.y) || bf16_odd(v.z) || bf16_odd(v.w);
+          *reinterpret_cast<u32x4*>(rows + s / 4 * BS + s % 4 * 16) = v;
+        }
+        if (some) odd[buf] = turn;
+        __syncthreads();                                   // the other buffer's readers are through, too
+        load_rows();
+        const bool apart = odd[buf] == turn;
+        ++turn;
+        const int want = g < 2 ? now[0] : now[1];
+        u32x4 x[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          x[i] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(rows + (wn + 16 * (i0 + i) + c) * BS + g * 16));
+          x[i] = *reinterpret_cast<const u32x4*>(rows + (wn / G::WN * 64 + 16 * i + c) * BS + g * 16);
 #pragma unroll
         for (int j = 0; j < TJ; ++j) {
-          const bool take = ids[wm + 16 * j + c] == which;
+          const bool take = of[j] >= 0 && of[j] == want;
           if (!__any(take)) continue;
-          const bool each = __all(take);
           u32x4 t[P];
 #pragma unroll
-          for (int k = 0; k < P; ++k)
+          for (int k = 0; k < P; ++k) {
             t[k] = *reinterpret_cast<const u32x4*>(ts + (wm + 16 * j + c) * TS + g * (16 * P) + 16 * k);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            f32x4 v = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            for (int e = 0; e < 4; ++e) t[k][e] = take ? t[k][e] : 0u;
+          }
+          if (!apart) {
 #pragma unroll
             for (int k = 0; k < P; ++k)
-              v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[i], __builtin_bit_cast(bf16x8, t[k]), v, 0, 0, 0);
-            if (each) {
-              acc(i0 + i, j) += v;
-            } else {
 #pragma unroll
-              for (int e = 0; e < 4; ++e) acc(i0 + i, j)[e] += take ? v[e] : 0.0f;
+              for (int i = 0; i < 4; ++i)
+                acc(i0 + i, j) = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                    __builtin_bit_cast(bf16x8, x[i]), __builtin_bit_cast(bf16x8, t[k]), acc(i0 + i, j), 0, 0, 0);
+          } else {
+            for (int half = 0; half < (two ? 2 : 1); ++half) {
+              const bool part = !two || (g >= 2) == (half == 1), own = of[j] >= 0 && of[j] == now[half];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                f32x4 v = acc(i0 + i, j);
+#pragma unroll
+                for (int k = 0; k < P; ++k)
+                  v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                      __builtin_bit_cast(bf16x8, part ? x[i] : u32x4{0u, 0u, 0u, 0u}),
+                      __builtin_bit_cast(bf16x8, t[k]), v, 0, 0, 0);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc(i0 + i, j)[e] = own ? v[e] : acc(i0 + i, j)[e];
+              }
             }
           }
           __builtin_amdgcn_sched_barrier(0);               // one tile's operands at a time: the sums fill the registers
         }
       }
-      which = after;
     }
     __syncthreads();                                       // t may be written over
   }

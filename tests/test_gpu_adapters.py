@@ -223,6 +223,42 @@ def test_infinite_and_nan_adapters_stay_with_their_tokens(m):
     assert y[(kind == 0) | (kind == 3)].isfinite().all()
 
 
+@pytest.mark.parametrize("rank", [7, 16, 40])
+@pytest.mark.parametrize("ranks,m,n", [(16, 200, 2050), (8, 520, 2600)])       # tiles of 128 and 256
+def test_tokens_of_large_tiles_keep_to_themselves(ranks, m, n, rank):
+    """Neither a neighbour's adapter nor infinities and NaNs in it change a bit
+    of a token, with one and two adapters to a matrix instruction."""
+    c = Case(11, ranks, m, n, 96, "bf16", "f32", 5, rank, _index("mixed", m, 5, 3))
+    lin, ad = c.params()
+    abi.ar_mx4_linear(lin)
+    torch.cuda.synchronize()
+    alone = c.y.clone()
+    abi.ar_mx4_linear_adapters(lin, ad, c.work(lin, ad))
+    torch.cuda.synchronize()
+    c.check()
+    both = c.y.clone()
+    index = c.idx.clone()
+    none, other = (index < 0) | (index >= 5), (index != 1) & (index != 2)
+    assert torch.equal(both[:, none], alone[:, none])
+    c.ad[0, 1] = float("nan")
+    c.bd[0, 2, :, rank - 1] = float("inf")
+    c.bd[0, 2, 5] = float("nan")
+    abi.ar_mx4_linear_adapters(lin, ad, c.work(lin, ad))
+    torch.cuda.synchronize()
+    assert torch.equal(c.y[:, other], both[:, other])
+    assert c.y[0, index == 1, :n].isnan().all()          # a is a rank's own, b all ranks'
+    assert not c.y[:, index == 2, :n].isfinite().any()
+    c.idx[other] = -1
+    abi.ar_mx4_linear_adapters(lin, ad, c.work(lin, ad))
+    torch.cuda.synchronize()
+    assert torch.equal(c.y[:, other], alone[:, other])
+    c.idx.copy_(index)
+    c.idx[~other] = -1
+    abi.ar_mx4_linear_adapters(lin, ad, c.work(lin, ad))
+    torch.cuda.synchronize()
+    assert torch.equal(c.y[:, other], both[:, other])
+
+
 def test_far_adapters():
     """Adapters more than 2^31 elements apart from the first."""
     c = Case(7, 1, 6, 70, 200, "mx8", "bf16", 2, 16, [0, 1, 1, 0, 1, 0])
