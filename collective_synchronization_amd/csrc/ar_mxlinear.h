@@ -668,8 +668,7 @@ __device__ __forceinline__ bool bf16_odd(uint32_t v) {
   return (v & 0x7F80u) == 0x7F80u || (v & 0x7F800000u) == 0x7F800000u;
 }
 
-// What adapters add to a workgroup's BM tokens by BN outputs, 64 outputs of a wave
-// at a time: one adapter after the other, for the tokens that have it (those of a
+// What adapters add to a workgroup's BM tokens by BN outputs: one adapter after the other, for the tokens that have it (those of a
 // request stand together, so most often there are one or two), and two at a time
 // where their dimensions fit into one matrix instruction.  The layer's operands are
 // done with, so t and the adapter's rows of b go through shared memory, 32 dimensions
@@ -679,19 +678,24 @@ __device__ __forceinline__ bool bf16_odd(uint32_t v) {
 // are taken for their own tokens alone.
 // t's values go as 2 bf16 parts for bf16 outputs, as 3, which is all of them, for
 // binary32 ones.
+// Bound by its own chain of loads (index, t, rows) where there are few adapters, by
+// the products of all tiles of 16 tokens with every adapter that one of them has
+// where there are many: 4096 x 8192 x 8192, 8-bit tokens, 196 us without adapters, 8
+// requests with one of rank 16 each 219, of rank 64 238 (23 and 4 of them t), 16
+// adapters of rank 16 in any order 268.  Rows of three adapters on their way, and
+// t in registers, changed nothing.
 template <class G, class Acc>
 __device__ __forceinline__ void add_adapters(const Adapters& ad, const MxLinArgs& a, int r, int m0, int n0, int wm,
                                              int wn, uint8_t* smem, Acc acc) {
   constexpr int P = G::YF == AR_F32 ? 3 : 2, TI = G::WN / 16, TJ = G::WM / 16, threads = G::threads;
   constexpr int TS = 64 * P + 16, BS = 64 + 16;            // 16 rows' reads meet different banks
-  constexpr int HB = G::BN / (TI / 4);                     // rows of b at a time: 64 of every wave's
-  constexpr int pieces = HB * 4 / threads, sets = G::BM / kWave;
-  static_assert(G::KG == 1 && TI % 4 == 0 && G::BM % kWave == 0 && HB * 4 % threads == 0, "");
-  static_assert(G::BM * (4 + TS) + 2 * HB * BS + 8 <= G::lds, "room for t and b");
+  constexpr int pieces = G::BN * 4 / threads, sets = G::BM / kWave;
+  static_assert(G::KG == 1 && TI % 4 == 0 && G::BM % kWave == 0 && G::BN * 4 % threads == 0, "");
+  static_assert(G::BM * (4 + TS) + 2 * G::BN * BS + 8 <= G::lds, "room for t and b");
   const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, g = lane >> 4;
   int* ids = reinterpret_cast<int*>(smem);
   uint8_t *ts = smem + G::BM * 4, *bs = ts + G::BM * TS;
-  int* odd = reinterpret_cast<int*>(bs + 2 * HB * BS);   // the last turn whose rows were odd, of each buffer
+  int* odd = reinterpret_cast<int*>(bs + 2 * G::BN * BS);   // the last turn whose rows were odd, of each buffer
   __syncthreads();
   for (int i = tid; i < G::BM; i += threads) {
     const int which = m0 + i < a.M ? ad.index[m0 + i] : -1;
@@ -722,6 +726,22 @@ __device__ __forceinline__ void add_adapters(const Adapters& ad, const MxLinArgs
   const bool two = ad.rank <= 16;                          // adapters at a time: dimensions 16 on are the second one's
   int turn = 0;
   for (int q = 0; q < ad.rank; q += 32) {
+    int which[2];
+    u32x4 w[pieces];
+    auto load_rows = [&]() {
+      which[0] = next();
+      which[1] = two ? next() : which[0];
+      if (which[0] < 0) return;
+#pragma unroll
+      for (int i = 0; i < pieces; ++i) {
+        const int s = i * threads + tid, row = s / 4, at = two ? 8 * (s % 2) : q + 8 * (s % 4);
+        const uint8_t* b = ad.b + r * ad.b_rank + (s % 4 < 2 || which[1] < 0 ? which[0] : which[1]) * ad.b_adapter;
+        w[i] = load_b8(b + min(n0 + row, a.N - 1) * ad.b_stride, at, ad.rank);
+      }
+    };
+#pragma unroll
+    for (int k = 0; k < sets; ++k) left[k] = all[k];
+    load_rows();
     for (int s = tid; s < G::BM * 4; s += threads) {
       const int row = s / 4, at = two ? 8 * (s % 2) : q + 8 * (s % 4);
       f32x4 v[2] = {f32x4{0.0f, 0.0f, 0.0f, 0.0f}, f32x4{0.0f, 0.0f, 0.0f, 0.0f}};
@@ -742,46 +762,30 @@ __device__ __forceinline__ void add_adapters(const Adapters& ad, const MxLinArgs
 #pragma unroll
       for (int k = 0; k < P; ++k) *reinterpret_cast<u32x4*>(ts + row * TS + s % 4 * (16 * P) + 16 * k) = p[k];
     }
+    while (which[0] >= 0) {
+      const int buf = turn & 1, now[2] = {which[0], which[1]};
+      uint8_t* rows = bs + buf * G::BN * BS;
+      bool some = false;
 #pragma unroll
-    for (int i0 = 0; i0 < TI; i0 += 4) {
-      int which[2];
-      u32x4 w[pieces];
-      auto load_rows = [&]() {
-        which[0] = next();
-        which[1] = two ? next() : which[0];
-        if (which[0] < 0) return;
-#pragma unroll
-        for (int i = 0; i < pieces; ++i) {
-          const int s = i * threads + tid, row = s / 4, at = two ? 8 * (s % 2) : q + 8 * (s % 4);
-          const int n = n0 + row / 64 * G::WN + 16 * i0 + row % 64;
-          const uint8_t* b = ad.b + r * ad.b_rank + (s % 4 < 2 || which[1] < 0 ? which[0] : which[1]) * ad.b_adapter;
-          w[i] = load_b8(b + min(n, a.N - 1) * ad.b_stride, at, ad.rank);
-        }
-      };
-#pragma unroll
-      for (int k = 0; k < sets; ++k) left[k] = all[k];
+      for (int i = 0; i < pieces; ++i) {
+        const int s = i * threads + tid;
+        const u32x4 v = keep_b8(w[i], two ? 8 * (s % 2) : q + 8 * (s % 4), ad.rank);
+        some |= bf16_odd(v.x) || bf16_odd(v.y) || bf16_odd(v.z) || bf16_odd(v.w);
+        *reinterpret_cast<u32x4*>(rows + s / 4 * BS + s % 4 * 16) = v;
+      }
+      if (some) odd[buf] = turn;
+      __syncthreads();                                   // the other buffer's readers are through, too
       load_rows();
-      while (which[0] >= 0) {
-        const int buf = turn & 1, now[2] = {which[0], which[1]};
-        uint8_t* rows = bs + buf * HB * BS;
-        bool some = false;
+      const bool apart = odd[buf] == turn;
+      ++turn;
+      const int want = g < 2 ? now[0] : now[1];
+      // this wave's rows of b, 4 tiles of outputs at a time
 #pragma unroll
-        for (int i = 0; i < pieces; ++i) {
-          const int s = i * threads + tid;
-          const u32x4 v = keep_b8(w[i], two ? 8 * (s % 2) : q + 8 * (s % 4), ad.rank);
-          some |= bf16_odd(v.x) || bf16_odd(v.y) || bf16_odd(v.z) || bf16_odd(v.w);
-          *reinterpret_cast<u32x4*>(rows + s / 4 * BS + s % 4 * 16) = v;
-        }
-        if (some) odd[buf] = turn;
-        __syncthreads();                                   // the other buffer's readers are through, too
-        load_rows();
-        const bool apart = odd[buf] == turn;
-        ++turn;
-        const int want = g < 2 ? now[0] : now[1];
+      for (int i0 = 0; i0 < TI; i0 += 4) {
         u32x4 x[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          x[i] = *reinterpret_cast<const u32x4*>(rows + (wn / G::WN * 64 + 16 * i + c) * BS + g * 16);
+          x[i] = *reinterpret_cast<const u32x4*>(rows + (wn + 16 * (i0 + i) + c) * BS + g * 16);
 #pragma unroll
         for (int j = 0; j < TJ; ++j) {
           const bool take = of[j] >= 0 && of[j] == want;
