@@ -191,6 +191,8 @@ struct Attn {
   // Weights times the scales of 8-bit values can have any exponent, so they are
   // bf16; for fp16 outputs in two parts, since one alone has 3 bits too few.
   static constexpr bool two = C8 && QF == AR_F16;
+  // (few rows take bf16 ones always so: they wait for memory, and their times do not change)
+  static constexpr bool few_two = VF == AR_BF16;
   static constexpr int KT = DT > 128 ? 32 : 64;            // keys of a tile
   static constexpr int CB = C8 ? 16 : 8;                   // elements of 16 bytes of the cache
   static constexpr int CH = pow2_up(DT / CB);              // lanes to a row
@@ -316,6 +318,7 @@ struct Attn {
     u32x4 w, w2, seen, v, odd;
     float sum;
   };
+  template <bool TWO>
   static __device__ __forceinline__ Apart apart(const float (&score)[8], float c, float ref, const float (&scale)[8],
                                                 u32x4 v) {
     Apart x;
@@ -338,7 +341,7 @@ struct Attn {
       }
       x.w[j] = pair16<VF>(e[0], e[1]);
       x.w2[j] = 0;
-      if constexpr (two) x.w2[j] = rest16<VF>(e[0], e[1], x.w[j]);
+      if constexpr (TWO) x.w2[j] = rest16<VF>(e[0], e[1], x.w[j]);
       x.seen[j] = pair16<VF>(s[0], s[1]);
       x.v[j] = v[j] & ~odd;
       x.odd[j] = ones16<VF>() & odd;
@@ -544,7 +547,7 @@ struct Attn {
               }
               const uint8_t* at = ks + v_base + ((4 * i) ^ v_swap) * 16 + 16 * t * RS;
               const u32x2 lo = read_transposed(at), hi = read_transposed(at + 8 * RS);
-              const Apart x = apart(score, a.c, ref, scale, u32x4{lo.x, lo.y, hi.x, hi.y});
+              const Apart x = apart<two>(score, a.c, ref, scale, u32x4{lo.x, lo.y, hi.x, hi.y});
               if constexpr (i == 0) l += x.sum;
               o[i] = mma32<VF>(x.v, x.w, o[i]);
               if constexpr (two) o[i] = mma32<VF>(x.v, x.w2, o[i]);
@@ -794,10 +797,10 @@ struct Attn {
           float again = ref;
           __asm__ volatile("" : "+v"(again));
           const u32x2 lo = read_transposed(at + ((2 * i) ^ swap) * 16), hi = read_transposed(at + 16 * RS + ((2 * i) ^ swap) * 16);
-          const Apart x = apart(score, a.c, again, scale, u32x4{lo.x, lo.y, hi.x, hi.y});
+          const Apart x = apart<few_two>(score, a.c, again, scale, u32x4{lo.x, lo.y, hi.x, hi.y});
           if (i == 0) l += x.sum;
           o[i] = mma16<VF>(x.v, x.w, o[i]);
-          if constexpr (two) o[i] = mma16<VF>(x.v, x.w2, o[i]);
+          if constexpr (few_two) o[i] = mma16<VF>(x.v, x.w2, o[i]);
           const f32x4 count = mma16<VF>(x.odd, x.seen, f32x4{0.0f, 0.0f, 0.0f, 0.0f});
 #pragma unroll
           for (int r = 0; r < 4; ++r) o[i][r] = count[r] > 0.0f ? __builtin_nanf("") : o[i][r];
@@ -816,14 +819,14 @@ struct Attn {
       const u32x4 w = u32x4{pair16<VF>(e[0][0], e[0][1]), pair16<VF>(e[0][2], e[0][3]),
                             pair16<VF>(e[1][0], e[1][1]), pair16<VF>(e[1][2], e[1][3])};
       u32x4 w2 = w;
-      if constexpr (two)
+      if constexpr (few_two)
         w2 = u32x4{rest16<VF>(e[0][0], e[0][1], w.x), rest16<VF>(e[0][2], e[0][3], w.y),
                    rest16<VF>(e[1][0], e[1][1], w.z), rest16<VF>(e[1][2], e[1][3], w.w)};
 #pragma unroll
       for (int i = 0; i < DT / 16; ++i) {
         const u32x2 lo = read_transposed(at + ((2 * i) ^ swap) * 16), hi = read_transposed(at + 16 * RS + ((2 * i) ^ swap) * 16);
         o[i] = mma16<VF>(u32x4{lo.x, lo.y, hi.x, hi.y}, w, o[i]);
-        if constexpr (two) o[i] = mma16<VF>(u32x4{lo.x, lo.y, hi.x, hi.y}, w2, o[i]);
+        if constexpr (few_two) o[i] = mma16<VF>(u32x4{lo.x, lo.y, hi.x, hi.y}, w2, o[i]);
       }
       }
       compiler_barrier();                                  // before the buffer is filled again

@@ -650,9 +650,10 @@ typedef struct {
  *      of the call, so calls that may overlap need each their own.
  * Products of 16-bit operands in the matrix cores, sums, maxima and the joined
  * rows in binary32.  The weights are rounded to `format` for their products with
- * the values (with an AR_E4M3_ROW cache to bf16, for fp16 outputs in two parts):
- * out is off by at most 2^-8 (fp16: 2^-11) of sum w |v| for that, and rounded
- * once.  The order
+ * the values (with an AR_E4M3_ROW cache to bf16, for fp16 outputs in two parts;
+ * where queries * heads / kv_heads, for the prefix times sequences, is at most 16,
+ * bf16 ones too): out is off by at most 2^-8 (fp16: 2^-11) of sum w |v| for
+ * that, and rounded once.  The order
  * of every sum is fixed by the sizes and lengths, so equal calls give equal
  * bits.  out may not overlap the inputs.  sequences 0: nothing is written.
  * AR_ESIZE: sequences, prefix or max_pages * page above 2^30, 2^26 or more
