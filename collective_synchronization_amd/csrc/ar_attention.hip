@@ -357,8 +357,8 @@ struct Attn {
   // wave has 32 rows, and tiles of KT keys pass through shared memory, the next
   // one on its way while one is multiplied (8-bit ones in registers, since they
   // are converted), and the pages of the one after that.  Two waves to a SIMD take
-  // turns with matrix cores and vector units.  128 x 64 heads over 32768: bf16 190 us
-  // (0.72 PFLOP/s), 8-bit 222: the matrix cores are busy 42% of the cycles, and the
+  // turns with matrix cores and vector units.  128 x 64 heads over 32768: bf16 187 us
+  // (0.73 PFLOP/s), 8-bit 219: the matrix cores are busy 42% of the cycles, and the
   // card runs at 1.5 to 1.9 GHz meanwhile.  With the scores of the next tile formed
   // beside the weights of this one 222 and 295: registers and shared memory for it
   // cost more than it hides.

@@ -681,8 +681,8 @@ __device__ __forceinline__ bool bf16_odd(uint32_t v) {
 // Bound by its own chain of loads (index, t, rows) where there are few adapters, by
 // the products of all tiles of 16 tokens with every adapter that one of them has
 // where there are many: 4096 x 8192 x 8192, 8-bit tokens, 196 us without adapters, 8
-// requests with one of rank 16 each 219, of rank 64 238 (23 and 4 of them t), 16
-// adapters of rank 16 in any order 268.  Rows of three adapters on their way, and
+// requests with one of rank 16 each 219, of rank 64 235 (23 and 4 of them t), 16
+// adapters of rank 16 in any order 265.  Rows of three adapters on their way, and
 // t in registers, changed nothing.
 template <class G, class Acc>
 __device__ __forceinline__ void add_adapters(const Adapters& ad, const MxLinArgs& a, int r, int m0, int n0, int wm,

@@ -539,8 +539,8 @@ typedef struct {
  * with infinities in b may be NaN.  Many tokens' t is added up from shares of K,
  * scaled before that: an infinite scale, or one that takes a share past
  * binary32, may give NaN.  The order of every sum is fixed by the
- * sizes, so equal calls give equal bits, and a token's bits do not depend on the
- * other tokens' adapters.  adapters, rank or inputs 0: ar_mx4_linear alone.
+ * sizes, so equal calls give equal bits, and a token's bits (but for a zero's
+ * sign) do not depend on the other tokens' adapters.  adapters, rank or inputs 0: ar_mx4_linear alone.
  * AR_ESIZE: b_stride of 2^23 and more, adapters whose offsets pass 2^60, and as
  * for ar_mx4_linear.
  */
