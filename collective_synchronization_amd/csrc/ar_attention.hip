@@ -916,6 +916,8 @@ __global__ __launch_bounds__(kAttnThreads, DT > 128 ? 1 : 2) void k_attention(At
     p.token0 = seq * a.queries;
     p.limit0 = length - a.queries + 1;
     p.causal = true;
+    // what the tile's last token does not see, none of its tokens does
+    p.k1 = min(p.k1, p.limit0 + (min(p.row0 + kTileRows, p.rows) - 1) / a.group);
     if (p.k0 >= p.k1) {
       for (int i = p.row0 + threadIdx.x; i < min(p.rows, p.row0 + kTileRows); i += kAttnThreads)
         *reinterpret_cast<f32x2*>(a.part_m + 2 * G::out_row(a, p, i)) = f32x2{0.0f, 0.0f};

@@ -183,6 +183,14 @@ def test_sharp_scores_and_no_lse(queries):
     Batch(1, (300, 17), queries, 8, 4, 128, 16, 513, "bf16", sharp=20.0).run(lse=False)
 
 
+@pytest.mark.parametrize("cache", ["same", "row8"])
+@pytest.mark.parametrize("group", [1, 5, 8])
+def test_many_tokens_of_a_step(group, cache):
+    """Several tiles of a sequence's rows, whose tokens stop at different keys, or before the first."""
+    Batch(8, (150, 149, 20, 0, 400, -1, 290), 150, 2 * group, 2, 64, 16, 33, "bf16", cache).run()
+    Batch(9, (150, 1000), 150, 2 * group, 2, 128, 64, 0, "f16", cache).run()
+
+
 @pytest.mark.parametrize("queries", [1, 3])
 def test_rising_scores(queries):
     """Every key scores more than all before it, by steps around the slack of the reference."""
