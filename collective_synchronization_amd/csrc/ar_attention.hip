@@ -899,7 +899,7 @@ __global__ __launch_bounds__(kAttnThreads, DT > 128 ? 1 : 2) void k_attention(At
     p.limit0 = 0;
     p.causal = false;
   } else {
-    const int tile = b % a.own_tiles;
+    const int tile = a.own_tiles - 1 - b % a.own_tiles;    // those that see most first
     b /= a.own_tiles;
     p.kh = b % kv;
     b /= kv;
@@ -916,7 +916,8 @@ __global__ __launch_bounds__(kAttnThreads, DT > 128 ? 1 : 2) void k_attention(At
     p.token0 = seq * a.queries;
     p.limit0 = length - a.queries + 1;
     p.causal = true;
-    // what the tile's last token does not see, none of its tokens does
+    // what the tile's last token does not see, none of its tokens does (2 x 2048
+    // tokens by themselves 554 us without this, 320 with it, 303 in this order of tiles)
     p.k1 = min(p.k1, p.limit0 + (min(p.row0 + kTileRows, p.rows) - 1) / a.group);
     if (p.k0 >= p.k1) {
       for (int i = p.row0 + threadIdx.x; i < min(p.rows, p.row0 + kTileRows); i += kAttnThreads)
