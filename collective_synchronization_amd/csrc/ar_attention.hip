@@ -304,6 +304,8 @@ struct Attn {
   static __device__ __forceinline__ bool values_odd(const uint8_t* values, const float* scales, int n, int lane) {
     uint32_t odd = 0;
     for (int i = lane; i < n * C16; i += kWave) {
+      // (what lies behind a row of 8-bit codes is not written)
+      if (C8 && C16 > DT / 8 && ((i % C16) ^ swap_v(i / C16)) >= DT / 8) continue;
       const u32x4 v = *reinterpret_cast<const u32x4*>(values + i * 16);
       odd |= odd_halves<VF>(v.x) | odd_halves<VF>(v.y) | odd_halves<VF>(v.z) | odd_halves<VF>(v.w);
     }
@@ -313,16 +315,15 @@ struct Attn {
     return __any(odd != 0);
   }
   // 8 keys' weights of a row, 1 for those that are seen, and a column's values and the
-  // places of odd ones.
+  // places of odd ones.  `sum`: the weights are added to it one by one, as they are
+  // where nothing is odd, so that bits do not depend on the values' way.
   struct Apart {
     u32x4 w, w2, seen, v, odd;
-    float sum;
   };
   template <bool TWO>
   static __device__ __forceinline__ Apart apart(const float (&score)[8], float c, float ref, const float (&scale)[8],
-                                                u32x4 v) {
+                                                u32x4 v, float& sum) {
     Apart x;
-    x.sum = 0.0f;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       float e[2], s[2];
@@ -332,7 +333,7 @@ struct Attn {
         const float t = score[2 * j + u];
         s[u] = t == -__builtin_inff() ? 0.0f : 1.0f;
         e[u] = t == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(__builtin_fmaf(t, c, -ref));
-        x.sum += e[u];
+        sum += e[u];
         if constexpr (C8) {
           const bool bad = abs_bits(scale[2 * j + u]) >= kInfBits;
           e[u] = bad ? 0.0f : e[u] * scale[2 * j + u];
@@ -547,8 +548,8 @@ struct Attn {
               }
               const uint8_t* at = ks + v_base + ((4 * i) ^ v_swap) * 16 + 16 * t * RS;
               const u32x2 lo = read_transposed(at), hi = read_transposed(at + 8 * RS);
-              const Apart x = apart<two>(score, a.c, ref, scale, u32x4{lo.x, lo.y, hi.x, hi.y});
-              if constexpr (i == 0) l += x.sum;
+              float aside = 0.0f;                          // the sum has them once
+              const Apart x = apart<two>(score, a.c, ref, scale, u32x4{lo.x, lo.y, hi.x, hi.y}, i == 0 ? l : aside);
               o[i] = mma32<VF>(x.v, x.w, o[i]);
               if constexpr (two) o[i] = mma32<VF>(x.v, x.w2, o[i]);
               count = mma32<VF>(x.odd, x.seen, count);
@@ -797,8 +798,8 @@ struct Attn {
           float again = ref;
           __asm__ volatile("" : "+v"(again));
           const u32x2 lo = read_transposed(at + ((2 * i) ^ swap) * 16), hi = read_transposed(at + 16 * RS + ((2 * i) ^ swap) * 16);
-          const Apart x = apart<few_two>(score, a.c, again, scale, u32x4{lo.x, lo.y, hi.x, hi.y});
-          if (i == 0) l += x.sum;
+          float aside = 0.0f;                              // the sum has them once
+          const Apart x = apart<few_two>(score, a.c, again, scale, u32x4{lo.x, lo.y, hi.x, hi.y}, i == 0 ? l : aside);
           o[i] = mma16<VF>(x.v, x.w, o[i]);
           if constexpr (few_two) o[i] = mma16<VF>(x.v, x.w2, o[i]);
           const f32x4 count = mma16<VF>(x.odd, x.seen, f32x4{0.0f, 0.0f, 0.0f, 0.0f});
