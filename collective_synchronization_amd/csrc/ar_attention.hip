@@ -88,11 +88,21 @@ __device__ __forceinline__ uint32_t pair16(float lo, float hi) {
   else return __builtin_bit_cast(uint32_t, f16x2{(_Float16)lo, (_Float16)hi});
 }
 
-// ... and what they leave of binary32 values, in the same type.
-template <int F>
-__device__ __forceinline__ uint32_t rest16(float lo, float hi, uint32_t pair) {
-  static_assert(F == AR_BF16, "");
-  return bf16_pair(lo - bf_lo(pair), hi - bf_hi(pair));
+// Two binary32 weights as two bf16 parts each, off by 2^-16 together: the first
+// is cut, not rounded, and the rest, which has 2^-23 of the weight added, is therefore
+// above zero wherever the weight is: times an infinite value both are the same
+// infinity.  SCALED: weights times scales, which may be infinities; these are in the rest.
+struct Parts16 {
+  uint32_t top, rest;
+};
+template <bool SCALED>
+__device__ __forceinline__ Parts16 parts16(float lo, float hi) {
+  constexpr float most = 0x1.fffffep127f, more = 0x1.000002p0f;
+  const float a = SCALED ? __builtin_amdgcn_fmed3f(lo, -most, most) : lo;
+  const float b = SCALED ? __builtin_amdgcn_fmed3f(hi, -most, most) : hi;
+  const uint32_t u = __float_as_uint(a), v = __float_as_uint(b);
+  return Parts16{__builtin_amdgcn_perm(v, u, 0x07060302u),
+                 bf16_pair(__builtin_fmaf(lo, more, -bf_hi(u)), __builtin_fmaf(hi, more, -bf_hi(v)))};
 }
 
 // 8 e4m3 codes in a 16-bit type, without loss.
@@ -166,13 +176,38 @@ __device__ __forceinline__ void load_to_lds(rsrc_t r, uint8_t* lds, uint32_t off
 }
 constexpr uint32_t kNowhere = 0x80000000u;   // past every range: reads as zeros
 
+// Masks, in integer arithmetic: a condition for each of many values would take more
+// scalar registers than there are, and cost the loops around it theirs.
 // Which halves of a pair of 16-bit values are infinities or NaNs: all ones there.
 template <int F>
 __device__ __forceinline__ uint32_t odd_halves(uint32_t v) {
-  constexpr uint32_t top = F == AR_BF16 ? 0x7F80u : 0x7C00u;
-  return ((v & top) == top ? 0xFFFFu : 0u) | ((v >> 16 & top) == top ? 0xFFFF0000u : 0u);
+  constexpr uint32_t exponent = F == AR_BF16 ? 0x7F807F80u : 0x7C007C00u, one = F == AR_BF16 ? 0x00800080u : 0x04000400u;
+  const uint32_t top = ((v & exponent) + one) & 0x80008000u;
+  return top | (top - (top >> 15));
 }
-template <int F> constexpr uint32_t ones16() { return F == AR_BF16 ? 0x3F803F80u : 0x3C003C00u; }
+// All ones for an infinity or a NaN.
+__device__ __forceinline__ uint32_t odd_mask(float v) {
+  return (uint32_t)((int32_t)((__float_as_uint(v) & kInfBits) + 0x00800000u) >> 31);
+}
+__device__ __forceinline__ uint32_t nonzero_mask(uint32_t v) {       // below 2^31
+  return (uint32_t)(-(int32_t)v >> 31);
+}
+__device__ __forceinline__ uint32_t choose(uint32_t mask, uint32_t one, uint32_t zero) {
+  return (one & mask) | (zero & ~mask);
+}
+// What an infinity or a NaN counts for, as a 16-bit value: powers of two (2^14 for a
+// NaN, 2^7 and 1), so that a sum over up to 64 keys says how many there are of each.
+template <int F>
+__device__ __forceinline__ uint32_t count_of(uint32_t nan, uint32_t negative) {
+  constexpr bool b = F == AR_BF16;
+  return choose(nan, b ? 0x4680u : 0x7400u, choose(negative, b ? 0x4300u : 0x5800u, b ? 0x3F80u : 0x3C00u));
+}
+__device__ __forceinline__ float add_counted(float sum, float count) {
+  const uint32_t n = (uint32_t)count;
+  float v = (n & 127) != 0 ? __builtin_inff() : 0.0f;
+  if ((n >> 7 & 127) != 0) v = v == 0.0f ? -__builtin_inff() : __builtin_nanf("");
+  return n == 0 ? sum : sum + (n >> 14 != 0 ? __builtin_nanf("") : v);
+}
 
 template <int I> struct Index { static constexpr int value = I; };
 template <int N, int I = 0, class F>
@@ -298,9 +333,9 @@ struct Attn {
   }
   // What a token of the step does not see may not touch it, be it an infinity or a
   // NaN, which its weight 0 would make NaN.  So where keys that some of the rows do
-  // not see have such values, or scales (values_odd), these are taken out, and
-  // counted for each output by a product of their places with those of the keys
-  // that are seen: an output with any is NaN.
+  // not see have such values, or scales (values_odd), these are taken out, and for
+  // each output those of the keys that it sees are counted by a product, for what
+  // they make of it.
   static __device__ __forceinline__ bool values_odd(const uint8_t* values, const float* scales, int n, int lane) {
     uint32_t odd = 0;
     for (int i = lane; i < n * C16; i += kWave) {
@@ -314,11 +349,17 @@ struct Attn {
     }
     return __any(odd != 0);
   }
-  // 8 keys' weights of a row, 1 for those that are seen, and a column's values and the
-  // places of odd ones.  `sum`: the weights are added to it one by one, as they are
-  // where nothing is odd, so that bits do not depend on the values' way.
+  // Halves of two keys' values that are odd, or whose scales are.
+  static __device__ __forceinline__ uint32_t odd_pair(uint32_t v, const float* scale) {
+    uint32_t odd = odd_halves<VF>(v);
+    if constexpr (C8) odd |= (odd_mask(scale[0]) & 0xFFFFu) | (odd_mask(scale[1]) & 0xFFFF0000u);
+    return odd;
+  }
+  // 8 keys' weights of a row, and a column's values without odd ones.  `sum`: the
+  // weights are added to it one by one, as they are where nothing is odd, so that bits
+  // do not depend on the values' way.
   struct Apart {
-    u32x4 w, w2, seen, v, odd;
+    u32x4 w, w2, v;
   };
   template <bool TWO>
   static __device__ __forceinline__ Apart apart(const float (&score)[8], float c, float ref, const float (&scale)[8],
@@ -326,26 +367,53 @@ struct Attn {
     Apart x;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      float e[2], s[2];
-      uint32_t odd = odd_halves<VF>(v[j]);
+      float e[2];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const float t = score[2 * j + u];
-        s[u] = t == -__builtin_inff() ? 0.0f : 1.0f;
-        e[u] = t == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(__builtin_fmaf(t, c, -ref));
+        e[u] = __builtin_amdgcn_exp2f(__builtin_fmaf(score[2 * j + u], c, -ref));
         sum += e[u];
         if constexpr (C8) {
-          const bool bad = abs_bits(scale[2 * j + u]) >= kInfBits;
-          e[u] = bad ? 0.0f : e[u] * scale[2 * j + u];
-          if (bad) odd |= u ? 0xFFFF0000u : 0xFFFFu;
+          const float by = scale[2 * j + u];
+          e[u] *= __uint_as_float(__float_as_uint(by) & ~odd_mask(by));
         }
       }
-      x.w[j] = pair16<VF>(e[0], e[1]);
-      x.w2[j] = 0;
-      if constexpr (TWO) x.w2[j] = rest16<VF>(e[0], e[1], x.w[j]);
+      if constexpr (TWO) {
+        const Parts16 p = parts16<C8>(e[0], e[1]);
+        x.w[j] = p.top;
+        x.w2[j] = p.rest;
+      } else {
+        x.w[j] = pair16<VF>(e[0], e[1]);
+        x.w2[j] = 0;
+      }
+      x.v[j] = v[j] & ~odd_pair(v[j], scale + 2 * j);
+    }
+    return x;
+  }
+  // 1 for those of 8 keys that are seen, and what a column's odd values count for.
+  struct Counted {
+    u32x4 seen, odd;
+  };
+  static __device__ __forceinline__ Counted counted(const float (&score)[8], const float (&scale)[8], u32x4 v) {
+    Counted x;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t odd = odd_pair(v[j], scale + 2 * j);
+      float s[2];
+      x.odd[j] = 0;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        s[u] = score[2 * j + u] == -__builtin_inff() ? 0.0f : 1.0f;
+        const uint32_t mine = v[j] >> 16 * u & 0xFFFFu;
+        uint32_t nan = nonzero_mask(mine & (VF == AR_BF16 ? 0x7Fu : 0x3FFu)), negative = nonzero_mask(mine & 0x8000u);
+        if constexpr (C8) {                                // codes are NaNs alone, scales infinities, too
+          const uint32_t by = __float_as_uint(scale[2 * j + u]);
+          nan = odd_halves<VF>(mine) | nonzero_mask(by & 0x7FFFFFu) | ~nonzero_mask(mine & 0x7FFFu);
+          negative ^= (uint32_t)((int32_t)by >> 31);
+        }
+        x.odd[j] |= count_of<VF>(nan, negative) << 16 * u;
+      }
+      x.odd[j] &= odd;
       x.seen[j] = pair16<VF>(s[0], s[1]);
-      x.v[j] = v[j] & ~odd;
-      x.odd[j] = ones16<VF>() & odd;
     }
     return x;
   }
@@ -531,13 +599,11 @@ struct Attn {
         if (LATER && !all_see.value && values_odd(ks + KT * RS, sc + KT, KT, lane)) {
           for_each<DT / 32>([&](auto index) {
             constexpr int i = index.value;
-            f32x16 count;
-#pragma unroll
-            for (int r = 0; r < 16; ++r) count[r] = 0.0f;
-            for_each<KT / 16>([&](auto index) {
+            // one piece at a time, and its weights formed anew for each i: registers are short
+            auto with_piece = [&](auto index, auto f) {
               constexpr int t = index.value;
-              __builtin_amdgcn_sched_barrier(0);           // one piece at a time, and its weights formed anew for
-              int first = 4 * half;                        // each i: registers are short
+              __builtin_amdgcn_sched_barrier(0);
+              int first = 4 * half;
               __asm__ volatile("" : "+v"(first));
               float score[8], scale[8];
 #pragma unroll
@@ -548,14 +614,27 @@ struct Attn {
               }
               const uint8_t* at = ks + v_base + ((4 * i) ^ v_swap) * 16 + 16 * t * RS;
               const u32x2 lo = read_transposed(at), hi = read_transposed(at + 8 * RS);
-              float aside = 0.0f;                          // the sum has them once
-              const Apart x = apart<two>(score, a.c, ref, scale, u32x4{lo.x, lo.y, hi.x, hi.y}, i == 0 ? l : aside);
-              o[i] = mma32<VF>(x.v, x.w, o[i]);
-              if constexpr (two) o[i] = mma32<VF>(x.v, x.w2, o[i]);
-              count = mma32<VF>(x.odd, x.seen, count);
+              f(score, scale, u32x4{lo.x, lo.y, hi.x, hi.y});
+            };
+            for_each<KT / 16>([&](auto index) {
+              with_piece(index, [&](const float (&score)[8], const float (&scale)[8], u32x4 v) {
+                float aside = 0.0f;                        // the sum has them once
+                const Apart x = apart<two>(score, a.c, ref, scale, v, i == 0 ? l : aside);
+                o[i] = mma32<VF>(x.v, x.w, o[i]);
+                if constexpr (two) o[i] = mma32<VF>(x.v, x.w2, o[i]);
+              });
+            });
+            f32x16 count;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) count[r] = 0.0f;
+            for_each<KT / 16>([&](auto index) {
+              with_piece(index, [&](const float (&score)[8], const float (&scale)[8], u32x4 v) {
+                const Counted x = counted(score, scale, v);
+                count = mma32<VF>(x.odd, x.seen, count);
+              });
             });
 #pragma unroll
-            for (int r = 0; r < 16; ++r) o[i][r] = count[r] > 0.0f ? __builtin_nanf("") : o[i][r];
+            for (int r = 0; r < 16; ++r) o[i][r] = add_counted(o[i][r], count[r]);
           });
         } else {
         u32x4 w[KT / 16], w2[two ? KT / 16 : 1];
@@ -580,8 +659,13 @@ struct Attn {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const float a0 = e[8 * u + 2 * j], a1 = e[8 * u + 2 * j + 1];
-              w[2 * t + u][j] = pair16<VF>(a0, a1);
-              if constexpr (two) w2[2 * t + u][j] = rest16<VF>(a0, a1, w[2 * t + u][j]);
+              if constexpr (two) {
+                const Parts16 p = parts16<C8>(a0, a1);
+                w[2 * t + u][j] = p.top;
+                w2[2 * t + u][j] = p.rest;
+              } else {
+                w[2 * t + u][j] = pair16<VF>(a0, a1);
+              }
             }
         }
 #pragma unroll
@@ -802,9 +886,10 @@ struct Attn {
           const Apart x = apart<few_two>(score, a.c, again, scale, u32x4{lo.x, lo.y, hi.x, hi.y}, i == 0 ? l : aside);
           o[i] = mma16<VF>(x.v, x.w, o[i]);
           if constexpr (few_two) o[i] = mma16<VF>(x.v, x.w2, o[i]);
-          const f32x4 count = mma16<VF>(x.odd, x.seen, f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+          const Counted y = counted(score, scale, u32x4{lo.x, lo.y, hi.x, hi.y});
+          const f32x4 count = mma16<VF>(y.odd, y.seen, f32x4{0.0f, 0.0f, 0.0f, 0.0f});
 #pragma unroll
-          for (int r = 0; r < 4; ++r) o[i][r] = count[r] > 0.0f ? __builtin_nanf("") : o[i][r];
+          for (int r = 0; r < 4; ++r) o[i][r] = add_counted(o[i][r], count[r]);
         }
       } else {
       f32x4 e[2];
@@ -817,12 +902,18 @@ struct Attn {
         }
         if constexpr (C8) e[t] *= *reinterpret_cast<const f32x4*>(sc + 32 + 16 * t + 4 * g);
       }
-      const u32x4 w = u32x4{pair16<VF>(e[0][0], e[0][1]), pair16<VF>(e[0][2], e[0][3]),
-                            pair16<VF>(e[1][0], e[1][1]), pair16<VF>(e[1][2], e[1][3])};
-      u32x4 w2 = w;
-      if constexpr (few_two)
-        w2 = u32x4{rest16<VF>(e[0][0], e[0][1], w.x), rest16<VF>(e[0][2], e[0][3], w.y),
-                   rest16<VF>(e[1][0], e[1][1], w.z), rest16<VF>(e[1][2], e[1][3], w.w)};
+      u32x4 w, w2;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float a0 = e[j / 2][j % 2 * 2], a1 = e[j / 2][j % 2 * 2 + 1];
+        if constexpr (few_two) {
+          const Parts16 p = parts16<C8>(a0, a1);
+          w[j] = p.top;
+          w2[j] = p.rest;
+        } else {
+          w[j] = pair16<VF>(a0, a1);
+        }
+      }
 #pragma unroll
       for (int i = 0; i < DT / 16; ++i) {
         const u32x2 lo = read_transposed(at + ((2 * i) ^ swap) * 16), hi = read_transposed(at + 16 * RS + ((2 * i) ^ swap) * 16);

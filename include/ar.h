@@ -645,6 +645,11 @@ typedef struct {
  *      tokens on a page that is none of 0 .. cache.pages - 1.
  *   What lies in the cache behind a sequence's last token does not count,
  *      whatever it is.
+ *   Infinities and NaNs among the values of tokens that a row sees: as in the
+ *      formula, an infinity, or NaN where two signs meet or one is a NaN, whatever the
+ *      batch's size; but times a weight of nothing they may be NaN (below 2^-110 of
+ *      the row's largest weight, for fp16 rows of the cache 2^-31).  A score of -inf
+ *      weighs nothing, as a token that is not seen.
  *   work: device, 256-byte aligned, at least
  *      ar_prefix_attention_work_bytes(p) bytes (AR_ESIZE); used for the time
  *      of the call, so calls that may overlap need each their own.
