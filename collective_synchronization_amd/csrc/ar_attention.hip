@@ -146,8 +146,9 @@ __device__ __forceinline__ float other_row_sum(float v) {
 
 // Where the maximum of a row has grown by less than 2^kSlack since the weights'
 // reference was taken, the reference stays: no sum has to be scaled, and the
-// weights stay below 2^kSlack.  In fp16 they are 2^kF16Up times as large, so
-// that those down to 2^-30 of the largest keep their bits.
+// weights stay below 2^kSlack.  In fp16 they are 2^kF16Up times as large, so that
+// those down to 2^-20 of the largest keep their bits; smaller ones are subnormal there,
+// each off by up to 2^-31 of the largest.
 constexpr float kSlack = 8.0f;
 constexpr float kF16Up = 6.0f;
 template <int F> constexpr float weights_up() { return F == AR_F16 ? kF16Up : 0.0f; }

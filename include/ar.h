@@ -658,7 +658,10 @@ typedef struct {
  * the values (with an AR_E4M3_ROW cache to bf16, for fp16 outputs in two parts;
  * where queries * heads / kv_heads, for the prefix times sequences, is at most 16,
  * bf16 ones too): out is off by at most 2^-8 (fp16: 2^-11) of sum w |v| for
- * that, and rounded once.  The order
+ * that, with an AR_F16 cache by 2^-31 of the row's largest weight times sum |v| more
+ * (weights below 2^-20 of it are subnormal in fp16), and rounded once.  Sums are
+ * of weights up to 2^8 times the values, before they are divided: values near the end
+ * of bf16's range can take them past binary32's.  The order
  * of every sum is fixed by the sizes and lengths, so equal calls give equal
  * bits.  out may not overlap the inputs.  sequences 0: nothing is written.
  * AR_ESIZE: sequences, prefix or max_pages * page above 2^30, 2^26 or more
