@@ -516,8 +516,30 @@ static int64_t delta_bytes(const ar_linear_params* p, const ar_adapter_params* q
   return (p->nranks * p->rows * delta_row(p) * 4 + 255) / 256 * 256;
 }
 
+// A work buffer that does for these tokens and for any fewer: both forms of t, and
+// sums made ready, need less again from some number of tokens on.  Of t, shares of K
+// are kTokenParts at most, and fewer than 256 for each group of kTokenGroup tokens
+// together; sums are made ready up to where the largest tiles begin.
 static int64_t adapter_work(const ar_linear_params* p, const ar_adapter_params* q) {
-  return adapters_count(p, q) ? t_bytes(p, q) + delta_bytes(p, q) : 0;
+  if (!adapters_count(p, q)) return 0;
+  int64_t t = t_ranks(p, q) * p->rows;
+  if (p->rows > kFewTokens) {
+    const int64_t groups = ceil_div64(q->rank, 64), shares = 256 * kTokenGroup / groups;
+    const int64_t most = kTokenParts * t < shares ? kTokenParts * t : shares;
+    if (t < most) t = most;
+  }
+  ar_linear_params few = *p;
+  MxLinArgs a = linear_args(p);
+  if (large_tiles(a, p->nranks)) {
+    int64_t small = 1, large = p->rows;                    // the first number of tokens with the largest tiles
+    while (small + 1 < large) {
+      a.M = (int32_t)((small + large) / 2);
+      if (large_tiles(a, p->nranks)) large = a.M;
+      else small = a.M;
+    }
+    few.rows = small;
+  }
+  return (t * t_row_bytes(q) + 255) / 256 * 256 + delta_bytes(&few, q);
 }
 
 static hipError_t launch_delta(const Adapters& ad, const MxLinArgs& a, int nranks, hipStream_t s) {

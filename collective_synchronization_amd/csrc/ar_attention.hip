@@ -1156,26 +1156,29 @@ struct AttnPlan {
 // 2 tokens, prefix 4999, own 777, heads of 96, 27 us with 512 pieces, 32 with 536.
 // (Pieces of split ones vary with the lengths: 8 sequences of up to 32768, 161
 // with 520, 169 with 512.)
+static int64_t row_tiles(int64_t rows) { return rows <= kFewRows ? 1 : ceil_div64(rows, kTileRows); }
+static int64_t step_keys(int64_t rows) { return rows <= kFewRows ? 128 : 64; }
+static int64_t most_places(const ar_attention_params* p) {
+  return p->cache.dim <= 64 ? 1024 : (p->cache.dim <= 128 ? 512 : 256);
+}
 static AttnPlan plan_attention(const ar_attention_params* p) {
   AttnPlan s{};
   const int64_t kv = p->cache.kv_heads, group = p->heads / kv;
   const int64_t rows = p->sequences * p->queries * group, own_rows = p->queries * group;
   const int64_t capacity = p->max_pages * p->cache.page;
-  auto tiles = [](int64_t r) { return r <= kFewRows ? 1 : ceil_div64(r, kTileRows); };
-  auto step = [](int64_t r) { return r <= kFewRows ? 128 : 64; };
-  s.prefix_tiles = (int32_t)tiles(rows);
-  s.own_tiles = (int32_t)tiles(own_rows);
-  const int64_t shared = kv * s.prefix_tiles * ceil_div64(p->prefix, step(rows));
-  const int64_t own = p->sequences * kv * s.own_tiles * ceil_div64(capacity, step(own_rows));
-  const int64_t places = p->cache.dim <= 64 ? 1024 : (p->cache.dim <= 128 ? 512 : 256);
+  s.prefix_tiles = (int32_t)row_tiles(rows);
+  s.own_tiles = (int32_t)row_tiles(own_rows);
+  const int64_t shared = kv * s.prefix_tiles * ceil_div64(p->prefix, step_keys(rows));
+  const int64_t own = p->sequences * kv * s.own_tiles * ceil_div64(capacity, step_keys(own_rows));
+  const int64_t places = most_places(p);
   int64_t steps = ceil_div64(shared + own, places), at_once = places;
   if (steps < 6) {
     steps = ceil_div64(shared + own, 256);
     at_once = 256;
   }
-  if (capacity > 0) s.own_splits = (int32_t)ceil_div64(capacity, steps * step(own_rows));
+  if (capacity > 0) s.own_splits = (int32_t)ceil_div64(capacity, steps * step_keys(own_rows));
   if (p->prefix > 0) {
-    int64_t n = ceil_div64(p->prefix, steps * step(rows));
+    int64_t n = ceil_div64(p->prefix, steps * step_keys(rows));
     const int64_t room = (at_once - p->sequences * kv * s.own_tiles * s.own_splits) / (kv * s.prefix_tiles);
     if (s.own_splits <= 1 && room < n && 4 * room >= 3 * n) n = room;
     s.prefix_chunk = (int32_t)(ceil_div64(ceil_div64(p->prefix, n), 64) * 64);
@@ -1184,10 +1187,23 @@ static AttnPlan plan_attention(const ar_attention_params* p) {
   return s;
 }
 
-static int64_t attention_bytes(const ar_attention_params* p, const AttnPlan& s) {
-  const int64_t rows = p->sequences * p->queries * p->heads;
-  const int64_t parts = s.prefix_splits + s.own_splits;
-  return (parts * rows * (p->cache.dim + 2) * 4 + 255) / 256 * 256;
+// A work buffer that does for the plan, and for that of every batch with fewer
+// sequences, a shorter prefix or fewer pages.  A plan's steps go into `places` times
+// what a workgroup takes, so that
+//     sequences * kv_heads * own_tiles * own_splits < places + sequences * kv_heads * own_tiles,
+// and the prefix's splits in the same way; times the rows of a tile neither bound falls
+// as a size grows.  Few keys have no more pieces than steps.
+static int64_t attention_bytes(const ar_attention_params* p) {
+  const int64_t kv = p->cache.kv_heads, own_rows = p->queries * (p->heads / kv);
+  const int64_t rows = p->sequences * p->queries * p->heads, shared_rows = p->sequences * own_rows;
+  const int64_t capacity = p->max_pages * p->cache.page, places = most_places(p);
+  const int64_t own_step = ceil_div64(capacity, step_keys(own_rows)), prefix_step = ceil_div64(p->prefix, step_keys(kTileRows));
+  const int64_t tile = shared_rows < kTileRows ? shared_rows : kTileRows;
+  auto least = [](int64_t a, int64_t b) { return a < b ? a : b; };
+  int64_t n = 0;                                           // rows of all parts
+  if (capacity > 0) n += least(own_step * rows, ceil_div64(places * own_rows, row_tiles(own_rows)) + rows);
+  if (p->prefix > 0) n += least(prefix_step * rows, places * tile + rows);
+  return (n * (p->cache.dim + 2) * 4 + 255) / 256 * 256;
 }
 
 template <int QF, bool C8, int DT>
@@ -1229,7 +1245,7 @@ int64_t ar_prefix_attention_work_bytes(const ar_attention_params* p) {
   const int rc = check_attention(p);
   if (rc) return rc;
   if (p->sequences == 0) return 0;
-  return attention_bytes(p, plan_attention(p));
+  return attention_bytes(p);
 }
 
 int ar_prefix_attention(const ar_attention_params* p, void* work, int64_t work_bytes, void* stream) {
@@ -1243,7 +1259,7 @@ int ar_prefix_attention(const ar_attention_params* p, void* work, int64_t work_b
     if (rc) return rc;
   }
   const AttnPlan plan = plan_attention(p);
-  const int64_t bytes = attention_bytes(p, plan);
+  const int64_t bytes = attention_bytes(p);
   if (bytes > 0) {
     if (!work) return AR_EINVAL;
     if (!aligned(work, 256)) return AR_EALIGN;

@@ -547,7 +547,11 @@ typedef struct {
 int ar_mx4_linear_adapters(const ar_linear_params* p, const ar_adapter_params* q, void* work,
                            int64_t work_bytes, void* stream);
 
-/* Bytes of its work buffer, by sizes, strides and formats; < 0 on bad parameters. */
+/*
+ * Bytes of its work buffer, by sizes, strides and formats; < 0 on bad parameters.  Fewer
+ * rows, with all else the same, never need more: a buffer for the most tokens does for
+ * all batches.
+ */
 int64_t ar_adapter_work_bytes(const ar_linear_params* p, const ar_adapter_params* q);
 
 /*
@@ -669,7 +673,10 @@ typedef struct {
  */
 int ar_prefix_attention(const ar_attention_params* p, void* work, int64_t work_bytes, void* stream);
 
-/* Bytes of its work buffer, by sizes alone (not lengths); < 0 on bad parameters. */
+/*
+ * Bytes of its work buffer, by sizes alone (not lengths); < 0 on bad parameters.  Fewer
+ * sequences, a shorter prefix or fewer pages, with all else the same, never need more.
+ */
 int64_t ar_prefix_attention_work_bytes(const ar_attention_params* p);
 
 /* ------------------------------------------------------------ simulator --- */
