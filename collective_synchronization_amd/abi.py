@@ -73,6 +73,7 @@ class ar_sim_params(ctypes.Structure):
 
 
 class ar_norm_params(ctypes.Structure):
+    device = None                                # of the tensors behind the addresses
     _fields_ = [("rows", ctypes.c_int64), ("hidden", ctypes.c_int64),
                 ("eps", ctypes.c_float), ("format", ctypes.c_int32),
                 ("gamma", ctypes.c_void_p), ("res_format", ctypes.c_int32),
@@ -84,6 +85,7 @@ class ar_norm_params(ctypes.Structure):
 
 
 class ar_linear_params(ctypes.Structure):
+    device = None                                # of the tensors behind the addresses
     _fields_ = [("nranks", ctypes.c_int32), ("reserved", ctypes.c_int32),
                 ("rows", ctypes.c_int64), ("outputs", ctypes.c_int64),
                 ("inputs", ctypes.c_int64), ("x_format", ctypes.c_int32),
@@ -98,6 +100,7 @@ class ar_linear_params(ctypes.Structure):
 
 
 class ar_adapter_params(ctypes.Structure):
+    device = None                                # of the tensors behind the addresses
     _fields_ = [("adapters", ctypes.c_int32), ("rank", ctypes.c_int32),
                 ("index", ctypes.c_void_p), ("scale", ctypes.c_void_p),
                 ("a", ctypes.c_void_p), ("a_stride", ctypes.c_int64),
@@ -108,6 +111,7 @@ class ar_adapter_params(ctypes.Structure):
 
 
 class ar_kv_cache(ctypes.Structure):
+    device = None                                # of the tensors behind the addresses
     _fields_ = [("format", ctypes.c_int32), ("page", ctypes.c_int32),
                 ("pages", ctypes.c_int64), ("kv_heads", ctypes.c_int32),
                 ("dim", ctypes.c_int32), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
@@ -118,6 +122,7 @@ class ar_kv_cache(ctypes.Structure):
 
 
 class ar_attention_params(ctypes.Structure):
+    device = None                                # of the tensors behind the addresses
     _fields_ = [("cache", ar_kv_cache), ("sequences", ctypes.c_int64),
                 ("queries", ctypes.c_int32), ("heads", ctypes.c_int32),
                 ("scale", ctypes.c_float), ("format", ctypes.c_int32),
@@ -279,6 +284,22 @@ def _gpu_ptrs(where: str, *xs):
             x = x.data_ptr()
         out.append(x)
     return out
+
+
+def _keep(params, tensors):
+    """Parameters that hold what their addresses belong to, and know its device."""
+    params.tensors = tensors
+    params.device = next((t.get_device() for t in tensors
+                          if t is not None and t.__class__ is not int), None)
+    return params
+
+
+def _same_device(where: str, params) -> None:
+    """Parameters made while another device was current are refused: a kernel
+    of this one would use that one's memory."""
+    if params.device is not None and params.device != _current_device():
+        raise ArError(AR_EINVAL, f"{where}: parameters of tensors on cuda:{params.device}, which "
+                                 "is not the current device")
 
 
 def _stream(stream) -> Optional[int]:
@@ -445,12 +466,12 @@ def norm_params(rows, hidden, eps, fmt, gamma, res_fmt, residual, residual_strid
     p = ar_norm_params(rows, hidden, eps, format_id(fmt), g, format_id(res_fmt),
                        format_id(y_fmt), r, residual_stride, h, residual_out_stride, o,
                        y_stride, s, scale_stride, 0)
-    p.tensors = tensors
-    return p
+    return _keep(p, tensors)
 
 
 def ar_residual_norm(params: ar_norm_params, x, x_stride, stream=None) -> None:
     x, = _gpu_ptrs("ar_residual_norm", x)
+    _same_device("ar_residual_norm", params)
     _check(_lib.ar_residual_norm(ctypes.byref(params), x, x_stride, _stream(stream)),
            "ar_residual_norm")
 
@@ -458,6 +479,7 @@ def ar_residual_norm(params: ar_norm_params, x, x_stride, stream=None) -> None:
 def ar_reduce_norm(desc, scratch, params: ar_norm_params, epoch, ctrl, timeout_ns: int = 0,
                    flags: int = 0, stream=None) -> None:
     scratch, ctrl = _gpu_ptrs("ar_reduce_norm", scratch, ctrl)
+    _same_device("ar_reduce_norm", params)
     _check(_lib.ar_reduce_norm(ctypes.byref(desc), scratch, ctypes.byref(params), epoch, ctrl,
                                timeout_ns, flags, _stream(stream)), "ar_reduce_norm")
 
@@ -491,11 +513,11 @@ def linear_params(nranks, rows, outputs, inputs, x_fmt, x, x_stride, x_rank_stri
                          x, x_stride, x_rank_stride, xs, x_scale_stride, x_scale_rank_stride,
                          w, w_stride, w_rank_stride, ws, w_scale_stride, w_scale_rank_stride,
                          y, y_stride, y_rank_stride)
-    p.tensors = tensors
-    return p
+    return _keep(p, tensors)
 
 
 def ar_mx4_linear(params: ar_linear_params, stream=None) -> None:
+    _same_device("ar_mx4_linear", params)
     _check(_lib.ar_mx4_linear(ctypes.byref(params), _stream(stream)), "ar_mx4_linear")
 
 
@@ -508,8 +530,7 @@ def adapter_params(adapters, rank, index, scale, a, a_stride, a_adapter_stride, 
     index, scale, a, b = _gpu_ptrs("adapter_params", *tensors)
     p = ar_adapter_params(adapters, rank, index, scale, a, a_stride, a_adapter_stride,
                           a_rank_stride, b, b_stride, b_adapter_stride, b_rank_stride, 0)
-    p.tensors = tensors
-    return p
+    return _keep(p, tensors)
 
 
 def ar_adapter_work_bytes(linear: ar_linear_params, adapters: ar_adapter_params) -> int:
@@ -522,6 +543,8 @@ def ar_mx4_linear_adapters(linear: ar_linear_params, adapters: ar_adapter_params
     """work: a device tensor of at least ar_adapter_work_bytes(linear, adapters)
     bytes, of this call alone while it runs (None where that is 0)."""
     w, = _gpu_ptrs("ar_mx4_linear_adapters", work)
+    _same_device("ar_mx4_linear_adapters", linear)
+    _same_device("ar_mx4_linear_adapters", adapters)
     nbytes = 0 if work is None else work.numel() * work.element_size()
     _check(_lib.ar_mx4_linear_adapters(ctypes.byref(linear), ctypes.byref(adapters), w, nbytes,
                                        _stream(stream)), "ar_mx4_linear_adapters")
@@ -536,8 +559,7 @@ def cache_params(fmt, pages, page, kv_heads, dim, k, v, page_stride, token_strid
     k, v, ks, vs = _gpu_ptrs("cache_params", *tensors)
     c = ar_kv_cache(format_id(fmt), page, pages, kv_heads, dim, k, v, page_stride, token_stride,
                     head_stride, ks, vs, scale_page_stride, scale_token_stride, scale_head_stride)
-    c.tensors = tensors
-    return c
+    return _keep(c, tensors)
 
 
 # ar_append_params, packed for each call: without a kernel 2.3 us, against 3.6
@@ -549,6 +571,7 @@ def ar_cache_append(cache: ar_kv_cache, sequences, queries, fmt, k, k_stride, k_
                     v_stride, v_head_stride, lengths, pages, pages_stride, max_pages,
                     stream=None) -> None:
     k, v, lengths, pages = _gpu_ptrs("ar_cache_append", k, v, lengths, pages)
+    _same_device("ar_cache_append", cache)
     p = _append_params(sequences, queries, format_id(fmt), k or 0, k_stride, k_head_stride, v or 0,
                        v_stride, v_head_stride, lengths or 0, pages or 0, pages_stride, max_pages)
     _check(_lib.ar_cache_append(ctypes.byref(cache), p, _stream(stream)), "ar_cache_append")
@@ -559,13 +582,13 @@ def attention_params(cache: ar_kv_cache, sequences, queries, heads, scale, fmt, 
                      prefix_pages, lengths, pages, pages_stride, max_pages) -> ar_attention_params:
     """One ar_prefix_attention; lse may be None.  The result keeps the tensors,
     the cache's among them; their types and sizes are not looked at."""
+    _same_device("attention_params", cache)
     tensors = q, out, lse, prefix_pages, lengths, pages
     q, out, lse, prefix_pages, lengths, pages = _gpu_ptrs("attention_params", *tensors)
     p = ar_attention_params(cache, sequences, queries, heads, scale, format_id(fmt), q, q_stride,
                             q_head_stride, out, out_stride, out_head_stride, lse, lse_stride,
                             prefix, prefix_pages, lengths, pages, pages_stride, max_pages, 0)
-    p.tensors = tensors + getattr(cache, "tensors", ())
-    return p
+    return _keep(p, tensors + getattr(cache, "tensors", ()))
 
 
 def ar_prefix_attention_work_bytes(params: ar_attention_params) -> int:
@@ -577,6 +600,7 @@ def ar_prefix_attention(params: ar_attention_params, work, stream=None) -> None:
     """work: a device tensor of at least ar_prefix_attention_work_bytes(params)
     bytes, of this call alone while it runs (None where that is 0)."""
     w, = _gpu_ptrs("ar_prefix_attention", work)
+    _same_device("ar_prefix_attention", params)
     nbytes = 0 if work is None else work.numel() * work.element_size()
     _check(_lib.ar_prefix_attention(ctypes.byref(params), w, nbytes, _stream(stream)),
            "ar_prefix_attention")
