@@ -302,6 +302,17 @@ def _same_device(where: str, params) -> None:
                                  "is not the current device")
 
 
+def _work(where: str, work):
+    """Address and bytes of a work buffer: of all that lies between its first
+    and last element, so one with gaps, which are another's, is refused."""
+    if work is None:
+        return None, 0
+    w, = _gpu_ptrs(where, work)
+    if not work.is_contiguous():
+        raise ArError(AR_EINVAL, f"{where}: a work buffer that is not contiguous")
+    return w, work.numel() * work.element_size()
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
         # what torch.cuda.current_stream().cuda_stream gives, without the
@@ -542,10 +553,9 @@ def ar_mx4_linear_adapters(linear: ar_linear_params, adapters: ar_adapter_params
                            stream=None) -> None:
     """work: a device tensor of at least ar_adapter_work_bytes(linear, adapters)
     bytes, of this call alone while it runs (None where that is 0)."""
-    w, = _gpu_ptrs("ar_mx4_linear_adapters", work)
+    w, nbytes = _work("ar_mx4_linear_adapters", work)
     _same_device("ar_mx4_linear_adapters", linear)
     _same_device("ar_mx4_linear_adapters", adapters)
-    nbytes = 0 if work is None else work.numel() * work.element_size()
     _check(_lib.ar_mx4_linear_adapters(ctypes.byref(linear), ctypes.byref(adapters), w, nbytes,
                                        _stream(stream)), "ar_mx4_linear_adapters")
 
@@ -599,9 +609,8 @@ def ar_prefix_attention_work_bytes(params: ar_attention_params) -> int:
 def ar_prefix_attention(params: ar_attention_params, work, stream=None) -> None:
     """work: a device tensor of at least ar_prefix_attention_work_bytes(params)
     bytes, of this call alone while it runs (None where that is 0)."""
-    w, = _gpu_ptrs("ar_prefix_attention", work)
+    w, nbytes = _work("ar_prefix_attention", work)
     _same_device("ar_prefix_attention", params)
-    nbytes = 0 if work is None else work.numel() * work.element_size()
     _check(_lib.ar_prefix_attention(ctypes.byref(params), w, nbytes, _stream(stream)),
            "ar_prefix_attention")
 

@@ -3,7 +3,7 @@ current, whose kernels would read and write that memory (no GPU is touched)."""
 import pytest
 import torch
 
-from collective_synchronization_amd import abi, buffers
+from collective_synchronization_amd import abi
 
 
 class Held:
@@ -95,6 +95,26 @@ def test_reduce_norm_of_another_device(current):
     with pytest.raises(abi.ArError) as e:
         abi.ar_reduce_norm(abi.ar_desc(), Held(1), p, 0, Held(1), stream=0)
     assert e.value.code == abi.AR_EINVAL and "device" in str(e.value)
+
+
+class Buffer(Held):
+    """A work buffer, every other element of its memory or all of them."""
+
+    def __init__(self, step):
+        super().__init__()
+        self.t = torch.empty(4096, dtype=torch.uint8)[::step]
+        self.numel, self.element_size, self.is_contiguous = self.t.numel, self.t.element_size, self.t.is_contiguous
+
+
+def test_a_work_buffer_with_gaps(current):
+    """Its bytes would be written one after the other, over what lies in the gaps."""
+    calls = (lambda w: abi.ar_prefix_attention(_attention(_cache()), w, stream=0),
+             lambda w: abi.ar_mx4_linear_adapters(_linear(), _adapters(), w, stream=0))
+    for call in calls:
+        call(Buffer(1))
+        with pytest.raises(abi.ArError) as e:
+            call(Buffer(2))
+        assert e.value.code == abi.AR_EINVAL and "contiguous" in str(e.value)
 
 
 def test_addresses_have_no_device(current):
