@@ -1144,6 +1144,12 @@ struct AttnPlan {
   int32_t prefix_splits, prefix_chunk, prefix_tiles, own_splits, own_tiles;
 };
 
+static int64_t row_tiles(int64_t rows) { return rows <= kFewRows ? 1 : ceil_div64(rows, kTileRows); }
+static int64_t step_keys(int64_t rows) { return rows <= kFewRows ? 128 : 64; }
+static int64_t most_places(const ar_attention_params* p) {
+  return p->cache.dim <= 64 ? 1024 : (p->cache.dim <= 128 ? 512 : 256);
+}
+
 // Pieces of keys.  A piece costs a step for each 64 keys of a tile of many rows,
 // or for each 128 that the waves of few rows take together; all are made as
 // long as fills the chip's places for workgroups once: four to a CU where heads are of
@@ -1152,15 +1158,13 @@ struct AttnPlan {
 // 128 x 64 heads over 32768, bf16: 192 us with 512 pieces, 204 with 1024; heads of 64
 // 112 and 105; of 256 277 and, with 256 pieces, 254; 16 x 64 heads over 8192 27 with
 // 512, 23 with 256.  Where no sequence's own tokens are split, the prefix has the
-// places that they leave, if that takes a quarter more of its pieces at most: 37 x
-// 2 tokens, prefix 4999, own 777, heads of 96, 27 us with 512 pieces, 32 with 536.
-// (Pieces of split ones vary with the lengths: 8 sequences of up to 32768, 161
-// with 520, 169 with 512.)
-static int64_t row_tiles(int64_t rows) { return rows <= kFewRows ? 1 : ceil_div64(rows, kTileRows); }
-static int64_t step_keys(int64_t rows) { return rows <= kFewRows ? 128 : 64; }
-static int64_t most_places(const ar_attention_params* p) {
-  return p->cache.dim <= 64 ? 1024 : (p->cache.dim <= 128 ? 512 : 256);
-}
+// places that they leave, if its pieces grow by a third at most for it: 37 x 2 tokens,
+// prefix 4999, own 777, heads of 96, 28.4 us so, 33.0 with 536 pieces; own 400 26.9 and
+// 27.8.  (Up to 256 pieces there are places for all: 20 x 2 tokens, own 777, 25.3 with
+// 288 pieces in 512 places, 28.6 with 256.  Pieces of split ones vary with the lengths:
+// 8 sequences of up to 32768, 161 with 520, 169 with 512.)  Own tokens count with all
+// that the table has room for, so a table much wider than the lengths leaves the
+// prefix in fewer and longer pieces than would be best.
 static AttnPlan plan_attention(const ar_attention_params* p) {
   AttnPlan s{};
   const int64_t kv = p->cache.kv_heads, group = p->heads / kv;
@@ -1171,15 +1175,12 @@ static AttnPlan plan_attention(const ar_attention_params* p) {
   const int64_t shared = kv * s.prefix_tiles * ceil_div64(p->prefix, step_keys(rows));
   const int64_t own = p->sequences * kv * s.own_tiles * ceil_div64(capacity, step_keys(own_rows));
   const int64_t places = most_places(p);
-  int64_t steps = ceil_div64(shared + own, places), at_once = places;
-  if (steps < 6) {
-    steps = ceil_div64(shared + own, 256);
-    at_once = 256;
-  }
+  int64_t steps = ceil_div64(shared + own, places);
+  if (steps < 6) steps = ceil_div64(shared + own, 256);
   if (capacity > 0) s.own_splits = (int32_t)ceil_div64(capacity, steps * step_keys(own_rows));
   if (p->prefix > 0) {
     int64_t n = ceil_div64(p->prefix, steps * step_keys(rows));
-    const int64_t room = (at_once - p->sequences * kv * s.own_tiles * s.own_splits) / (kv * s.prefix_tiles);
+    const int64_t room = (places - p->sequences * kv * s.own_tiles * s.own_splits) / (kv * s.prefix_tiles);
     if (s.own_splits <= 1 && room < n && 4 * room >= 3 * n) n = room;
     s.prefix_chunk = (int32_t)(ceil_div64(ceil_div64(p->prefix, n), 64) * 64);
     s.prefix_splits = (int32_t)ceil_div64(p->prefix, s.prefix_chunk);
