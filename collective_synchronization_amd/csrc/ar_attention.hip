@@ -1163,8 +1163,10 @@ static int64_t most_places(const ar_attention_params* p) {
 // 27.8.  (Up to 256 pieces there are places for all: 20 x 2 tokens, own 777, 25.3 with
 // 288 pieces in 512 places, 28.6 with 256.  Pieces of split ones vary with the lengths:
 // 8 sequences of up to 32768, 161 with 520, 169 with 512.)  Own tokens count with all
-// that the table has room for, so a table much wider than the lengths leaves the
-// prefix in fewer and longer pieces than would be best.
+// that the table has room for, which may be far more than there are: the prefix's
+// pieces are therefore at most twice as long as by itself.  16 x 64 heads, prefix 8192,
+// own 500, a table for 512 tokens 26 us, for 32768 27, 98 without that limit; 128 x 64
+// heads, prefix 32768, 8-bit, own 200, a table for 32768 245 and 910.
 static AttnPlan plan_attention(const ar_attention_params* p) {
   AttnPlan s{};
   const int64_t kv = p->cache.kv_heads, group = p->heads / kv;
@@ -1175,11 +1177,15 @@ static AttnPlan plan_attention(const ar_attention_params* p) {
   const int64_t shared = kv * s.prefix_tiles * ceil_div64(p->prefix, step_keys(rows));
   const int64_t own = p->sequences * kv * s.own_tiles * ceil_div64(capacity, step_keys(own_rows));
   const int64_t places = most_places(p);
-  int64_t steps = ceil_div64(shared + own, places);
-  if (steps < 6) steps = ceil_div64(shared + own, 256);
+  auto piece = [&](int64_t all) {
+    const int64_t n = ceil_div64(all, places);
+    return n < 6 ? ceil_div64(all, 256) : n;
+  };
+  const int64_t steps = piece(shared + own);
   if (capacity > 0) s.own_splits = (int32_t)ceil_div64(capacity, steps * step_keys(own_rows));
   if (p->prefix > 0) {
-    int64_t n = ceil_div64(p->prefix, steps * step_keys(rows));
+    const int64_t alone = piece(shared) < 3 ? 6 : 2 * piece(shared);
+    int64_t n = ceil_div64(p->prefix, (steps < alone ? steps : alone) * step_keys(rows));
     const int64_t room = (places - p->sequences * kv * s.own_tiles * s.own_splits) / (kv * s.prefix_tiles);
     if (s.own_splits <= 1 && room < n && 4 * room >= 3 * n) n = room;
     s.prefix_chunk = (int32_t)(ceil_div64(ceil_div64(p->prefix, n), 64) * 64);

@@ -94,3 +94,11 @@ def test_fp16_weights_far_below_the_largest(cache, queries):
         b.vd.copy_(torch.from_numpy(b.v).to(torch.float16))
     b.run()
     assert float(b.out[0, 0, 0]) > 0.0
+
+
+@pytest.mark.parametrize("cache", ["same", "row8"])
+@pytest.mark.parametrize("queries", [1, 9])
+@pytest.mark.parametrize("width", [7, 300, 20000])
+def test_tables_wider_than_the_lengths(width, queries, cache):
+    """A table with room for far more tokens than there are cuts the keys otherwise and changes nothing."""
+    Batch(15, (40, 100, 0, 77), queries, 8, 2, 64, 16, 1500, "bf16", cache, width=width).run()
