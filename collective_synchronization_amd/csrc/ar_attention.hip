@@ -1164,7 +1164,7 @@ static int64_t most_places(const ar_attention_params* p) {
 // 288 pieces in 512 places, 28.6 with 256.  Pieces of split ones vary with the lengths:
 // 8 sequences of up to 32768, 161 with 520, 169 with 512.)  Own tokens count with all
 // that the table has room for, which may be far more than there are: the prefix's
-// pieces are therefore at most twice as long as by itself.  16 x 64 heads, prefix 8192,
+// pieces are therefore at most twice as long as by itself, or 8 steps.  16 x 64 heads, prefix 8192,
 // own 500, a table for 512 tokens 26 us, for 32768 27, 98 without that limit; 128 x 64
 // heads, prefix 32768, 8-bit, own 200, a table for 32768 245 and 910.
 static AttnPlan plan_attention(const ar_attention_params* p) {
@@ -1184,7 +1184,7 @@ static AttnPlan plan_attention(const ar_attention_params* p) {
   const int64_t steps = piece(shared + own);
   if (capacity > 0) s.own_splits = (int32_t)ceil_div64(capacity, steps * step_keys(own_rows));
   if (p->prefix > 0) {
-    const int64_t alone = piece(shared) < 3 ? 6 : 2 * piece(shared);
+    const int64_t alone = piece(shared) < 4 ? 8 : 2 * piece(shared);
     int64_t n = ceil_div64(p->prefix, (steps < alone ? steps : alone) * step_keys(rows));
     const int64_t room = (places - p->sequences * kv * s.own_tiles * s.own_splits) / (kv * s.prefix_tiles);
     if (s.own_splits <= 1 && room < n && 4 * room >= 3 * n) n = room;
