@@ -482,8 +482,10 @@ static int64_t t_row_bytes(const ar_adapter_params* q) { return ceil_div64(q->ra
 constexpr int kTokenBlocks = 1024;
 
 // Outputs of all ranks up to which up to 16 dimensions of 16 tokens' adapters are
-// left to the layer's own waves: 4 x 16 x 8192 18.4 us both ways with an adapter
-// for each token, 14.5 and 17.8 with one for all.
+// left to the layer's own waves, against sums made ready, K 2048, with an adapter for
+// each token (and one for all): 4 x 16 x 4096 12.6 and 15.8 us (12.6 and 15.8),
+// 4 x 16 x 8192 18.6 and 18.8 (14.9 and 18.4), 1 x 16 x 65536 29.7 and 29.5 (23.7 and
+// 27.1), 8 x 16 x 8192 30.4 and 28.7 (23.7 and 27.5).
 constexpr int64_t kLaneOutputs = 1 << 19;
 
 struct TokenPlan {

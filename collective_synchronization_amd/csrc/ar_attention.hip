@@ -91,7 +91,9 @@ __device__ __forceinline__ uint32_t pair16(float lo, float hi) {
 // Two binary32 weights as two bf16 parts each, off by 2^-16 together: the first
 // is cut, not rounded, and the rest, which has 2^-23 of the weight added, is therefore
 // above zero wherever the weight is: times an infinite value both are the same
-// infinity.  SCALED: weights times scales, which may be infinities; these are in the rest.
+// infinity.  SCALED: weights times scales, which may be infinities; these are in the rest
+// (64 x 2 tokens behind 8192, fp16 on an 8-bit cache: 84 us, 77 with rounded parts, which
+// make NaNs of infinities).
 struct Parts16 {
   uint32_t top, rest;
 };
@@ -427,11 +429,12 @@ struct Attn {
   // wave has 32 rows, and tiles of KT keys pass through shared memory, the next
   // one on its way while one is multiplied (8-bit ones in registers, since they
   // are converted), and the pages of the one after that.  Two waves to a SIMD take
-  // turns with matrix cores and vector units.  128 x 64 heads over 32768: bf16 187 us
-  // (0.73 PFLOP/s), 8-bit 219: the matrix cores are busy 42% of the cycles, and the
-  // card runs at 1.5 to 1.9 GHz meanwhile.  With the scores of the next tile formed
-  // beside the weights of this one 222 and 295: registers and shared memory for it
-  // cost more than it hides.
+  // turns with matrix cores and vector units.  128 x 64 heads over 32768: bf16 168 us
+  // (0.82 PFLOP/s), 8-bit 194; the matrix cores are busy 42% and 33% of the cycles.
+  // With the scores of the next tile formed beside the weights of this one 222 and 295,
+  // where this form took 190 and 222: registers and shared memory for it cost more
+  // than it hides.  With LATER, heads of 128 and 8-bit rows 44 to 58 vector registers
+  // are spilled (64 x 2 tokens behind 8192 73 us, 62 in bf16).
   static __device__ void many_rows(const AttnArgs& a, const Piece& p, uint8_t* smem) {
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -1155,8 +1158,8 @@ static int64_t most_places(const ar_attention_params* p) {
 // long as fills the chip's places for workgroups once: four to a CU where heads are of
 // up to 64, two up to 128, else one, by registers and shared memory.  Short pieces
 // are made twice as long: their rows' way through memory to the join counts more.
-// 128 x 64 heads over 32768, bf16: 192 us with 512 pieces, 204 with 1024; heads of 64
-// 112 and 105; of 256 277 and, with 256 pieces, 254; 16 x 64 heads over 8192 27 with
+// 128 x 64 heads over 32768, bf16: 168 us with 512 pieces, 179 with 1024; heads of 64
+// 101 to 105 and 103; of 256 241 and, with 256 pieces, 226; 16 x 64 heads over 8192 27 with
 // 512, 23 with 256.  Where no sequence's own tokens are split, the prefix has the
 // places that they leave, if its pieces grow by a third at most for it: 37 x 2 tokens,
 // prefix 4999, own 777, heads of 96, 28.4 us so, 33.0 with 536 pieces; own 400 26.9 and
@@ -1164,9 +1167,11 @@ static int64_t most_places(const ar_attention_params* p) {
 // 288 pieces in 512 places, 28.6 with 256.  Pieces of split ones vary with the lengths:
 // 8 sequences of up to 32768, 161 with 520, 169 with 512.)  Own tokens count with all
 // that the table has room for, which may be far more than there are: the prefix's
-// pieces are therefore at most twice as long as by itself, or 8 steps.  16 x 64 heads, prefix 8192,
-// own 500, a table for 512 tokens 26 us, for 32768 27, 98 without that limit; 128 x 64
-// heads, prefix 32768, 8-bit, own 200, a table for 32768 245 and 910.
+// pieces are therefore at most twice as long as by itself, or 8 steps.  16 x 64 heads,
+// prefix 8192, own 500, a table for 512 tokens 26 us, for 32768 27, 98 without that
+// limit; 128 x 64 heads, prefix 32768, 8-bit, own 200, a table for 32768 245 and 910.
+// Own pieces are as many for every sequence: one of 32768 tokens among 127 of 200 is
+// 335 us, 31 by itself.
 static AttnPlan plan_attention(const ar_attention_params* p) {
   AttnPlan s{};
   const int64_t kv = p->cache.kv_heads, group = p->heads / kv;
