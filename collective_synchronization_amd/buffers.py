@@ -104,8 +104,9 @@ class PagedCache:
         if fmt is None or v.dtype != k.dtype or k.shape != v.shape or sequences == 0 or \
                 k.shape[0] % sequences or k.shape[1:] != (self.kv_heads, self.dim) or \
                 lengths.dtype != torch.int32 or pages.dtype != torch.int32 or \
-                lengths.numel() != sequences or \
-                k.stride(2) != 1 or v.stride(2) != 1 or pages.stride(1) != 1 or lengths.stride(0) != 1:
+                lengths.numel() != sequences or pages.dim() != 2 or \
+                k.stride(2) != 1 or v.stride(2) != 1 or not lengths.is_contiguous() or \
+                (pages.shape[1] > 1 and pages.stride(1) != 1):
             raise ValueError("append: types or shapes that do not fit the cache")
         abi.ar_cache_append(self.params, sequences, k.shape[0] // sequences, fmt, k, k.stride(0),
                             k.stride(1), v, v.stride(0), v.stride(1), lengths, pages,
